@@ -40,8 +40,10 @@ EXPORTS = ("rkv_create", "rkv_destroy", "rkv_score", "rkv_select", "rkv_compact"
            "rkv_compress", "rkv_compress_host", "rkv_evict_in_place", "rkv_fill_slots",
            "rkv_select_ex", "rkv_refree_budget", "rkv_check_status", "rkv_launch_count", "rkv_set_timing",
            "rkv_read_timing", "rkv_score_noalloc", "rkv_noalloc_check_status", "rkv_inject_fault",
-           "rkv_debug_intermediates", "rkv_status_string", "rkv_version")
-KERNELS = ("score", "plan", "gemm", "select", "compact", "evict", "fill", "refree", "finish")
+           "rkv_debug_intermediates", "rkv_status_string", "rkv_version", "rkv_attend",
+           "rkv_attend_shared", "rkv_evict_accumulated", "rkv_fill_slots_ex")
+KERNELS = ("score", "plan", "gemm", "select", "compact", "evict", "fill", "refree", "finish",
+           "attend", "shared", "join", "weight", "drop")
 
 
 class RkvConfig(ctypes.Structure):
@@ -60,6 +62,23 @@ class RkvBatch(ctypes.Structure):
     _fields_ = [("num_units", ctypes.c_int), ("tok_off", ctypes.c_void_p),
                 ("tok_off_host", ctypes.c_void_p), ("K", ctypes.c_void_p),
                 ("V", ctypes.c_void_p), ("Q", ctypes.c_void_p)]
+
+
+class RkvAttention(ctypes.Structure):
+    _fields_ = [("num_queries", ctypes.c_int), ("local", ctypes.c_int), ("sinks", ctypes.c_int),
+                ("Q", ctypes.c_void_p), ("keep", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("q_pos", ctypes.c_void_p), ("acc_in", ctypes.c_void_p),
+                ("acc_out", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p)]
+
+
+class RkvPrefix(ctypes.Structure):
+    _fields_ = [("num_prefixes", ctypes.c_int), ("num_units", ctypes.c_int),
+                ("off", ctypes.c_void_p), ("off_host", ctypes.c_void_p),
+                ("K", ctypes.c_void_p), ("V", ctypes.c_void_p),
+                ("unit_prefix", ctypes.c_void_p), ("unit_prefix_host", ctypes.c_void_p),
+                ("mem_off", ctypes.c_void_p), ("mem_off_host", ctypes.c_void_p),
+                ("mem", ctypes.c_void_p), ("mem_host", ctypes.c_void_p)]
 
 
 class RkvError(RuntimeError):
@@ -97,6 +116,13 @@ def lib():
     L.rkv_select_ex.argtypes = [vp, ctypes.POINTER(RkvBatch), vp, vp, f32, i32, vp, i32, vp, vp,
                                 vp]
     L.rkv_refree_budget.argtypes = [vp, ctypes.POINTER(RkvBatch), f32, i32, i32, vp, vp, vp, vp]
+    L.rkv_attend.argtypes = [vp, ctypes.POINTER(RkvBatch), ctypes.POINTER(RkvAttention), vp]
+    L.rkv_attend_shared.argtypes = [vp, ctypes.POINTER(RkvBatch), ctypes.POINTER(RkvPrefix),
+                                    ctypes.POINTER(RkvAttention), vp]
+    L.rkv_evict_accumulated.argtypes = [vp, ctypes.POINTER(RkvBatch), vp, vp, vp, i32, vp, i32,
+                                        vp, vp, vp, vp, vp, vp, vp]
+    L.rkv_fill_slots_ex.argtypes = [vp, ctypes.POINTER(RkvBatch), vp, vp, vp, vp, vp, vp, vp, vp,
+                                    vp, vp, vp, vp, vp, vp, vp]
     L.rkv_check_status.argtypes = [vp, vp]
     L.rkv_launch_count.argtypes = [vp]
     L.rkv_launch_count.restype = i64
@@ -115,7 +141,8 @@ def lib():
                  "rkv_select_ex", "rkv_refree_budget", "rkv_check_status", "rkv_set_timing",
                  "rkv_read_timing",
                  "rkv_score_noalloc", "rkv_noalloc_check_status", "rkv_inject_fault",
-                 "rkv_debug_intermediates", "rkv_version"):
+                 "rkv_debug_intermediates", "rkv_version", "rkv_attend", "rkv_attend_shared",
+                 "rkv_evict_accumulated", "rkv_fill_slots_ex"):
         getattr(L, name).restype = i32
     _lib = L
     return L
@@ -138,6 +165,27 @@ def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _tensor(t, name: str, dtype, shape, device, optional: bool = True):
+    """Pointer of a contiguous tensor of this type, shape and device (or None)."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is required")
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _stream_on(device, stream) -> int:
+    """The stream's handle; by default the current stream of ``device``."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    return stream.cuda_stream
 
 
 def score_noalloc(group: int, window: int, batch: "Batch", a, r, m=None, stream=None):
@@ -163,9 +211,10 @@ class Batch:
     """Views of one batch of unit caches (tensors stay owned by the caller).
 
     K, V: [T, d] bf16 CUDA tensors; Q: [U, G, w, d] bf16; tok_off: host int64
-    offsets [U+1] (a device copy is made once, here)."""
+    offsets [U+1] (a device copy is made once, here).  A batch of offsets alone
+    (K, V, Q None; for evict_accumulated) names its ``device``."""
 
-    def __init__(self, K, V, Q, tok_off):
+    def __init__(self, K, V, Q, tok_off, device=None):
         for name, t in (("K", K), ("V", V), ("Q", Q)):
             if t is not None:
                 if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous():
@@ -173,7 +222,9 @@ class Batch:
         self.K, self.V, self.Q = K, V, Q
         off = np.ascontiguousarray(np.asarray(tok_off, dtype=np.int64))
         self.tok_off_host = off
-        dev = (K if K is not None else Q).device
+        dev = next((t.device for t in (K, Q) if t is not None), device)
+        if dev is None:
+            raise ValueError("a batch without K and Q needs a device")
         self.tok_off = torch.from_numpy(off).to(dev)
         self.c = RkvBatch(len(off) - 1, self.tok_off.data_ptr(),
                           off.ctypes.data, _ptr(K), _ptr(V), _ptr(Q))
@@ -185,6 +236,49 @@ class Batch:
     @property
     def num_tokens(self):
         return int(self.tok_off_host[-1])
+
+
+class Offsets:
+    """Row offsets [U+1] of per-unit runs of new tokens, with their device copy."""
+
+    def __init__(self, values, device):
+        self.host = np.ascontiguousarray(np.asarray(values, dtype=np.int64))
+        if self.host.ndim != 1 or len(self.host) < 1:
+            raise ValueError("offsets are U + 1 values")
+        self.dev = torch.from_numpy(self.host).to(device)
+
+
+class Prefix:
+    """Prefixes that several units of a batch share (``rkv_prefix``).
+
+    K, V: [rows, 128] bf16 CUDA tensors; off: P + 1 row offsets; unit_prefix: the
+    prefix of each unit of the batch, -1 for none."""
+
+    def __init__(self, K, V, off, unit_prefix):
+        off = np.ascontiguousarray(np.asarray(off, dtype=np.int64))
+        up = np.ascontiguousarray(np.asarray(unit_prefix, dtype=np.int32))
+        P = len(off) - 1
+        if off.ndim != 1 or P < 0 or off[0] != 0 or np.any(np.diff(off) < 0):
+            raise ValueError("off must start at 0 and not decrease")
+        if up.ndim != 1 or np.any(up < -1) or np.any(up >= P):
+            raise ValueError("unit_prefix must hold prefix indices, or -1")
+        for name, t in (("K", K), ("V", V)):
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            _tensor(t, name, torch.bfloat16, (int(off[-1]), 128), K.device)
+        order = np.argsort(up, kind="stable").astype(np.int32)
+        mem = np.ascontiguousarray(order[np.count_nonzero(up < 0):])
+        mem_off = np.zeros(P + 1, dtype=np.int32)
+        np.cumsum(np.bincount(up[up >= 0], minlength=P), out=mem_off[1:])
+        self.K, self.V = K, V
+        self._host = (off, up, mem_off, mem)
+        self._dev = tuple(torch.from_numpy(x).to(K.device) for x in self._host)
+        h, d = self._host, self._dev
+        # empty arrays still need an address (nothing is read there)
+        ptr = lambda t, x: t.data_ptr() or x.ctypes.data
+        self.c = RkvPrefix(P, len(up), d[0].data_ptr(), h[0].ctypes.data, K.data_ptr(),
+                           V.data_ptr(), ptr(d[1], h[1]), h[1].ctypes.data, d[2].data_ptr(),
+                           h[2].ctypes.data, ptr(d[3], h[3]), h[3].ctypes.data)
 
 
 class Engine:
@@ -213,6 +307,7 @@ class Engine:
         h = ctypes.c_void_p()
         _check(lib().rkv_create(ctypes.byref(self.cfg), ctypes.byref(h)), "rkv_create")
         self.h = h
+        self.device = torch.device("cuda", torch.cuda.current_device())
 
     def close(self):
         if getattr(self, "h", None):
@@ -307,6 +402,97 @@ class Engine:
         _check(lib().rkv_refree_budget(self.h, ctypes.byref(batch.c), float(T), int(sinks),
                                        int(max_budget), _ptr(p_last), _ptr(budgets),
                                        _ptr(keep_count), _stream(stream)), "rkv_refree_budget")
+
+    def attend(self, batch: Batch, Q, out, lse=None, *, keep=None, pos=None, q_pos=None,
+               local: int = 0, sinks: int = 0, acc=None, acc_out=None, stream=None):
+        """Decode attention over the live rows of the units (``rkv_attend``).
+
+        Q, out: bf16 [U, G, n_q, 128], the n_q newest queries (n_q <= window); lse:
+        fp32 [U, G, n_q]; keep: uint8 [T]; pos: int32 [T] with q_pos: int32 [U];
+        local, sinks: sliding window and sinks; acc_out: fp32 [T], acc plus this
+        call's weights (may be acc itself)."""
+        args = self._attention(batch, Q, out, lse, keep, pos, q_pos, local, sinks, acc, acc_out)
+        _check(lib().rkv_attend(self.h, ctypes.byref(batch.c), ctypes.byref(args),
+                                _stream_on(self.device, stream)), "rkv_attend")
+
+    def attend_shared(self, batch: Batch, prefix: Prefix, Q, out, lse=None, *, keep=None,
+                      pos=None, q_pos=None, local: int = 0, sinks: int = 0, acc=None,
+                      acc_out=None, stream=None):
+        """``attend`` where the units' rows follow a prefix that several of them
+        share and that is read once for all (``rkv_attend_shared``)."""
+        if prefix.K.device != self.device:
+            raise ValueError(f"the prefix is on {prefix.K.device}, the engine on {self.device}")
+        args = self._attention(batch, Q, out, lse, keep, pos, q_pos, local, sinks, acc, acc_out)
+        _check(lib().rkv_attend_shared(self.h, ctypes.byref(batch.c), ctypes.byref(prefix.c),
+                                       ctypes.byref(args), _stream_on(self.device, stream)),
+               "rkv_attend_shared")
+
+    def _attention(self, batch, Q, out, lse, keep, pos, q_pos, local, sinks, acc, acc_out):
+        U, T, dev = batch.num_units, batch.num_tokens, self.device
+        if Q.dim() != 4:
+            raise ValueError("Q must be [U, G, n_q, 128]")
+        nq = Q.shape[2]
+        shape = (U, self.group, nq, 128)
+        bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+        for name, t in (("K", batch.K), ("V", batch.V)):
+            _tensor(t, name, bf, (T, 128), dev, optional=False)
+        return RkvAttention(
+            nq, int(local), int(sinks), _tensor(Q, "Q", bf, shape, dev),
+            _tensor(keep, "keep", torch.uint8, (T,), dev), _tensor(pos, "pos", i32, (T,), dev),
+            _tensor(q_pos, "q_pos", i32, (U,), dev), _tensor(acc, "acc", f32, (T,), dev),
+            _tensor(acc_out, "acc_out", f32, (T,), dev),
+            _tensor(out, "out", bf, shape, dev, optional=False),
+            _tensor(lse, "lse", f32, shape[:3], dev))
+
+    def evict_accumulated(self, batch: Batch, acc, budget: int, keep, free_slots, n_free, *,
+                          live=None, pos=None, budgets=None, sinks: int = 0, acc_out=None,
+                          idx=None, n_kept=None, stream=None):
+        """Keep the sinks, the w newest and the ``budget`` heaviest other live rows
+        of every unit (``rkv_evict_accumulated``).  live: uint8 [T] before the call
+        (may be keep); idx int32 [U, budget + sinks + w] with n_kept int32 [U]."""
+        U, T, dev = batch.num_units, batch.num_tokens, self.device
+        u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+        W = int(budget) + int(sinks) + self.window
+        _check(lib().rkv_evict_accumulated(
+            self.h, ctypes.byref(batch.c), _tensor(acc, "acc", f32, (T,), dev, optional=False),
+            _tensor(live, "live", u8, (T,), dev), _tensor(pos, "pos", i32, (T,), dev),
+            int(budget), _tensor(budgets, "budgets", i32, (U,), dev), int(sinks),
+            _tensor(keep, "keep", u8, (T,), dev, optional=False),
+            _tensor(free_slots, "free_slots", i32, (T,), dev, optional=False),
+            _tensor(n_free, "n_free", i32, (U,), dev, optional=False),
+            _tensor(acc_out, "acc_out", f32, (T,), dev), _tensor(idx, "idx", i32, (U, W), dev),
+            _tensor(n_kept, "n_kept", i32, (U,), dev), _stream_on(dev, stream)),
+            "rkv_evict_accumulated")
+
+    def fill_slots_ex(self, batch: Batch, new_off: Offsets, K_new, V_new, keep, free_slots,
+                      n_free, *, pos=None, pos_new=None, acc=None, free_out=None,
+                      n_free_out=None, stream=None):
+        """``fill_slots`` that also writes the filled rows' positions (pos from
+        pos_new) and zeroes their accumulated weight (acc), and can leave the
+        remaining list in other buffers (``rkv_fill_slots_ex``)."""
+        U, T, dev = batch.num_units, batch.num_tokens, self.device
+        n = int(new_off.host[-1])
+        bf, u8, f32, i32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
+        if len(new_off.host) != U + 1 or new_off.dev.device != dev:
+            raise ValueError(f"new_off must hold {U + 1} offsets on {dev}")
+        if (free_out is None) != (n_free_out is None):
+            raise ValueError("free_out and n_free_out go together")
+        if (pos is None) != (pos_new is None):
+            raise ValueError("pos and pos_new go together")
+        free = _tensor(free_slots, "free_slots", i32, (T,), dev, optional=False)
+        count = _tensor(n_free, "n_free", i32, (U,), dev, optional=False)
+        _check(lib().rkv_fill_slots_ex(
+            self.h, ctypes.byref(batch.c),
+            _tensor(batch.K, "K", bf, (T, 128), dev, optional=False),
+            _tensor(batch.V, "V", bf, (T, 128), dev, optional=False), new_off.dev.data_ptr(),
+            new_off.host.ctypes.data, _tensor(K_new, "K_new", bf, (n, 128), dev, optional=False),
+            _tensor(V_new, "V_new", bf, (n, 128), dev, optional=False),
+            _tensor(pos_new, "pos_new", i32, (n,), dev),
+            _tensor(keep, "keep", u8, (T,), dev, optional=False), free, count,
+            _tensor(pos, "pos", i32, (T,), dev), _tensor(acc, "acc", f32, (T,), dev),
+            free if free_out is None else _tensor(free_out, "free_out", i32, (T,), dev),
+            count if n_free_out is None else _tensor(n_free_out, "n_free_out", i32, (U,), dev),
+            _stream_on(dev, stream)), "rkv_fill_slots_ex")
 
     def check_status(self, stream=None):
         _check(lib().rkv_check_status(self.h, _stream(stream)), "device status")

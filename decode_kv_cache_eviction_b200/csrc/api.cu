@@ -20,14 +20,6 @@ size_t round_up(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 constexpr int kSmemCap = 227 * 1024;
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int cuda_fail(cudaError_t e) {
-  (void)e;
-  cudaGetLastError();
-  return RKV_ERR_CUDA;
-}
-
 int make_map(rkv_engine* e, CUtensorMap* m, const void* ptr, uint64_t rows, uint32_t box_rows) {
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(kHeadDim) * 2};
@@ -62,18 +54,6 @@ int check_batch(const rkv_engine* e, const rkv_batch* b, int64_t* T, int* nmax, 
   *nmax = nm;
   *cmax = nm - e->cfg.window;
   return RKV_OK;
-}
-
-// Record the start event of a launch of `kernel` (when timing is on).
-void t_begin(rkv_engine* e, int kernel, cudaStream_t st) {
-  if (!e->timing || e->nev >= rkv_engine::kMaxEv) return;
-  e->ev_kernel[e->nev] = kernel;
-  cudaEventRecord(e->ev[e->nev][0], st);
-}
-void t_end(rkv_engine* e, cudaStream_t st) {
-  if (!e->timing || e->nev >= rkv_engine::kMaxEv) return;
-  cudaEventRecord(e->ev[e->nev][1], st);
-  ++e->nev;
 }
 
 // Fault injected for the next engine creation (rkv_inject_fault(NULL, ...)).
@@ -202,7 +182,8 @@ int rkv_create(const rkv_config* cfg, rkv_engine** out) {
   if (cfg->max_unit_tokens > 0) e->max_n = static_cast<int>(cfg->max_unit_tokens);
   e->max_chunks = score_max_chunks(cfg->max_tokens, cfg->max_units, e->score_ctas, e->rp);
 
-  if (select_configure() != cudaSuccess || inplace_configure() != cudaSuccess) {
+  if (select_configure() != cudaSuccess || inplace_configure() != cudaSuccess ||
+      attend_configure() != cudaSuccess || drop_configure() != cudaSuccess) {
     delete e;
     return cuda_fail(cudaErrorUnknown);
   }
@@ -309,6 +290,8 @@ int rkv_destroy(rkv_engine* e) {
       for (int k = 0; k < 2; ++k) cudaEventDestroy(e->ev[i][k]);
   rkv_host_pipeline_free(e);
   cudaFree(e->rf_z);
+  cudaFree(e->at_part);
+  cudaFree(e->at_shared);
   cudaFree(e->status);
   cudaFree(e->chunk_off);
   cudaFree(e->chunk_unit);
@@ -611,9 +594,10 @@ int rkv_fill_slots(rkv_engine* e, const rkv_batch* b, void* K, void* V, const in
     return RKV_ERR_INVALID_ARG;
   if (U == 0 || Tn == 0) return RKV_OK;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const FillExtra x = {nullptr, nullptr, nullptr, free_slots, n_free};
   t_begin(e, RKV_KERNEL_FILL, st);
   cudaError_t err = launch_fill_slots(b->tok_off, U, new_off, K_new, V_new, K, V, keep,
-                                      free_slots, n_free, e->status, e->nsm, st);
+                                      free_slots, n_free, x, e->status, e->nsm, st);
   t_end(e, st);
   if (err != cudaSuccess) return cuda_fail(err);
   ++e->launches;

@@ -1,0 +1,694 @@
+// Decode attention over a live cache: for every unit, G heads x n_q queries
+// against the unit's visible rows (live, not later than the query, inside the
+// sliding window or a sink),
+//   z = q . k / sqrt(d),  out = sum_i softmax(z)_i v_i,  lse = log sum_i e^z_i,
+// and optionally the weight of every row, acc_out_i = acc_i + sum_{g,t} p_i.
+//
+// One pass over K and V with a running maximum and sum.  A unit's rows are cut
+// into chunks, one CTA each, and the chunks' (maximum, sum, weighted V) are
+// joined in chunk order (join_kernel), so results do not depend on timing.
+//
+// Bound: HBM.  A row is 512 bytes, and with R = G n_q query rows costs 512 R
+// flops; at R <= 32 that is below what mma.sync sustains at full bandwidth, so
+// the products run on m16n8k16 steps with the 16 TOKENS as the M side: the few
+// query rows are the N side (8 per step), nothing is padded to 16 or 128 rows,
+// and a K or V fragment is read once for all query rows.
+//
+// A warp works alone: it scans its 32-row groups (keep byte, position), appends
+// the visible rows to a short list, and copies 16 listed rows of K and V per
+// stage into its own shared-memory ring with cp.async.  Rows that no query
+// sees are never read, and missing rows of the last stage are zero-filled.
+// Only __syncwarp and cp.async.wait_group order the ring.
+#include <cuda_bf16.h>
+#include <limits.h>
+
+#include "ptx.cuh"
+#include "rkv_internal.cuh"
+
+namespace rkv {
+namespace {
+
+constexpr int kAtWarps = 4;
+constexpr int kAtThreads = 32 * kAtWarps;
+constexpr int kAtStages = 3;
+constexpr int kAtTok = 16;                     // rows per stage
+constexpr int kList = 64;                      // visible-row list (ring) of a warp
+constexpr int kRowBytes = 256;
+constexpr int kOStride = 132;                  // floats per output row in shared memory
+
+enum AtMode { kOwn = 0, kPrefix = 1, kWeights = 2 };
+
+template <int kMode>
+__host__ __device__ constexpr int at_stage_bytes() {
+  return kAtTok * kRowBytes * (kMode == kWeights ? 1 : 2);
+}
+
+struct AtWarpShared {
+  int slot[kList];
+  int pos[kList];
+  int mslot[kAtStages][kAtTok];   // rows of each stage
+  int mpos[kAtStages][kAtTok];
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
+  const int bytes = on ? 16 : 0;   // 0: the 16 bytes are zero-filled, src is not read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&a)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&a)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// D (16 x 8, fp32) += A (16 x 16, bf16, row-major) . B (16 x 8, bf16), one warp.
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ bool finite(float x) {
+  return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u;
+}
+__device__ __forceinline__ int clamp32(int64_t x) {
+  return x > INT_MAX ? INT_MAX : x < INT_MIN ? INT_MIN : static_cast<int>(x);
+}
+
+// A unit's prefix length (0 without one) and the position of its newest query.
+__device__ __forceinline__ int prefix_len(const AttendParams& p, int u) {
+  if (!p.unit_prefix) return 0;
+  const int x = __ldg(&p.unit_prefix[u]);
+  return x < 0 ? 0 : static_cast<int>(__ldg(&p.pre_off[x + 1]) - __ldg(&p.pre_off[x]));
+}
+__device__ __forceinline__ int64_t newest_query(const AttendParams& p, int u) {
+  if (p.q_pos) return __ldg(&p.q_pos[u]);
+  return prefix_len(p, u) + (__ldg(&p.tok_off[u + 1]) - __ldg(&p.tok_off[u])) - 1;
+}
+__device__ __forceinline__ bool sees(int pos, int qp, int lo, int sinks) {
+  return pos <= qp && (pos > lo || pos < sinks);
+}
+
+// The 32-row groups that can hold visible rows when row i sits at position
+// first + i: the sinks' groups [0, gs), then [start, start + nv - gs).
+struct Span {
+  int gs, start, nv;
+};
+__device__ __forceinline__ Span visible_span(int n, int first, int64_t qmin, int64_t qmax,
+                                             int local, int sinks) {
+  Span s = {0, 0, 0};
+  const int64_t hi = min(static_cast<int64_t>(n), qmax - first + 1);   // rows past hi are later
+  if (hi <= 0) return s;
+  const int gh = static_cast<int>((hi + 31) >> 5);
+  if (local > 0) {
+    const int64_t ns = min(hi, max(static_cast<int64_t>(sinks) - first, static_cast<int64_t>(0)));
+    const int64_t lo = max(static_cast<int64_t>(0), qmin - local + 1 - first);
+    s.gs = static_cast<int>((ns + 31) >> 5);
+    s.start = max(s.gs, static_cast<int>(min(lo, hi) >> 5));
+  }
+  s.nv = s.gs + max(0, gh - s.start);
+  return s;
+}
+
+// Writes four dimensions of a finished row: out = o / L (0 for a row that saw
+// nothing), and from the row's first lane its log-sum-exp.  log2(L) + M is the
+// sum's logarithm to base 2; a row without weight gets +inf in lse2, so that the
+// weights pass gives it p = 0.
+__device__ __forceinline__ void attend_store(const AttendParams& p, int64_t row, int d4, float M,
+                                             float L, float4 o) {
+  const bool none = L == 0.f;
+  const float f = none ? 0.f : 1.f / L;
+  if (none) o = make_float4(0.f, 0.f, 0.f, 0.f);
+  p.out[row * 32 + d4] = make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
+  if (d4 == 0) {
+    const float s = M + log2f(L);
+    if (p.lse) p.lse[row] = none ? -INFINITY : s * 0.6931471805599453f;
+    if (p.lse2) p.lse2[row] = none ? INFINITY : s;
+  }
+}
+
+// NB: query rows / 8 of this launch (1, 2 or 4).
+template <int NB, int kMode>
+__global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParams p) {
+  extern __shared__ __align__(128) uint8_t at_smem[];
+  __shared__ AtWarpShared wsh[kAtWarps];
+  __shared__ int s_qp[32];
+  __shared__ float s_ml[kAtWarps][2][32];
+  const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
+  const int g = lane >> 2, q = lane & 3;
+  AtWarpShared& ws = wsh[wp];
+
+  // what this CTA works on: rows [row0, row0 + nrow) of queries against groups
+  // of the sequence of N rows at `base`
+  const int item = blockIdx.x / p.maxch, chunk = blockIdx.x - item * p.maxch;
+  const int row0 = kMode == kWeights ? 0 : static_cast<int>(blockIdx.y) * 32;
+  int total = p.R;   // query rows of the item
+  int64_t base, end;
+  int mo = 0;
+  if (kMode == kPrefix) {
+    base = __ldg(&p.pre_off[item]);
+    end = __ldg(&p.pre_off[item + 1]);
+    mo = __ldg(&p.mem_off[item]);
+    total = (__ldg(&p.mem_off[item + 1]) - mo) * p.R;
+    if (row0 >= total) return;
+  } else {
+    base = __ldg(&p.tok_off[item]);
+    end = __ldg(&p.tok_off[item + 1]);
+  }
+  const int N = static_cast<int>(end - base);
+  const int nrow = min(32, total - row0);
+  // query row r of this CTA: its unit and its row of Q
+  auto row_of = [&](int r) -> int64_t {
+    if (kMode != kPrefix) return static_cast<int64_t>(item) * p.R + row0 + r;
+    const int m = (row0 + r) / p.R;
+    return static_cast<int64_t>(__ldg(&p.mem[mo + m])) * p.R + (row0 + r - m * p.R);
+  };
+  int first = 0;
+  int64_t qmin, qmax;
+  if (kMode == kPrefix) {
+    if (tid < 32) {
+      int v = INT_MIN;
+      if (tid < nrow) {
+        const int64_t rr = row_of(tid);
+        const int u = static_cast<int>(rr / p.R);
+        const int t = static_cast<int>(rr - static_cast<int64_t>(u) * p.R) % p.nq;
+        v = clamp32(newest_query(p, u) - (p.nq - 1) + t);
+      }
+      s_qp[tid] = v;
+    }
+    __syncthreads();
+    int lo = s_qp[0], hi = s_qp[0];
+    for (int r = 1; r < nrow; ++r) {
+      lo = min(lo, s_qp[r]);
+      hi = max(hi, s_qp[r]);
+    }
+    qmin = lo;
+    qmax = hi;
+  } else {
+    first = prefix_len(p, item);
+    qmax = newest_query(p, item);
+    qmin = qmax - (p.nq - 1);
+    if (tid < 32)
+      s_qp[tid] = tid < nrow ? clamp32(qmin + (row0 + tid) % p.nq) : INT_MIN;
+    __syncthreads();
+  }
+  const int qmax32 = clamp32(qmax);
+  const int lo_any = p.local > 0 ? clamp32(qmin - p.local) : INT_MIN;
+  Span sp;
+  if (kMode == kWeights || p.pos) {   // every row: all are written, or any may hold any position
+    sp.gs = sp.start = 0;
+    sp.nv = (N + 31) >> 5;
+  } else {
+    sp = visible_span(N, first, qmin, qmax, p.local, p.sinks);
+  }
+  const int v_end = min(sp.nv, (chunk + 1) * p.gpc);
+  const uint8_t* keep = kMode == kPrefix ? nullptr : p.keep;
+  const int32_t* pos = kMode == kPrefix ? nullptr : p.pos;
+  const uint4* Kg = kMode == kPrefix ? p.PK : p.K;
+  const uint4* Vg = kMode == kPrefix ? p.PV : p.V;
+
+  // query rows as B fragments: row 8 nb + g, dimensions 16 ks + 2q + {0, 1} and + 8
+  uint32_t bq[NB][8][2];
+  int qp[NB][2], qlo[NB][2];    // limits of this lane's rows 8 nb + 2q + e
+  float lse2[NB][2];            // weights pass: log2 of the rows' sums
+  auto load_rows = [&](int r0) {   // rows r0 .. of this CTA (the weights pass moves on in r0)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int r = r0 + 8 * nb + g;
+      const bool on = kMode == kWeights ? r < p.R : r < nrow;
+      const uint32_t* src = p.Q + (on ? row_of(r) : 0) * 64;
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        bq[nb][ks][0] = on ? __ldg(&src[8 * ks + q]) : 0u;
+        bq[nb][ks][1] = on ? __ldg(&src[8 * ks + q + 4]) : 0u;
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int x = r0 + 8 * nb + 2 * q + e;
+        if (kMode == kWeights) {
+          const bool in = x < p.R;
+          qp[nb][e] = in ? clamp32(qmin + x % p.nq) : INT_MIN;
+          lse2[nb][e] = in ? __ldg(&p.lse2[static_cast<int64_t>(item) * p.R + x]) : 0.f;
+        } else {
+          qp[nb][e] = s_qp[x];
+        }
+        qlo[nb][e] = p.local > 0
+                         ? clamp32(static_cast<int64_t>(qp[nb][e]) - p.local) : INT_MIN;
+      }
+    }
+  };
+  load_rows(0);
+
+  constexpr int kStage = at_stage_bytes<kMode>();
+  uint8_t* ring = at_smem + wp * (kAtStages * kStage);
+  const uint32_t ring_a = smem_u32(ring);
+  // ldmatrix lane offsets: K rows as A (tokens x d), V rows transposed (d x tokens)
+  const int kt = (lane & 7) + ((lane >> 3) & 1) * 8, kc = lane >> 4;
+  const int vt = (lane & 7) + ((lane >> 4) & 1) * 8, vc = (lane >> 3) & 1;
+
+  float O[8][NB][4];
+  float m[NB][2], l[NB][2];
+  // A result that is not finite can come from a value in a row that another
+  // query of the unit may not see (0 x inf in the product), or from the split
+  // of p into two parts.  The chunk is then done again with such V rows taken
+  // out of the product and added one by one to the query rows that see them.
+  for (int careful = 0; careful < 2; ++careful) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int mb = 0; mb < 8; ++mb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) O[mb][nb][e] = 0.f;
+      m[nb][0] = m[nb][1] = -INFINITY;
+      l[nb][0] = l[nb][1] = 0.f;
+    }
+    int v = chunk * p.gpc + wp;   // next group of this warp
+    int head = 0, cnt = 0;        // list: first entry, entries
+    // rows of group v (virtual order: sinks' groups, then the window's)
+    auto scan = [&]() {
+      const int grp = v < sp.gs ? v : sp.start + (v - sp.gs);
+      const int slot = 32 * grp + lane;
+      bool on = slot < N;
+      int ps = first + slot;
+      if (on && keep) on = __ldg(&keep[base + slot]) != 0;
+      if (pos && slot < N) ps = __ldg(&pos[base + slot]);
+      if (kMode == kPrefix && p.local > 0) {
+        bool any = false;
+        for (int r = 0; r < nrow; ++r) {
+          const int x = s_qp[r];
+          any |= sees(ps, x, clamp32(static_cast<int64_t>(x) - p.local), p.sinks);
+        }
+        on = on && any;
+      } else {
+        on = on && sees(ps, qmax32, lo_any, p.sinks);
+      }
+      if (kMode == kWeights && !on && slot < N)
+        p.acc_out[base + slot] = p.acc_in ? p.acc_in[base + slot] : 0.f;
+      const uint32_t mask = __ballot_sync(0xffffffffu, on);
+      if (on) {
+        const int at = (head + cnt + __popc(mask & ((1u << lane) - 1u))) & (kList - 1);
+        ws.slot[at] = slot;
+        ws.pos[at] = ps;
+      }
+      cnt += __popc(mask);
+      v += kAtWarps;
+    };
+    int issued = 0, done = 0, last = kAtTok;   // stages; rows of the last stage
+    auto produce = [&]() {
+      while (cnt < kAtTok && v < v_end) scan();
+      __syncwarp();
+      if (cnt > 0) {
+        const int n = min(cnt, kAtTok);
+        const int s = issued % kAtStages;
+        const uint32_t dst = ring_a + s * kStage;
+        const int c = lane & 15;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 2 * i + (lane >> 4);
+          const bool on = r < n;
+          const int64_t row = base + (on ? ws.slot[(head + r) & (kList - 1)] : 0);
+          const uint32_t d = dst + r * kRowBytes + ((c ^ (r & 7)) << 4);
+          cp16(d, Kg + row * 16 + c, on);
+          if (kMode != kWeights) cp16(d + kAtTok * kRowBytes, Vg + row * 16 + c, on);
+        }
+        if (lane < kAtTok) {
+          ws.mslot[s][lane] = ws.slot[(head + lane) & (kList - 1)];
+          ws.mpos[s][lane] = ws.pos[(head + lane) & (kList - 1)];
+        }
+        head = (head + n) & (kList - 1);
+        cnt -= n;
+        ++issued;
+        last = n;
+      }
+      cp_commit();
+      __syncwarp();
+    };
+    for (int s = 0; s < kAtStages - 1; ++s) produce();
+    for (;;) {
+      produce();
+      cp_wait<kAtStages - 1>();
+      __syncwarp();
+      if (done == issued) break;
+      const int s = done % kAtStages;
+      ++done;
+      const int n = done == issued ? last : kAtTok;
+      const uint32_t ka = ring_a + s * kStage, va = ka + kAtTok * kRowBytes;
+      const bool in0 = g < n, in1 = g + 8 < n;      // this lane's tokens g, g + 8
+      const int p0 = ws.mpos[s][g], p1 = ws.mpos[s][g + 8];
+      float wsum0 = 0.f, wsum1 = 0.f;
+      for (int r0 = 0;;) {
+        // logits of 16 tokens x 8 NB query rows
+        float c[NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[nb][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          uint32_t a[4];
+          ldsm4(a, ka + kt * kRowBytes + (((2 * ks + kc) ^ (kt & 7)) << 4));
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) mma16816(c[nb], a, bq[nb][ks][0], bq[nb][ks][1]);
+        }
+        if constexpr (kMode == kWeights) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (sees(p0, qp[nb][e], qlo[nb][e], p.sinks))
+                wsum0 += ex2(fmaf(c[nb][e], p.scale_log2, -lse2[nb][e]));
+              if (sees(p1, qp[nb][e], qlo[nb][e], p.sinks))
+                wsum1 += ex2(fmaf(c[nb][2 + e], p.scale_log2, -lse2[nb][e]));
+            }
+          r0 += 8 * NB;
+          if (8 * NB < p.R) load_rows(r0 < p.R ? r0 : 0);   // back to the first rows at the end
+          if (r0 < p.R) continue;
+          break;
+        } else {
+          uint32_t bh[NB][2], bl[NB][2];
+          float mref[NB][2];
+          bool grew = false;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (!(in0 && sees(p0, qp[nb][e], qlo[nb][e], p.sinks))) c[nb][e] = -INFINITY;
+              if (!(in1 && sees(p1, qp[nb][e], qlo[nb][e], p.sinks))) c[nb][2 + e] = -INFINITY;
+              float x = fmaxf(c[nb][e], c[nb][2 + e]);
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+              x *= p.scale_log2;
+              grew |= x > m[nb][e];
+              mref[nb][e] = fmaxf(x, m[nb][e]);
+            }
+          if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                // m = -inf (nothing seen yet): the factor is 0, and so are O and l
+                const float f = mref[nb][e] == m[nb][e] ? 1.f : ex2(m[nb][e] - mref[nb][e]);
+                m[nb][e] = mref[nb][e];
+                l[nb][e] *= f;
+#pragma unroll
+                for (int mb = 0; mb < 8; ++mb) {
+                  O[mb][nb][e] *= f;
+                  O[mb][nb][2 + e] *= f;
+                }
+              }
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float ref = m[nb][e] == -INFINITY ? 0.f : m[nb][e];
+              c[nb][e] = ex2(fmaf(c[nb][e], p.scale_log2, -ref));
+              c[nb][2 + e] = ex2(fmaf(c[nb][2 + e], p.scale_log2, -ref));
+              l[nb][e] += c[nb][e] + c[nb][2 + e];
+            }
+            // p as the sum of two bf16 (about 16 bits): one bf16 alone would cost the
+            // result as much again as its own rounding, and the steps are not the bound
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float x = c[nb][2 * h], y = c[nb][2 * h + 1];
+              const uint32_t hi = pack_bf16(x, y);
+              const uint32_t lo = pack_bf16(x - bf_lo(hi), y - bf_hi(hi));
+              bh[nb][h] = transpose8x8(hi);
+              bl[nb][h] = transpose8x8(lo);
+            }
+          }
+          if (careful) {
+            // tokens whose V row holds a value that is not finite
+            uint32_t bad = 0;
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+              const int r = 2 * i + (lane >> 4);
+              const uint4 x = *reinterpret_cast<const uint4*>(
+                  ring + s * kStage + kAtTok * kRowBytes + r * kRowBytes + (lane & 15) * 16);
+              auto two = [](uint32_t w) {
+                return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+              };
+              const uint32_t b =
+                  __ballot_sync(0xffffffffu, two(x.x) || two(x.y) || two(x.z) || two(x.w));
+              bad |= ((b & 0xffffu) ? 1u : 0u) << (2 * i) | ((b >> 16) ? 1u : 0u) << (2 * i + 1);
+            }
+#pragma unroll 1
+            for (; bad; bad &= bad - 1u) {
+              const int t = __ffs(bad) - 1;
+              uint8_t* vr = ring + s * kStage + kAtTok * kRowBytes + t * kRowBytes;
+              const int pt = ws.mpos[s][t];
+              float pv[NB][2];
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float a = __shfl_sync(0xffffffffu, c[nb][e], (t & 7) * 4 + q);
+                  const float b = __shfl_sync(0xffffffffu, c[nb][2 + e], (t & 7) * 4 + q);
+                  pv[nb][e] = t < 8 ? a : b;
+                }
+#pragma unroll
+              for (int mb = 0; mb < 8; ++mb)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const int ch = (2 * mb + h) ^ (t & 7);
+                  const float x = __bfloat162float(
+                      *reinterpret_cast<const __nv_bfloat16*>(vr + ch * 16 + g * 2));
+#pragma unroll
+                  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                      if (sees(pt, qp[nb][e], qlo[nb][e], p.sinks))
+                        O[mb][nb][2 * h + e] += pv[nb][e] * x;
+                }
+              __syncwarp();
+              if (lane < 16) *reinterpret_cast<uint4*>(vr + lane * 16) = make_uint4(0, 0, 0, 0);
+              __syncwarp();
+            }
+          }
+          // O^T (128 d x 8 NB) += V^T (128 d x 16) . p^T (16 x 8 NB)
+#pragma unroll
+          for (int mb = 0; mb < 8; ++mb) {
+            uint32_t a[4];
+            ldsm4_t(a, va + vt * kRowBytes + (((2 * mb + vc) ^ (vt & 7)) << 4));
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              mma16816(O[mb][nb], a, bh[nb][0], bh[nb][1]);
+              mma16816(O[mb][nb], a, bl[nb][0], bl[nb][1]);
+            }
+          }
+          break;
+        }
+      }
+      if constexpr (kMode == kWeights) {
+        // a token's sum over its query rows: the four lanes of its group
+        wsum0 += __shfl_xor_sync(0xffffffffu, wsum0, 1);
+        wsum0 += __shfl_xor_sync(0xffffffffu, wsum0, 2);
+        wsum1 += __shfl_xor_sync(0xffffffffu, wsum1, 1);
+        wsum1 += __shfl_xor_sync(0xffffffffu, wsum1, 2);
+        if (q == 0) {
+          if (in0) {
+            const int64_t i = base + ws.mslot[s][g];
+            p.acc_out[i] = (p.acc_in ? p.acc_in[i] : 0.f) + wsum0;
+          }
+          if (in1) {
+            const int64_t i = base + ws.mslot[s][g + 8];
+            p.acc_out[i] = (p.acc_in ? p.acc_in[i] : 0.f) + wsum1;
+          }
+        }
+      }
+      __syncwarp();   // this stage's slot is written next
+    }
+    cp_wait<0>();
+    if constexpr (kMode == kWeights) {
+      return;
+    } else {
+      if (careful) break;
+      bool ok = true;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int mb = 0; mb < 8; ++mb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ok = ok && finite(O[mb][nb][e]);
+      if (!__any_sync(0xffffffffu, !ok)) break;
+      __syncwarp();
+    }
+  }
+  if constexpr (kMode != kWeights) {
+    // the warps' parts to shared memory (the rings are done with), then joined
+    __syncthreads();
+    float* sO = reinterpret_cast<float*>(at_smem);   // [warp][8 NB][kOStride]
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = l[nb][e];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        const int r = 8 * nb + 2 * q + e;
+        if (g == 0) {
+          s_ml[wp][0][r] = m[nb][e];
+          s_ml[wp][1][r] = x;
+        }
+        float* o = sO + (wp * 8 * NB + r) * kOStride;
+#pragma unroll
+        for (int mb = 0; mb < 8; ++mb) {
+          o[16 * mb + g] = O[mb][nb][e];
+          o[16 * mb + g + 8] = O[mb][nb][2 + e];
+        }
+      }
+    }
+    __syncthreads();
+    const int nr = min(nrow, 8 * NB);
+    for (int i = tid; i < nr * 32; i += kAtThreads) {
+      const int r = i >> 5, d4 = i & 31;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kAtWarps; ++w) M = fmaxf(M, s_ml[w][0][r]);
+      float L = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kAtWarps; ++w) {
+        const float mw = s_ml[w][0][r], lw = s_ml[w][1][r];
+        // nothing seen by this warp (a row of NaN logits keeps m = -inf with l = NaN)
+        if (mw == -INFINITY && lw == 0.f) continue;
+        const float f = mw == M ? 1.f : ex2(mw - M);
+        const float4 x = *reinterpret_cast<const float4*>(
+            sO + (w * 8 * NB + r) * kOStride + 4 * d4);
+        L += f * lw;
+        o.x += f * x.x;
+        o.y += f * x.y;
+        o.z += f * x.z;
+        o.w += f * x.w;
+      }
+      const int64_t row = row_of(r);
+      if (p.part_o) {
+        const int64_t at =
+            kMode == kPrefix
+                ? static_cast<int64_t>(chunk) * p.rows + row
+                : (static_cast<int64_t>(item) * p.maxch + chunk) * p.R + row0 + r;
+        *reinterpret_cast<float4*>(p.part_o + at * 128 + 4 * d4) = o;
+        if (d4 == 0) p.part_ml[at] = make_float2(M, L);
+      } else {
+        attend_store(p, row, d4, M, L, o);
+      }
+    }
+  }
+}
+
+// Joins the parts of every query row, one warp per row, in a fixed order: the
+// prefix's chunks, then the unit's own.
+__global__ void __launch_bounds__(256) join_kernel(const AttendParams p, const JoinParams j) {
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= j.rows) return;
+  const int u = static_cast<int>(row / p.R), r = static_cast<int>(row - static_cast<int64_t>(u) * p.R);
+  const bool pre = p.unit_prefix && __ldg(&p.unit_prefix[u]) >= 0;
+  const int np = pre ? j.pre_chunks : 0;
+  float M = -INFINITY, L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = 0; c < np + j.own_chunks; ++c) {
+    const bool own = c >= np;
+    const int64_t at = own ? (static_cast<int64_t>(u) * j.own_chunks + (c - np)) * p.R + r
+                           : static_cast<int64_t>(c) * j.rows + row;
+    const float2 ml = own ? j.own_ml[at] : j.pre_ml[at];
+    if (ml.x == -INFINITY && ml.y == 0.f) continue;   // nothing visible there
+    const float4 x = *reinterpret_cast<const float4*>((own ? j.own_o : j.pre_o) + at * 128 + 4 * lane);
+    const float N = fmaxf(M, ml.x);
+    const float f = M == N ? 1.f : ex2(M - N), h = ml.x == N ? 1.f : ex2(ml.x - N);
+    M = N;
+    L = L * f + ml.y * h;
+    o.x = o.x * f + x.x * h;
+    o.y = o.y * f + x.y * h;
+    o.z = o.z * f + x.z * h;
+    o.w = o.w * f + x.w * h;
+  }
+  attend_store(p, row, lane, M, L, o);
+}
+
+template <int NB, int kMode>
+__host__ __device__ constexpr int at_smem_bytes() {
+  const int ring = kAtWarps * kAtStages * at_stage_bytes<kMode>();
+  const int fin = kMode == kWeights ? 0 : kAtWarps * 8 * NB * kOStride * 4;
+  return ring > fin ? ring : fin;
+}
+
+template <int NB, int kMode>
+cudaError_t configure_one() {
+  return cudaFuncSetAttribute(attend_kernel<NB, kMode>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              at_smem_bytes<NB, kMode>());
+}
+template <int kMode>
+cudaError_t configure_mode() {
+  cudaError_t e = configure_one<1, kMode>();
+  if (e == cudaSuccess) e = configure_one<2, kMode>();
+  if (e == cudaSuccess) e = configure_one<4, kMode>();
+  return e;
+}
+
+template <int kMode>
+cudaError_t launch_mode(const AttendParams& p, int rows, dim3 grid, cudaStream_t st) {
+  if (rows <= 8)
+    attend_kernel<1, kMode><<<grid, kAtThreads, at_smem_bytes<1, kMode>(), st>>>(p);
+  else if (rows <= 16)
+    attend_kernel<2, kMode><<<grid, kAtThreads, at_smem_bytes<2, kMode>(), st>>>(p);
+  else
+    attend_kernel<4, kMode><<<grid, kAtThreads, at_smem_bytes<4, kMode>(), st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t attend_configure() {
+  cudaError_t e = configure_mode<kOwn>();
+  if (e == cudaSuccess) e = configure_mode<kPrefix>();
+  if (e == cudaSuccess) e = configure_mode<kWeights>();
+  return e;
+}
+
+cudaError_t launch_attend(const AttendParams& p, int U, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>(U) * p.maxch, (p.R + 31) / 32);
+  return launch_mode<kOwn>(p, p.R, grid, st);
+}
+
+cudaError_t launch_attend_prefix(const AttendParams& p, int P, int max_rows, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>(P) * p.maxch, (max_rows + 31) / 32);
+  return launch_mode<kPrefix>(p, max_rows, grid, st);
+}
+
+cudaError_t launch_attend_join(const AttendParams& p, const JoinParams& j, cudaStream_t st) {
+  join_kernel<<<static_cast<unsigned>((j.rows + 7) / 8), 256, 0, st>>>(p, j);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_attend_weights(const AttendParams& p, int U, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>(U) * p.maxch, 1);
+  return launch_mode<kWeights>(p, p.R, grid, st);
+}
+
+}  // namespace rkv

@@ -1,0 +1,408 @@
+// C ABI of the operators that read and keep a live cache: attention over it
+// (with a shared prefix or without), eviction by accumulated weight, and new
+// tokens into freed slots with their positions.
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/rkv.h"
+#include "engine.cuh"
+#include "ptx.cuh"
+#include "rkv_internal.cuh"
+
+using namespace rkv;
+
+namespace {
+
+// The engine's device for the length of a call, whichever is current.
+struct DeviceGuard {
+  int was = -1;
+  bool ok = true;
+  explicit DeviceGuard(int dev) {
+    int cur = 0;
+    ok = cudaGetDevice(&cur) == cudaSuccess;
+    if (ok && cur != dev) {
+      ok = cudaSetDevice(dev) == cudaSuccess;
+      if (ok) was = cur;
+    }
+  }
+  ~DeviceGuard() {
+    if (was >= 0) cudaSetDevice(was);
+  }
+};
+
+struct Lengths {
+  int64_t T = 0;
+  int nmax = 0;
+};
+
+// Host-side checks of a batch whose units may have any length from 0 on.
+int check_rows(const rkv_engine* e, const rkv_batch* b, Lengths* L) {
+  if (!b || b->num_units < 0) return RKV_ERR_INVALID_ARG;
+  if (b->num_units > e->cfg.max_units) return RKV_ERR_CAPACITY;
+  if (!b->tok_off_host || !b->tok_off || !aligned(b->tok_off, 8)) return RKV_ERR_INVALID_ARG;
+  const int64_t* off = b->tok_off_host;
+  if (off[0] != 0) return RKV_ERR_INVALID_ARG;
+  int64_t nm = 0;
+  for (int u = 0; u < b->num_units; ++u) {
+    const int64_t n = off[u + 1] - off[u];
+    if (n < 0) return RKV_ERR_INVALID_ARG;
+    nm = std::max(nm, n);
+  }
+  if (nm > e->max_n) return RKV_ERR_UNSUPPORTED;
+  L->T = off[b->num_units];
+  if (L->T > e->cfg.max_tokens) return RKV_ERR_CAPACITY;
+  L->nmax = static_cast<int>(nm);
+  return RKV_OK;
+}
+
+// Rows of query parts that the scratch of unsplit-prefix calls holds: eight
+// full waves of 32-row CTAs.
+constexpr int64_t kPartRows = 75776;
+constexpr int64_t kPartFloats = 130;   // 128 values, maximum and sum
+
+int64_t shared_rows(const rkv_engine* e) {
+  return std::max<int64_t>(2ll * e->cfg.max_units * e->cfg.group * e->cfg.window, kPartRows);
+}
+
+// Scratch of the attention calls, allocated once: `rows` parts, then the
+// rows' log2 sums.  Not while a stream is captured.
+int attend_scratch(rkv_engine* e, float** buf, int64_t rows, cudaStream_t st) {
+  if (*buf) return RKV_OK;
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(st, &cs) != cudaSuccess) return cuda_fail(cudaErrorUnknown);
+  if (cs != cudaStreamCaptureStatusNone) return RKV_ERR_INVALID_ARG;
+  const size_t n = static_cast<size_t>(rows) * kPartFloats +
+                   static_cast<size_t>(e->cfg.max_units) * e->cfg.group * e->cfg.window;
+  if (rkv_engine_alloc(e, reinterpret_cast<void**>(buf), n * sizeof(float)) != cudaSuccess) {
+    cudaGetLastError();
+    *buf = nullptr;
+    return RKV_ERR_OOM;
+  }
+  return RKV_OK;
+}
+
+// Chunks of an item of `groups` 32-row groups (nmax the longest, sum over all
+// items): the cheapest count by waves of resident CTAs, a CTA costing its
+// groups and about four more, at most `cap`.
+int pick_chunks(int64_t items, int64_t sum, int64_t nmax, int64_t slots, int64_t cap) {
+  const int64_t avg = std::max<int64_t>(1, (sum + items - 1) / std::max<int64_t>(items, 1));
+  const int64_t most = std::min<int64_t>(std::max<int64_t>(1, cap), std::max<int64_t>(1, nmax / 4));
+  int64_t best = 1;
+  double least = 1e300;
+  for (int64_t c = 1; c <= std::min<int64_t>(most, 4096); c += c < 32 ? 1 : c / 16) {
+    const int64_t gpc = (nmax + c - 1) / c;
+    const int64_t ctas = items * ((avg + gpc - 1) / gpc);
+    const double cost = static_cast<double>((ctas + slots - 1) / slots) * (gpc + 4.0) +
+                        (c > 1 ? 4.0 : 0.0);
+    if (cost < least) {
+      least = cost;
+      best = c;
+    }
+  }
+  return static_cast<int>(best);
+}
+
+int check_prefix(const rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, int64_t* sum,
+                 int64_t* longest, int* most) {
+  if (x->num_prefixes < 0) return RKV_ERR_INVALID_ARG;
+  if (!x->off || !x->off_host || !x->unit_prefix || !x->unit_prefix_host || !x->mem_off ||
+      !x->mem_off_host || !x->mem || !x->mem_host)
+    return RKV_ERR_INVALID_ARG;
+  if (!aligned(x->off, 8) || !aligned(x->unit_prefix, 4) || !aligned(x->mem_off, 4) ||
+      !aligned(x->mem, 4))
+    return RKV_ERR_INVALID_ARG;
+  const int P = x->num_prefixes, U = b->num_units;
+  if (x->num_units != U || x->off_host[0] != 0 || x->mem_off_host[0] != 0)
+    return RKV_ERR_INVALID_ARG;
+  *longest = 0;
+  *most = 0;
+  for (int k = 0; k < P; ++k) {
+    const int64_t n = x->off_host[k + 1] - x->off_host[k];
+    const int m0 = x->mem_off_host[k], m1 = x->mem_off_host[k + 1];
+    if (n < 0 || m1 < m0) return RKV_ERR_INVALID_ARG;
+    if (n >= (static_cast<int64_t>(1) << 30)) return RKV_ERR_UNSUPPORTED;
+    *longest = std::max(*longest, n);
+    *most = std::max(*most, m1 - m0);
+  }
+  *sum = x->off_host[P];
+  int with = 0;
+  for (int u = 0; u < U; ++u) {
+    const int k = x->unit_prefix_host[u];
+    if (k < -1 || k >= P) return RKV_ERR_INVALID_ARG;
+    with += k >= 0;
+  }
+  // every unit with a prefix is listed once, under its prefix, in ascending order
+  if (x->mem_off_host[P] != with) return RKV_ERR_INVALID_ARG;
+  for (int k = 0; k < P; ++k)
+    for (int i = x->mem_off_host[k]; i < x->mem_off_host[k + 1]; ++i) {
+      const int u = x->mem_host[i];
+      if (u < 0 || u >= U || x->unit_prefix_host[u] != k ||
+          (i > x->mem_off_host[k] && x->mem_host[i - 1] >= u))
+        return RKV_ERR_INVALID_ARG;
+    }
+  if (*sum > 0 && (!x->K || !x->V || !aligned(x->K, 16) || !aligned(x->V, 16)))
+    return RKV_ERR_INVALID_ARG;
+  (void)e;
+  return RKV_OK;
+}
+
+// Groups of a sequence of n rows that a window of `local` tokens and the sinks
+// can touch, at most.
+int64_t reach(int64_t n, int local, int sinks, int nq) {
+  const int64_t all = (n + 31) / 32;
+  if (local <= 0) return all;
+  return std::min<int64_t>(all, (static_cast<int64_t>(sinks) + 31) / 32 +
+                                    (static_cast<int64_t>(local) + nq) / 32 + 2);
+}
+
+int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_attention* a,
+           rkv_stream_t stream) {
+  if (!e || !a) return RKV_ERR_INVALID_ARG;
+  Lengths L;
+  int rc = check_rows(e, b, &L);
+  if (rc != RKV_OK) return rc;
+  const int U = b->num_units;
+  if (a->num_queries < 1 || a->local < 0 || a->sinks < 0) return RKV_ERR_INVALID_ARG;
+  if (a->num_queries > e->cfg.window) return RKV_ERR_UNSUPPORTED;
+  if (U == 0) return RKV_OK;
+  if (!a->Q || !a->out || (L.T > 0 && (!b->K || !b->V))) return RKV_ERR_INVALID_ARG;
+  if (a->pos && !a->q_pos) return RKV_ERR_INVALID_ARG;
+  if (a->acc_in && !a->acc_out) return RKV_ERR_INVALID_ARG;
+  if (!aligned(b->K, 16) || !aligned(b->V, 16) || !aligned(a->Q, 16) || !aligned(a->out, 16) ||
+      !aligned(a->lse, 4) || !aligned(a->pos, 4) || !aligned(a->q_pos, 4) ||
+      !aligned(a->acc_in, 4) || !aligned(a->acc_out, 4))
+    return RKV_ERR_INVALID_ARG;
+  int64_t psum = 0, plong = 0;
+  int members = 0;
+  if (x) {
+    rc = check_prefix(e, b, x, &psum, &plong, &members);
+    if (rc != RKV_OK) return rc;
+    if (members == 0) x = nullptr;   // no unit has a prefix
+  }
+  DeviceGuard dev(e->device);
+  if (!dev.ok) return cuda_fail(cudaErrorUnknown);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t cap = x ? shared_rows(e) : kPartRows;
+  float** buf = x ? &e->at_shared : &e->at_part;
+  rc = attend_scratch(e, buf, cap, st);
+  if (rc != RKV_OK) return rc;
+
+  const int R = e->cfg.group * a->num_queries;
+  const int64_t rows = static_cast<int64_t>(U) * R;
+  const int rg = (R + 31) / 32;
+  AttendParams p = {};
+  p.tok_off = b->tok_off;
+  p.K = static_cast<const uint4*>(b->K);
+  p.V = static_cast<const uint4*>(b->V);
+  p.Q = static_cast<const uint32_t*>(a->Q);
+  p.keep = a->keep;
+  p.pos = a->pos;
+  p.q_pos = a->q_pos;
+  p.R = R;
+  p.nq = a->num_queries;
+  p.local = a->local;
+  p.sinks = a->sinks;
+  p.scale_log2 = kLog2e / sqrtf(static_cast<float>(kHeadDim));
+  p.out = static_cast<uint2*>(a->out);
+  p.lse = a->lse;
+  p.rows = rows;
+  float* part_o = *buf;
+  float2* part_ml = reinterpret_cast<float2*>(part_o + cap * 128);
+  float* lse2 = reinterpret_cast<float*>(part_ml + cap);
+  p.lse2 = a->acc_out ? lse2 : nullptr;
+  if (x) {
+    p.unit_prefix = x->unit_prefix;
+    p.pre_off = x->off;
+    p.mem_off = x->mem_off;
+    p.mem = x->mem;
+    p.PK = static_cast<const uint4*>(x->K);
+    p.PV = static_cast<const uint4*>(x->V);
+  }
+
+  // the units' own rows
+  int64_t gsum = 0, gmax = 1;
+  for (int u = 0; u < U; ++u) {
+    const int64_t n = b->tok_off_host[u + 1] - b->tok_off_host[u];
+    const int64_t g = a->pos ? (n + 31) / 32 : reach(n, a->local, a->sinks, p.nq);
+    gsum += g;
+    gmax = std::max(gmax, g);
+  }
+  const int64_t slots = std::max(1, 2 * e->nsm / rg);
+  const int own = pick_chunks(U, gsum, gmax, slots, cap / rows - (x ? 1 : 0));
+  p.maxch = own;
+  p.gpc = static_cast<int>((gmax + own - 1) / own);
+  JoinParams j = {};
+  const bool join = x || own > 1;
+  if (join) {
+    p.part_o = part_o;
+    p.part_ml = part_ml;
+    j.rows = rows;
+    j.own_chunks = own;
+    j.own_o = part_o;
+    j.own_ml = part_ml;
+  }
+  cudaError_t err;
+  t_begin(e, RKV_KERNEL_ATTEND, st);
+  err = launch_attend(p, U, st);
+  t_end(e, st);
+  if (err != cudaSuccess) return cuda_fail(err);
+  ++e->launches;
+
+  if (x) {
+    const int64_t used = static_cast<int64_t>(own) * rows;
+    const int64_t mrows = static_cast<int64_t>(members) * R;
+    const int64_t blocks = (mrows + 31) / 32;
+    int64_t pg = 0, pmax = 1;
+    for (int k = 0; k < x->num_prefixes; ++k) {
+      const int64_t g = (x->off_host[k + 1] - x->off_host[k] + 31) / 32;
+      pg += g;
+      pmax = std::max(pmax, g);
+    }
+    AttendParams pp = p;
+    pp.keep = nullptr;
+    pp.pos = nullptr;
+    pp.maxch = pick_chunks(x->num_prefixes, pg, pmax,
+                           std::max<int64_t>(1, 2 * e->nsm / blocks), (cap - used) / rows);
+    pp.gpc = static_cast<int>((pmax + pp.maxch - 1) / pp.maxch);
+    pp.part_o = part_o + used * 128;
+    pp.part_ml = part_ml + used;
+    j.pre_chunks = pp.maxch;
+    j.pre_o = pp.part_o;
+    j.pre_ml = pp.part_ml;
+    t_begin(e, RKV_KERNEL_SHARED, st);
+    err = launch_attend_prefix(pp, x->num_prefixes, static_cast<int>(mrows), st);
+    t_end(e, st);
+    if (err != cudaSuccess) return cuda_fail(err);
+    ++e->launches;
+  }
+  if (join) {
+    t_begin(e, RKV_KERNEL_JOIN, st);
+    err = launch_attend_join(p, j, st);
+    t_end(e, st);
+    if (err != cudaSuccess) return cuda_fail(err);
+    ++e->launches;
+  }
+  if (a->acc_out) {
+    AttendParams pw = p;
+    pw.acc_in = a->acc_in;
+    pw.acc_out = a->acc_out;
+    const int64_t all = (static_cast<int64_t>(L.nmax) + 31) / 32;
+    pw.maxch = pick_chunks(U, (L.T + 31) / 32 + U, std::max<int64_t>(all, 1), 2 * e->nsm,
+                           std::max<int64_t>(1, (static_cast<int64_t>(1) << 30) / U));
+    pw.gpc = static_cast<int>((std::max<int64_t>(all, 1) + pw.maxch - 1) / pw.maxch);
+    t_begin(e, RKV_KERNEL_WEIGHT, st);
+    err = launch_attend_weights(pw, U, st);
+    t_end(e, st);
+    if (err != cudaSuccess) return cuda_fail(err);
+    ++e->launches;
+  }
+  return RKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int rkv_attend(rkv_engine* e, const rkv_batch* b, const rkv_attention* a, rkv_stream_t stream) {
+  NvtxRange nvtx_("rkv_attend");
+  return attend(e, b, nullptr, a, stream);
+}
+
+int rkv_attend_shared(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x,
+                      const rkv_attention* a, rkv_stream_t stream) {
+  NvtxRange nvtx_("rkv_attend_shared");
+  if (!x) return RKV_ERR_INVALID_ARG;
+  return attend(e, b, x, a, stream);
+}
+
+int rkv_evict_accumulated(rkv_engine* e, const rkv_batch* b, const float* acc,
+                          const uint8_t* live, const int32_t* pos, int budget,
+                          const int32_t* budgets, int sinks, uint8_t* keep, int32_t* free_slots,
+                          int32_t* n_free, float* acc_out, int32_t* idx, int32_t* n_kept,
+                          rkv_stream_t stream) {
+  NvtxRange nvtx_("rkv_evict_accumulated");
+  if (!e) return RKV_ERR_INVALID_ARG;
+  Lengths L;
+  int rc = check_rows(e, b, &L);
+  if (rc != RKV_OK) return rc;
+  const int U = b->num_units;
+  if (budget < 0 || sinks < 0 || (idx == nullptr) != (n_kept == nullptr))
+    return RKV_ERR_INVALID_ARG;
+  if (U == 0) return RKV_OK;
+  if (!n_free || (L.T > 0 && (!acc || !keep || !free_slots))) return RKV_ERR_INVALID_ARG;
+  if (!aligned(acc, 4) || !aligned(pos, 4) || !aligned(budgets, 4) || !aligned(free_slots, 4) ||
+      !aligned(n_free, 4) || !aligned(acc_out, 4) || !aligned(idx, 4) || !aligned(n_kept, 4))
+    return RKV_ERR_INVALID_ARG;
+  const int64_t W = static_cast<int64_t>(budget) + sinks + e->cfg.window;
+  if (idx && (W >= (static_cast<int64_t>(1) << 30) || U * W >= (static_cast<int64_t>(1) << 31)))
+    return RKV_ERR_UNSUPPORTED;
+  DeviceGuard dev(e->device);
+  if (!dev.ok) return cuda_fail(cudaErrorUnknown);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  DropParams p = {};
+  p.tok_off = b->tok_off;
+  p.acc = acc;
+  p.live = live;
+  p.pos = pos;
+  p.budgets = budgets;
+  p.budget = budget;
+  p.sinks = sinks;
+  p.w = e->cfg.window;
+  p.W = idx ? static_cast<int>(W) : 0;
+  p.keep = keep;
+  p.free_slots = free_slots;
+  p.n_free = n_free;
+  p.acc_out = acc_out;
+  p.idx = idx;
+  p.n_kept = n_kept;
+  p.status = e->status;
+  t_begin(e, RKV_KERNEL_DROP, st);
+  cudaError_t err = launch_drop(p, U, L.nmax, st);
+  t_end(e, st);
+  if (err != cudaSuccess) return cuda_fail(err);
+  ++e->launches;
+  return RKV_OK;
+}
+
+int rkv_fill_slots_ex(rkv_engine* e, const rkv_batch* b, void* K, void* V,
+                      const int64_t* new_off, const int64_t* new_off_host, const void* K_new,
+                      const void* V_new, const int32_t* pos_new, uint8_t* keep,
+                      const int32_t* free_slots, const int32_t* n_free, int32_t* pos, float* acc,
+                      int32_t* free_out, int32_t* n_free_out, rkv_stream_t stream) {
+  NvtxRange nvtx_("rkv_fill_slots_ex");
+  if (!e) return RKV_ERR_INVALID_ARG;
+  Lengths L;
+  int rc = check_rows(e, b, &L);
+  if (rc != RKV_OK) return rc;
+  const int U = b->num_units;
+  if (!new_off || !new_off_host || !aligned(new_off, 8) || new_off_host[0] != 0)
+    return RKV_ERR_INVALID_ARG;
+  for (int u = 0; u < U; ++u)
+    if (new_off_host[u + 1] < new_off_host[u]) return RKV_ERR_INVALID_ARG;
+  const int64_t Tn = new_off_host[U];
+  if (Tn >= (static_cast<int64_t>(1) << 31)) return RKV_ERR_UNSUPPORTED;
+  if (U == 0) return RKV_OK;
+  if (!n_free || !n_free_out ||
+      (L.T > 0 && (!K || !V || !keep || !free_slots || !free_out)) ||
+      (Tn > 0 && (!K_new || !V_new || (pos && !pos_new))))
+    return RKV_ERR_INVALID_ARG;
+  // the list and its counts move together
+  if ((free_slots == free_out) != (n_free == n_free_out) && L.T > 0) return RKV_ERR_INVALID_ARG;
+  if (!aligned(K, 16) || !aligned(V, 16) || !aligned(K_new, 16) || !aligned(V_new, 16) ||
+      !aligned(pos_new, 4) || !aligned(free_slots, 4) || !aligned(n_free, 4) ||
+      !aligned(pos, 4) || !aligned(acc, 4) || !aligned(free_out, 4) || !aligned(n_free_out, 4))
+    return RKV_ERR_INVALID_ARG;
+  DeviceGuard dev(e->device);
+  if (!dev.ok) return cuda_fail(cudaErrorUnknown);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const FillExtra x = {pos_new, pos, acc, free_out, n_free_out};
+  t_begin(e, RKV_KERNEL_FILL, st);
+  cudaError_t err = launch_fill_slots(b->tok_off, U, new_off, K_new, V_new, K, V, keep,
+                                      free_slots, n_free, x, e->status, e->nsm, st);
+  t_end(e, st);
+  if (err != cudaSuccess) return cuda_fail(err);
+  ++e->launches;
+  return RKV_OK;
+}
+
+}  // extern "C"

@@ -73,7 +73,34 @@ struct rkv_engine {
   bool h_made = false;
   // rkv_refree_budget's logit scratch (max_tokens x padded G floats), on first use
   float* rf_z = nullptr;
+  // attention scratch, on first use: parts of split units and the rows' log2
+  // sums (at_part), the same and the prefixes' parts of shared calls (at_shared)
+  float* at_part = nullptr;
+  float* at_shared = nullptr;
 };
+
+namespace rkv {
+// Helpers of the C entry points.
+inline bool aligned(const void* p, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(p) % a) == 0;
+}
+inline int cuda_fail(cudaError_t e) {
+  (void)e;
+  cudaGetLastError();
+  return RKV_ERR_CUDA;
+}
+// Record the start event of a launch of `kernel` (when timing is on).
+inline void t_begin(rkv_engine* e, int kernel, cudaStream_t st) {
+  if (!e->timing || e->nev >= rkv_engine::kMaxEv) return;
+  e->ev_kernel[e->nev] = kernel;
+  cudaEventRecord(e->ev[e->nev][0], st);
+}
+inline void t_end(rkv_engine* e, cudaStream_t st) {
+  if (!e->timing || e->nev >= rkv_engine::kMaxEv) return;
+  cudaEventRecord(e->ev[e->nev][1], st);
+  ++e->nev;
+}
+}  // namespace rkv
 
 // Frees everything rkv_compress_host allocated (called by rkv_destroy).
 void rkv_host_pipeline_free(rkv_engine* e);

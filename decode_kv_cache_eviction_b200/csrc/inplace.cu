@@ -13,7 +13,9 @@
 //   256-byte row, 128-bit accesses) to slot free[t]; the slot is marked live;
 //   then the remaining free slots move to the front of the list, tile by tile
 //   in ascending order (each tile is read completely before it is written,
-//   and a tile only reads positions that no earlier tile wrote).
+//   and a tile only reads positions that no earlier tile wrote).  Optionally
+//   the filled slots get their tokens' positions and a zero accumulated weight,
+//   and the list that is left goes to another buffer.
 #include "ptx.cuh"
 #include "rkv_internal.cuh"
 
@@ -143,8 +145,10 @@ __global__ void __launch_bounds__(kFillThreads)
     fill_slots_kernel(const int64_t* __restrict__ tok_off, int U,
                       const int64_t* __restrict__ new_off, const uint4* __restrict__ Kn,
                       const uint4* __restrict__ Vn, uint4* __restrict__ K, uint4* __restrict__ V,
-                      uint8_t* __restrict__ keep, int32_t* __restrict__ free_slots,
-                      int32_t* __restrict__ n_free, int* status) {
+                      uint8_t* __restrict__ keep, const int32_t* free_slots,
+                      const int32_t* n_free, int32_t* free_out, int32_t* n_free_out,
+                      const int32_t* __restrict__ pos_new, int32_t* __restrict__ pos,
+                      float* __restrict__ acc, int* status) {
   const int tid = threadIdx.x;
   const int sub = tid & 15;            // 16-byte word of the 256-byte row
   const int rsub = tid >> 4;           // one of 16 rows in flight
@@ -157,7 +161,8 @@ __global__ void __launch_bounds__(kFillThreads)
     if (nf < 0 || nf > N) nf = 0;      // not produced by evict_in_place: take nothing
     const int n = want < nf ? want : nf;
     if (want > nf && tid == 0) atomicOr(status, kStatusBadIndex);
-    int32_t* fu = free_slots + base;
+    const int32_t* fu = free_slots + base;
+    int32_t* fo = free_out + base;
     for (int t = rsub; t < n; t += kFillThreads / 16) {
       const int slot = fu[t];
       if (slot < 0 || slot >= N) {
@@ -168,18 +173,24 @@ __global__ void __launch_bounds__(kFillThreads)
       const int64_t src = (nb + t) * 16 + sub;
       K[dst] = __ldcs(&Kn[src]);
       V[dst] = __ldcs(&Vn[src]);
-      if (sub == 0) keep[base + slot] = 1;
+      if (sub == 0) {
+        keep[base + slot] = 1;
+        if (pos) pos[base + slot] = pos_new[nb + t];
+        if (acc) acc[base + slot] = 0.f;
+      }
     }
     __syncthreads();   // every used slot has been read from the list
     // the remaining nf - n free slots move to the front; the tail becomes -1
-    for (int t0 = 0; t0 < nf; t0 += kFillThreads) {
+    // (a list written elsewhere is written whole)
+    const int wn = fo == fu ? nf : N;
+    for (int t0 = 0; t0 < wn; t0 += kFillThreads) {
       const int t = t0 + tid;
       const int v = t + n < nf ? fu[t + n] : -1;
       __syncthreads();
-      if (t < nf) fu[t] = v;
+      if (t < wn) fo[t] = v;
       __syncthreads();
     }
-    if (tid == 0) n_free[u] = nf - n;
+    if (tid == 0) n_free_out[u] = nf - n;
     __syncthreads();
   }
 }
@@ -205,13 +216,14 @@ cudaError_t launch_evict_in_place(const int64_t* tok_off, int U, int nmax, int W
 
 cudaError_t launch_fill_slots(const int64_t* tok_off, int U, const int64_t* new_off,
                               const void* K_new, const void* V_new, void* K, void* V,
-                              uint8_t* keep, int32_t* free_slots, int32_t* n_free, int* status,
-                              int nsm, cudaStream_t st) {
+                              uint8_t* keep, const int32_t* free_slots, const int32_t* n_free,
+                              const FillExtra& x, int* status, int nsm, cudaStream_t st) {
   int grid = nsm * 4;
   if (grid > U) grid = U;
   fill_slots_kernel<<<grid, kFillThreads, 0, st>>>(
       tok_off, U, new_off, static_cast<const uint4*>(K_new), static_cast<const uint4*>(V_new),
-      static_cast<uint4*>(K), static_cast<uint4*>(V), keep, free_slots, n_free, status);
+      static_cast<uint4*>(K), static_cast<uint4*>(V), keep, free_slots, n_free, x.free_out,
+      x.n_free_out, x.pos_new, x.pos, x.acc, status);
   return cudaGetLastError();
 }
 

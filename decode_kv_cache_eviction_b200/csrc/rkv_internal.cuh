@@ -281,9 +281,84 @@ cudaError_t launch_evict_in_place(const int64_t* tok_off, int U, int nmax, int W
                                   const int32_t* idx, const int32_t* n_kept, uint8_t* keep,
                                   int32_t* free_slots, int32_t* n_free, int* status, int nsm,
                                   cudaStream_t st);
+// What rkv_fill_slots_ex adds to rkv_fill_slots (all null without it): the
+// positions and zero weights of the filled slots, and other buffers for the
+// list that is left (null: in place).
+struct FillExtra {
+  const int32_t* pos_new;
+  int32_t* pos;
+  float* acc;
+  int32_t* free_out;
+  int32_t* n_free_out;
+};
 cudaError_t launch_fill_slots(const int64_t* tok_off, int U, const int64_t* new_off,
                               const void* K_new, const void* V_new, void* K, void* V,
-                              uint8_t* keep, int32_t* free_slots, int32_t* n_free, int* status,
-                              int nsm, cudaStream_t st);
+                              uint8_t* keep, const int32_t* free_slots, const int32_t* n_free,
+                              const FillExtra& x, int* status, int nsm, cudaStream_t st);
+
+// ---------------------------------------------------------------- attention
+struct AttendParams {
+  const int64_t* tok_off;        // [U+1]
+  const uint4* K;
+  const uint4* V;
+  const uint32_t* Q;             // [U, G, nq, d] bf16
+  const uint8_t* keep;           // [T] or null
+  const int32_t* pos;            // [T] or null
+  const int32_t* q_pos;          // [U] or null
+  int R;                         // G * nq query rows per unit
+  int nq;
+  int local;                     // sliding window in tokens (0: none)
+  int sinks;
+  int maxch;                     // chunks per unit (or prefix)
+  int gpc;                       // 32-row groups per chunk
+  float scale_log2;              // log2(e) / sqrt(d)
+  uint2* out;                    // [U, G, nq, d] bf16
+  float* lse;                    // [U, G, nq] or null
+  float* lse2;                   // scratch [U * R]: log2 of the rows' sums, or null
+  const float* acc_in;           // [T] or null
+  float* acc_out;                // [T] or null
+  float* part_o;                 // parts [.., 128], null: the chunk is the whole row
+  float2* part_ml;               // parts' (maximum in log2 units, sum)
+  // shared prefixes
+  int64_t rows;                  // U * R
+  const int32_t* unit_prefix;    // [U] or null
+  const int64_t* pre_off;        // [P+1]
+  const int32_t* mem_off;        // [P+1]
+  const int32_t* mem;            // units of each prefix, ascending
+  const uint4* PK;
+  const uint4* PV;
+};
+struct JoinParams {
+  int64_t rows;                  // U * R
+  int own_chunks, pre_chunks;
+  const float* own_o;            // [U, own_chunks, R, 128]
+  const float2* own_ml;
+  const float* pre_o;            // [pre_chunks, U * R, 128]
+  const float2* pre_ml;
+};
+cudaError_t attend_configure();
+cudaError_t launch_attend(const AttendParams& p, int U, cudaStream_t st);
+cudaError_t launch_attend_prefix(const AttendParams& p, int P, int max_rows, cudaStream_t st);
+cudaError_t launch_attend_join(const AttendParams& p, const JoinParams& j, cudaStream_t st);
+cudaError_t launch_attend_weights(const AttendParams& p, int U, cudaStream_t st);
+
+// ---------------------------------------------------------------- eviction by weight
+struct DropParams {
+  const int64_t* tok_off;        // [U+1]
+  const float* acc;              // [T]
+  const uint8_t* live;           // [T] or null
+  const int32_t* pos;            // [T] or null
+  const int32_t* budgets;        // [U] or null
+  int budget, sinks, w, W;       // W = budget + sinks + w, the row stride of idx
+  uint8_t* keep;                 // [T]
+  int32_t* free_slots;           // [T]
+  int32_t* n_free;               // [U]
+  float* acc_out;                // [T] or null
+  int32_t* idx;                  // [U, W] or null
+  int32_t* n_kept;               // [U] or null
+  int* status;
+};
+cudaError_t drop_configure();
+cudaError_t launch_drop(const DropParams& p, int U, int nmax, cudaStream_t st);
 
 }  // namespace rkv

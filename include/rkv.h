@@ -223,6 +223,103 @@ int rkv_fill_slots(rkv_engine* eng, const rkv_batch* batch, void* K, void* V,
                    const void* V_new, uint8_t* keep, int32_t* free_slots, int32_t* n_free,
                    rkv_stream_t stream);
 
+/* Decode attention over a live cache: what a decode step computes from the cache
+ * that the calls above keep (the article's 边生成边压缩: the cache is compressed
+ * while it is being read).  Query (g, t) of unit u, t < n_q, sits at position
+ * qp = q_pos[u] - (n_q - 1) + t and sees row i of its unit if
+ *   keep[row] != 0, and pos <= qp, and
+ *   (local == 0 or pos > qp - local or pos < sinks),
+ * where pos is the row's position.  Over the rows it sees, with z = q . k / sqrt(d):
+ *   out = sum softmax(z) v (bf16, rounded once),  lse = log sum e^z;
+ * a query that sees nothing gets out = 0 and lse = -inf.  What lies in a row that a
+ * query does not see (stale values, infinities, NaN) does not reach its result. */
+typedef struct {
+  int num_queries;         /* n_q, 1 <= n_q <= the engine's window */
+  int local;               /* sliding window in positions, 0: none */
+  int sinks;               /* positions below it stay visible behind the window */
+  const void* Q;           /* device bf16 [U, G, n_q, d], post-RoPE */
+  const uint8_t* keep;     /* device [T] live mask (rkv_evict_in_place), NULL: all live */
+  const int32_t* pos;      /* device [T] position of every row, NULL: row i of a unit
+                              sits at i (behind its prefix: prefix length + i) */
+  const int32_t* q_pos;    /* device [U] position of the newest query, NULL: of the
+                              unit's last row; required with pos */
+  const float* acc_in;     /* device [T] accumulated weights so far, NULL: zeros */
+  float* acc_out;          /* device [T] or NULL: acc_in + sum over (g, t) of softmax(z)
+                              for every row of the units; may be acc_in itself */
+  void* out;               /* device bf16 [U, G, n_q, d] */
+  float* lse;              /* device [U, G, n_q] or NULL */
+} rkv_attention;
+
+/* Attention over the batch's own rows (K, V, tok_off; the batch's Q is not used).
+ * Units may have any length from 0 to the engine's limit.  Sums are held in
+ * fp32 and results do not depend on timing.  The first call allocates a scratch
+ * of about 40 MB, kept until rkv_destroy (RKV_ERR_OOM if that fails;
+ * RKV_ERR_INVALID_ARG if `stream` is being captured then: make one call before a
+ * capture).  Runs on the engine's device, whichever is current.  Captured calls
+ * share the engine's scratch like eager ones: replays must be ordered with the
+ * engine's other calls. */
+int rkv_attend(rkv_engine* eng, const rkv_batch* batch, const rkv_attention* att,
+               rkv_stream_t stream);
+
+/* Prefixes that several units share (samples of one prompt): their K and V are
+ * stored once, and each prefix is read once for all its units. */
+typedef struct {
+  int num_prefixes;                /* P >= 0 */
+  int num_units;                   /* U of the batches it is used with */
+  const int64_t* off;              /* device [P+1] row offsets into K and V */
+  const int64_t* off_host;         /* HOST copy */
+  const void* K;                   /* device bf16 [off[P], d] */
+  const void* V;
+  const int32_t* unit_prefix;      /* device [U]: prefix of each unit, -1: none */
+  const int32_t* unit_prefix_host; /* HOST copy */
+  const int32_t* mem_off;          /* device [P+1]: prefix p's units are */
+  const int32_t* mem_off_host;     /*   mem[mem_off[p]] .. mem[mem_off[p+1]-1], */
+  const int32_t* mem;              /* device [mem_off[P]], ascending within a prefix */
+  const int32_t* mem_host;         /* HOST copies */
+} rkv_prefix;
+
+/* rkv_attend where a unit's keys are its prefix's rows followed by its own: prefix
+ * row j sits at position j, own row i at prefix length + i (or pos[row]), and
+ * the newest query at prefix length + N_u - 1 (or q_pos[u]).  All prefix rows are
+ * live; keep, acc_in and acc_out cover the own rows (weights are those of the
+ * softmax over both parts).  The first call allocates a scratch of
+ * 520 * max(2 max_units G w, 75776) bytes, under the same conditions. */
+int rkv_attend_shared(rkv_engine* eng, const rkv_batch* batch, const rkv_prefix* prefix,
+                      const rkv_attention* att, rkv_stream_t stream);
+
+/* Eviction by accumulated attention weight (rkv_attend's acc_out), in place.  Of
+ * unit u's live rows there stay: those at positions below `sinks`, those at the w
+ * newest positions (above newest - w, newest the largest live position), and of
+ * the rest the B_u rows of largest weight, B_u = budgets ? clamp(budgets[u], 0,
+ * budget) : budget; equal weights go to the lower row, -0 equals +0, NaN ranks
+ * below every number.
+ *   acc [T]; live [T] live mask before the call or NULL (all live); pos [T] or
+ *   NULL (row index); budgets device [U] or NULL;
+ *   keep [T] uint8, free_slots [T], n_free [U]: as rkv_evict_in_place writes them
+ *     (keep may be live itself);
+ *   acc_out [T] or NULL: acc where the row stays, 0 elsewhere (may be acc);
+ *   idx [U, budget + sinks + w] and n_kept [U], both or neither: the kept rows in
+ *     ascending order, then -1, for rkv_compact with budget + sinks as its budget.
+ * Live rows of one unit have distinct positions; if more rows stay than idx can
+ * hold, the first ones are written and RKV_ERR_DEVICE is set. */
+int rkv_evict_accumulated(rkv_engine* eng, const rkv_batch* batch, const float* acc,
+                          const uint8_t* live, const int32_t* pos, int budget,
+                          const int32_t* budgets, int sinks, uint8_t* keep,
+                          int32_t* free_slots, int32_t* n_free, float* acc_out, int32_t* idx,
+                          int32_t* n_kept, rkv_stream_t stream);
+
+/* rkv_fill_slots that also keeps what attention and eviction read: a filled row gets
+ * its token's position (pos [T] from pos_new [new_off[U]]) and a zero accumulated
+ * weight (acc [T]); pos and acc may be NULL.  The list that is left goes to
+ * free_out [T] and n_free_out [U]: the input buffers themselves (in place), or
+ * others, which are written whole.  Units may have any length from 0 on.  Everything
+ * else as for rkv_fill_slots. */
+int rkv_fill_slots_ex(rkv_engine* eng, const rkv_batch* batch, void* K, void* V,
+                      const int64_t* new_off, const int64_t* new_off_host, const void* K_new,
+                      const void* V_new, const int32_t* pos_new, uint8_t* keep,
+                      const int32_t* free_slots, const int32_t* n_free, int32_t* pos,
+                      float* acc, int32_t* free_out, int32_t* n_free_out, rkv_stream_t stream);
+
 /* rkv_score, rkv_select and rkv_compact in one call.  a and r are caller-owned
  * scratch [T] fp32 (they hold the scores afterwards). */
 int rkv_compress(rkv_engine* eng, const rkv_batch* batch, float lambda, int budget,
@@ -309,7 +406,12 @@ enum {
   RKV_KERNEL_FILL = 6,    /* new tokens into free slots */
   RKV_KERNEL_REFREE = 7,  /* adaptive budget (newest query's attention row) */
   RKV_KERNEL_FINISH = 8,  /* symmetric GEMM form: partial sums -> m, token softmax -> r */
-  RKV_NUM_KERNELS = 9
+  RKV_KERNEL_ATTEND = 9,  /* attention over the units' own rows */
+  RKV_KERNEL_SHARED = 10, /* attention over shared prefixes */
+  RKV_KERNEL_JOIN = 11,   /* parts of split rows joined */
+  RKV_KERNEL_WEIGHT = 12, /* accumulated attention weights */
+  RKV_KERNEL_DROP = 13,   /* eviction by accumulated weight */
+  RKV_NUM_KERNELS = 14
 };
 
 /* Per-kernel timing.  While enabled, the engine records a pair of CUDA events

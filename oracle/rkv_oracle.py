@@ -241,6 +241,54 @@ def fill_free_slots(K: np.ndarray, V: np.ndarray, keep: np.ndarray, free: np.nda
     return K2, V2, keep2
 
 
+def attend(Q, K, V, pos, q_pos, live=None, local: int = 0, sinks: int = 0):
+    """Decode attention of one unit.  Q [G, n, d]; K, V [N, d]; pos [N] positions;
+    q_pos [n] positions of the queries.  Query t sees row i if it is live, not
+    later (pos <= q_pos) and inside the window (pos > q_pos - local) or a sink
+    (pos < sinks).  Returns out [G, n, d], lse [G, n], p [G, n, N] (all rows;
+    0 where unseen), seen [n, N].  A query that sees nothing has out 0, lse -inf."""
+    G, n, d = Q.shape
+    N = len(K)
+    pos = np.asarray(pos, dtype=np.int64)
+    out, lse = np.zeros((G, n, d)), np.full((G, n), -np.inf)
+    p = np.zeros((G, n, N))
+    seen = np.zeros((n, N), dtype=bool)
+    for t in range(n):
+        at = int(q_pos[t])
+        s = pos <= at
+        if local:
+            s &= (pos > at - local) | (pos < sinks)
+        if live is not None:
+            s &= np.asarray(live) != 0
+        seen[t] = s
+        if not s.any():
+            continue
+        z = Q[:, t] @ K[s].T / np.sqrt(d)
+        top = z.max(axis=1, keepdims=True)
+        e = np.exp(z - top)
+        total = e.sum(axis=1, keepdims=True)
+        lse[:, t] = (top + np.log(total))[:, 0]
+        p[:, t, s] = e / total
+        out[:, t] = (e / total) @ V[s]
+    return out, lse, p, seen
+
+
+def evict_accumulated(acc, pos, live, w: int, budget: int, sinks: int = 0):
+    """Rows that stay when a unit is evicted by accumulated attention weight: live
+    rows at positions below ``sinks`` or above newest - w (newest: the largest
+    live position), and the ``budget`` heaviest other live rows (ties: lower row;
+    NaN last).  Returns the kept rows, ascending."""
+    rows = np.flatnonzero(np.asarray(live))
+    if len(rows) == 0:
+        return rows
+    pos = np.asarray(pos, dtype=np.int64)
+    newest = pos[rows].max()
+    safe = (pos[rows] < sinks) | (pos[rows] > newest - w)
+    rest = rows[~safe]
+    order = np.lexsort((rest, -np.asarray(acc)[rest]))   # NaN sorts last
+    return np.sort(np.concatenate([rows[safe], rest[order[:budget]]])).astype(np.int64)
+
+
 def run_unit(Q, K, V, w: int, budget: int, lam: float, redundancy="rowblocks"):
     """Whole path for one unit.  ``redundancy`` picks the row-mean definition
     (``rowblocks``), its closed form (``closed``) or the row-max reading

@@ -1,0 +1,113 @@
+"""Host-side checks of the attention and weight-eviction calls (no GPU needed):
+argument checks of the C entry points and the binding, struct layouts, and the
+oracle's definitions pinned by hand."""
+import ctypes
+import os
+import subprocess
+import tempfile
+
+import numpy as np
+import pytest
+import torch
+
+import decode_kv_cache_eviction_b200 as rkv
+from decode_kv_cache_eviction_b200 import _binding as B
+from oracle import rkv_oracle as ora
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from decode_kv_cache_eviction_b200 import build
+    build.build()
+
+
+def test_struct_layouts_match_header():
+    fields = {"rkv_attention": B.RkvAttention, "rkv_prefix": B.RkvPrefix}
+    lines = []
+    for name, s in fields.items():
+        lines.append(f'printf("%zu\\n", sizeof({name}));')
+        lines += [f'printf("%zu\\n", offsetof({name}, {f}));' for f, _ in s._fields_]
+    src = '#include <stdio.h>\n#include <stddef.h>\n#include "rkv.h"\nint main(void){' + "".join(lines) + "return 0;}"
+    with tempfile.TemporaryDirectory() as d:
+        c, exe = os.path.join(d, "t.c"), os.path.join(d, "t")
+        open(c, "w").write(src)
+        subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", os.path.join(ROOT, "include"),
+                        c, "-o", exe], check=True)
+        got = [int(x) for x in subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()]
+    want = []
+    for s in fields.values():
+        want.append(ctypes.sizeof(s))
+        want += [getattr(s, f).offset for f, _ in s._fields_]
+    assert got == want
+
+
+def test_null_arguments():
+    L = rkv.lib()
+    n = None
+    att = B.RkvAttention()
+    assert L.rkv_attend(n, n, n, n) == B.RKV_ERR_INVALID_ARG
+    assert L.rkv_attend(n, n, ctypes.byref(att), n) == B.RKV_ERR_INVALID_ARG
+    assert L.rkv_attend_shared(n, n, n, ctypes.byref(att), n) == B.RKV_ERR_INVALID_ARG
+    assert L.rkv_evict_accumulated(n, n, n, n, n, 4, n, 0, n, n, n, n, n, n, n) == B.RKV_ERR_INVALID_ARG
+    assert L.rkv_fill_slots_ex(n, n, n, n, n, n, n, n, n, n, n, n, n, n, n, n, n) == B.RKV_ERR_INVALID_ARG
+
+
+def test_prefix_plan_arguments():
+    kv = torch.zeros((10, 128), dtype=torch.bfloat16)
+    for off, up in (([1, 10], [0]), ([0, 10, 5], [0]), ([0, 10], [1]), ([0, 10], [-2]), ([0], [0])):
+        with pytest.raises(ValueError):
+            rkv.Prefix(kv, kv, off, up)
+    with pytest.raises(ValueError):                 # not on a GPU
+        rkv.Prefix(kv, kv, [0, 10], [0, 0])
+
+
+def test_batch_of_offsets_needs_a_device():
+    with pytest.raises(ValueError):
+        rkv.Batch(None, None, None, [0, 5])
+    b = rkv.Batch(None, None, None, [0, 5], device="cpu")
+    assert b.num_units == 1 and b.num_tokens == 5
+    with pytest.raises(ValueError):
+        rkv.Offsets([[0, 1]], "cpu")
+
+
+def test_oracle_attend_by_hand():
+    """Two keys along one axis: z = 1 and 0, p = e / (e + 1)."""
+    d = 4
+    q = np.zeros((1, 2, d))
+    q[0, :, 0] = 2.0
+    k = np.zeros((3, d))
+    k[0, 0] = 1.0
+    v = np.array([[1.0] * d, [3.0] * d, [100.0] * d])
+    out, lse, p, seen = ora.attend(q, k, v, [0, 1, 2], [1, 2], live=[1, 1, 0])
+    a = np.e / (np.e + 1)
+    assert np.allclose(p[0], [[a, 1 - a, 0]] * 2) and np.allclose(lse, np.log(np.e + 1))
+    assert np.allclose(out[0], a + 3 * (1 - a))
+    assert seen.tolist() == [[True, True, False]] * 2
+    # a window of one position, with and without a sink; a query before everything
+    out, lse, p, _ = ora.attend(q[:, :1], k, v, [0, 1, 2], [2], local=1)
+    assert np.allclose(out, 100.0)
+    _, _, p, _ = ora.attend(q[:, :1], k, v, [0, 1, 2], [2], local=1, sinks=1)
+    assert np.allclose(p[0, 0], [a, 0, 1 - a])
+    out, lse, _, _ = ora.attend(q[:, :1], k, v, [0, 1, 2], [-1])
+    assert np.all(out == 0) and np.all(np.isneginf(lse))
+
+
+def test_oracle_attend_matches_importance():
+    """Without masks, the mean of p over queries and heads is the importance."""
+    rng = np.random.default_rng(0)
+    Q, K = rng.standard_normal((2, 3, 8)), rng.standard_normal((20, 8))
+    _, _, p, _ = ora.attend(Q, K, K, np.arange(20), 17 + np.arange(3))
+    assert np.allclose(p, ora.attention_probs(Q, K))
+
+
+def test_oracle_evict_accumulated_by_hand():
+    acc = np.array([9.0, 1.0, 5.0, 5.0, np.nan, 0.0, 2.0])
+    kept = lambda *a, **k: ora.evict_accumulated(acc, *a, **k).tolist()
+    assert kept(range(7), [1] * 7, 1, 2) == [0, 2, 6]          # newest 6, then 9 and the first 5
+    assert kept(range(7), [1] * 7, 1, 5, sinks=1) == [0, 1, 2, 3, 4, 5, 6]
+    assert kept(range(7), [1] * 7, 1, 4, sinks=1) == [0, 1, 2, 3, 5, 6]   # NaN goes last
+    assert kept([6, 5, 4, 3, 2, 1, 0], [1] * 7, 2, 1, sinks=1) == [0, 1, 2, 6]
+    assert kept(range(7), [0, 1, 0, 1, 1, 1, 0], 1, 1) == [3, 5]
+    assert kept(range(7), [0] * 7, 3, 5) == []
