@@ -83,7 +83,35 @@ int64_t sym_scratch_bound(int64_t max_tokens, int max_units, int64_t max_len) {
   return static_cast<int64_t>(std::min(b1, b2)) + 1;
 }
 
+// Scratch of rkv_refree_budget: logits [max_tokens x GP], per-unit chunk offsets,
+// per-chunk head statistics and energies.
+struct RefreeScratch {
+  size_t z, off, cs, ce;
+};
+RefreeScratch refree_scratch(const rkv_config& cfg) {
+  const int GP = refree_padded_group(cfg.group);
+  const size_t max_ch = static_cast<size_t>(refree_max_chunks(cfg.max_tokens, cfg.max_units));
+  RefreeScratch s;
+  s.z = round_up(sizeof(float) * static_cast<size_t>(cfg.max_tokens) * GP);
+  s.off = round_up(sizeof(int) * (static_cast<size_t>(cfg.max_units) + 1));
+  s.cs = round_up(sizeof(float2) * max_ch * GP);
+  s.ce = round_up(sizeof(float) * max_ch);
+  return s;
+}
+
 }  // namespace
+
+int rkv_logit_scratch(rkv_engine* e) {
+  if (e->rf_z) return RKV_OK;
+  const RefreeScratch s = refree_scratch(e->cfg);
+  if (dev_alloc(&e->fault, reinterpret_cast<void**>(&e->rf_z), s.z + s.off + s.cs + s.ce) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    e->rf_z = nullptr;
+    return RKV_ERR_OOM;
+  }
+  return RKV_OK;
+}
 
 cudaError_t rkv_engine_alloc(rkv_engine* e, void** p, size_t bytes) {
   return dev_alloc(&e->fault, p, bytes);
@@ -183,7 +211,7 @@ int rkv_create(const rkv_config* cfg, rkv_engine** out) {
   e->max_chunks = score_max_chunks(cfg->max_tokens, cfg->max_units, e->score_ctas, e->rp);
 
   if (select_configure() != cudaSuccess || inplace_configure() != cudaSuccess ||
-      attend_configure() != cudaSuccess || drop_configure() != cudaSuccess) {
+      attend_configure() != cudaSuccess) {
     delete e;
     return cuda_fail(cudaErrorUnknown);
   }
@@ -622,22 +650,9 @@ int rkv_refree_budget(rkv_engine* e, const rkv_batch* b, float T, int sinks, int
   if (e->cfg.group > 8) return RKV_ERR_UNSUPPORTED;
   const int U = b->num_units;
   if (U == 0) return RKV_OK;
-  // scratch, on first use: logits [max_tokens x GP], per-unit chunk offsets,
-  // per-chunk head statistics and energies
-  const int GP = refree_padded_group(e->cfg.group);
-  const int64_t max_ch = refree_max_chunks(e->cfg.max_tokens, e->cfg.max_units);
-  const size_t z_bytes = round_up(sizeof(float) * static_cast<size_t>(e->cfg.max_tokens) * GP);
-  const size_t off_bytes = round_up(sizeof(int) * (static_cast<size_t>(e->cfg.max_units) + 1));
-  const size_t cs_bytes = round_up(sizeof(float2) * static_cast<size_t>(max_ch) * GP);
-  const size_t ce_bytes = round_up(sizeof(float) * static_cast<size_t>(max_ch));
-  if (!e->rf_z) {
-    if (dev_alloc(&e->fault, reinterpret_cast<void**>(&e->rf_z),
-                  z_bytes + off_bytes + cs_bytes + ce_bytes) != cudaSuccess) {
-      cudaGetLastError();
-      e->rf_z = nullptr;
-      return RKV_ERR_OOM;
-    }
-  }
+  const RefreeScratch sc = refree_scratch(e->cfg);
+  rc = rkv_logit_scratch(e);
+  if (rc != RKV_OK) return rc;
   int64_t nchunks = 0;
   for (int u = 0; u < U; ++u)
     nchunks += (b->tok_off_host[u + 1] - b->tok_off_host[u] + kRfChunk - 1) / kRfChunk;
@@ -654,9 +669,9 @@ int rkv_refree_budget(rkv_engine* e, const rkv_batch* b, float T, int sinks, int
   ra.T = T;
   ra.max_budget = max_budget;
   ra.zbuf = reinterpret_cast<float*>(scr);
-  ra.chunk_off = reinterpret_cast<int*>(scr + z_bytes);
-  ra.cstat = reinterpret_cast<float2*>(scr + z_bytes + off_bytes);
-  ra.cenergy = reinterpret_cast<float*>(scr + z_bytes + off_bytes + cs_bytes);
+  ra.chunk_off = reinterpret_cast<int*>(scr + sc.z);
+  ra.cstat = reinterpret_cast<float2*>(scr + sc.z + sc.off);
+  ra.cenergy = reinterpret_cast<float*>(scr + sc.z + sc.off + sc.cs);
   ra.p_last = p_last;
   ra.budgets = budgets;
   ra.keep_count = keep_count;

@@ -149,6 +149,116 @@ __device__ __forceinline__ void attend_store(const AttendParams& p, int64_t row,
   }
 }
 
+// Joins the n parts of one query row and writes it, one warp: lane 4-dimension
+// groups, parts in order.  Part c is at index at(c) of o / ml.  The parts' (maximum,
+// sum) pairs of 32 parts are loaded at once, one per lane, and four parts' values
+// are in flight.
+template <class At>
+__device__ __forceinline__ void join_row(const AttendParams& p, int64_t row, int n, At at) {
+  const int lane = threadIdx.x & 31;
+  float M = -INFINITY, L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c0 = 0; c0 < n; c0 += 32) {
+    float2 ml = make_float2(-INFINITY, 0.f);
+    const float4* src = nullptr;
+    if (c0 + lane < n) at(c0 + lane, ml, src);
+    const unsigned some = __ballot_sync(0xffffffffu, !(ml.x == -INFINITY && ml.y == 0.f));
+    if (some == 0) continue;   // nothing visible in these parts
+    float top = ml.x;
+#pragma unroll
+    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const float N = fmaxf(M, top);
+    const float f = M == N ? 1.f : ex2(M - N);
+    const float h = ml.x == N ? 1.f : ex2(ml.x - N);
+    float l = ml.y * h;
+#pragma unroll
+    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    M = N;
+    L = L * f + l;
+    o.x *= f;
+    o.y *= f;
+    o.z *= f;
+    o.w *= f;
+    const int e = min(32, n - c0);
+    for (int k0 = 0; k0 < e; k0 += 4) {
+      float4 x[4];
+      float w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint64_t a = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), k0 + k);
+        w[k] = __shfl_sync(0xffffffffu, h, k0 + k);
+        x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if ((some >> (k0 + k)) & 1u) x[k] = __ldcg(reinterpret_cast<const float4*>(a) + lane);
+        else w[k] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        o.x = fmaf(x[k].x, w[k], o.x);
+        o.y = fmaf(x[k].y, w[k], o.y);
+        o.z = fmaf(x[k].z, w[k], o.z);
+        o.w = fmaf(x[k].w, w[k], o.w);
+      }
+    }
+  }
+  attend_store(p, row, lane, M, L, o);
+}
+
+// acc_out = acc_in + sum_r 2^(z_r - lse2_r) for rows i0 .. i1 of a unit, from the
+// logits that the attention pass left in p.z (one query per head, so a row is
+// seen by all heads or by none).  GP: floats per row of p.z.
+template <int GP>
+__device__ __forceinline__ void weights_from_logits(const AttendParams& p, int64_t base, int first,
+                                                    int64_t qpos, const float* lse2, int i0,
+                                                    int i1) {
+  const int qp = clamp32(qpos), lo = p.local > 0 ? clamp32(qpos - p.local) : INT_MIN;
+  float ls[GP];
+#pragma unroll
+  for (int r = 0; r < GP; ++r) ls[r] = r < p.R ? lse2[r] : INFINITY;
+#pragma unroll 4
+  for (int i = i0 + threadIdx.x; i < i1; i += blockDim.x) {
+    const int64_t at = base + i;
+    float a = p.acc_in ? p.acc_in[at] : 0.f;
+    bool on = !p.keep || p.keep[at] != 0;
+    const int ps = p.pos ? p.pos[at] : first + i;
+    on = on && sees(ps, qp, lo, p.sinks);
+    if (on) {
+      float z[GP];
+      const float* src = p.z + at * GP;
+      if constexpr (GP == 1) {
+        z[0] = __ldcg(src);
+      } else if constexpr (GP == 2) {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+        z[0] = x.x;
+        z[1] = x.y;
+      } else {
+#pragma unroll
+        for (int k = 0; k < GP / 4; ++k) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(src) + k);
+          z[4 * k] = x.x;
+          z[4 * k + 1] = x.y;
+          z[4 * k + 2] = x.z;
+          z[4 * k + 3] = x.w;
+        }
+      }
+      float w = 0.f;
+#pragma unroll
+      for (int r = 0; r < GP; ++r)
+        if (r < p.R) w += ex2(fmaf(z[r], p.scale_log2, -ls[r]));
+      a += w;
+    }
+    p.acc_out[at] = a;
+  }
+}
+__device__ __forceinline__ void weights_any(const AttendParams& p, int64_t base, int first,
+                                            int64_t qpos, const float* lse2, int i0, int i1) {
+  switch (p.gp) {
+    case 1: weights_from_logits<1>(p, base, first, qpos, lse2, i0, i1); break;
+    case 2: weights_from_logits<2>(p, base, first, qpos, lse2, i0, i1); break;
+    case 4: weights_from_logits<4>(p, base, first, qpos, lse2, i0, i1); break;
+    default: weights_from_logits<8>(p, base, first, qpos, lse2, i0, i1); break;
+  }
+}
+
 // NB: query rows / 8 of this launch (1, 2 or 4).
 template <int NB, int kMode>
 __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParams p) {
@@ -156,6 +266,8 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
   __shared__ AtWarpShared wsh[kAtWarps];
   __shared__ int s_qp[32];
   __shared__ float s_ml[kAtWarps][2][32];
+  __shared__ float s_lse2[32];
+  __shared__ int s_last;
   const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
   const int g = lane >> 2, q = lane & 3;
   AtWarpShared& ws = wsh[wp];
@@ -387,6 +499,19 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
           if (r0 < p.R) continue;
           break;
         } else {
+          if constexpr (NB == 1 && kMode == kOwn) {
+            if (p.z && 2 * q < p.gp) {   // logits for the weights, before masks and scaling
+              float* z0 = p.z + (base + ws.mslot[s][g]) * p.gp + 2 * q;
+              float* z1 = p.z + (base + ws.mslot[s][g + 8]) * p.gp + 2 * q;
+              if (p.gp == 1) {
+                if (in0) *z0 = c[0][0];
+                if (in1) *z1 = c[0][2];
+              } else {
+                if (in0) __stcg(reinterpret_cast<float2*>(z0), make_float2(c[0][0], c[0][1]));
+                if (in1) __stcg(reinterpret_cast<float2*>(z1), make_float2(c[0][2], c[0][3]));
+              }
+            }
+          }
           uint32_t bh[NB][2], bl[NB][2];
           float mref[NB][2];
           bool grew = false;
@@ -591,43 +716,65 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
             kMode == kPrefix
                 ? static_cast<int64_t>(chunk) * p.rows + row
                 : (static_cast<int64_t>(item) * p.maxch + chunk) * p.R + row0 + r;
-        *reinterpret_cast<float4*>(p.part_o + at * 128 + 4 * d4) = o;
-        if (d4 == 0) p.part_ml[at] = make_float2(M, L);
+        __stcg(reinterpret_cast<float4*>(p.part_o + at * 128 + 4 * d4), o);
+        if (d4 == 0) __stcg(&p.part_ml[at], make_float2(M, L));
       } else {
         attend_store(p, row, d4, M, L, o);
+        if (d4 == 0) s_lse2[r] = L == 0.f ? INFINITY : M + log2f(L);
+      }
+    }
+    if constexpr (kMode == kOwn) {
+      if (p.count) {
+        // the CTA that finishes a unit's rows last joins its parts
+        __threadfence();
+        __syncthreads();
+        int* cnt = p.count + static_cast<int64_t>(item) * gridDim.y + blockIdx.y;
+        if (tid == 0) s_last = atomicAdd(cnt, 1) == p.maxch - 1;
+        __syncthreads();
+        if (!s_last) return;
+        __threadfence();
+        if (tid == 0) *cnt = 0;   // ready for the next call
+        const int64_t at0 = static_cast<int64_t>(item) * p.maxch * p.R + row0;
+        for (int r = wp; r < nrow; r += kAtWarps)
+          join_row(p, row_of(r), p.maxch, [&](int c, float2& ml, const float4*& src) {
+            const int64_t at = at0 + static_cast<int64_t>(c) * p.R + r;
+            ml = __ldcg(&p.part_ml[at]);
+            src = reinterpret_cast<const float4*>(p.part_o + at * 128);
+          });
+      } else if (NB == 1 && p.z && !p.part_o) {
+        __syncthreads();   // all logits of the unit are written
+        weights_any(p, base, first, qmax, s_lse2, 0, N);
       }
     }
   }
 }
 
-// Joins the parts of every query row, one warp per row, in a fixed order: the
+// The weights pass from stored logits: chunks of gpc groups of one unit per CTA.
+__global__ void __launch_bounds__(256) weights_kernel(const AttendParams p) {
+  const int item = blockIdx.x / p.maxch, chunk = blockIdx.x - item * p.maxch;
+  const int64_t base = __ldg(&p.tok_off[item]);
+  const int N = static_cast<int>(__ldg(&p.tok_off[item + 1]) - base);
+  const int64_t i0 = static_cast<int64_t>(chunk) * p.gpc * 32;
+  if (i0 >= N) return;
+  weights_any(p, base, prefix_len(p, item), newest_query(p, item),
+              p.lse2 + static_cast<int64_t>(item) * p.R, static_cast<int>(i0),
+              static_cast<int>(min(static_cast<int64_t>(N), i0 + static_cast<int64_t>(p.gpc) * 32)));
+}
+
+// Joins the parts of every query row of a shared call, one warp per row: the
 // prefix's chunks, then the unit's own.
-__global__ void __launch_bounds__(256) join_kernel(const AttendParams p, const JoinParams j) {
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(128) join_kernel(const AttendParams p, const JoinParams j) {
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   if (row >= j.rows) return;
   const int u = static_cast<int>(row / p.R), r = static_cast<int>(row - static_cast<int64_t>(u) * p.R);
-  const bool pre = p.unit_prefix && __ldg(&p.unit_prefix[u]) >= 0;
-  const int np = pre ? j.pre_chunks : 0;
-  float M = -INFINITY, L = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = 0; c < np + j.own_chunks; ++c) {
+  const int np = __ldg(&p.unit_prefix[u]) >= 0 ? j.pre_chunks : 0;
+  join_row(p, row, np + j.own_chunks, [&](int c, float2& ml, const float4*& src) {
     const bool own = c >= np;
     const int64_t at = own ? (static_cast<int64_t>(u) * j.own_chunks + (c - np)) * p.R + r
                            : static_cast<int64_t>(c) * j.rows + row;
-    const float2 ml = own ? j.own_ml[at] : j.pre_ml[at];
-    if (ml.x == -INFINITY && ml.y == 0.f) continue;   // nothing visible there
-    const float4 x = *reinterpret_cast<const float4*>((own ? j.own_o : j.pre_o) + at * 128 + 4 * lane);
-    const float N = fmaxf(M, ml.x);
-    const float f = M == N ? 1.f : ex2(M - N), h = ml.x == N ? 1.f : ex2(ml.x - N);
-    M = N;
-    L = L * f + ml.y * h;
-    o.x = o.x * f + x.x * h;
-    o.y = o.y * f + x.y * h;
-    o.z = o.z * f + x.z * h;
-    o.w = o.w * f + x.w * h;
-  }
-  attend_store(p, row, lane, M, L, o);
+    ml = own ? j.own_ml[at] : j.pre_ml[at];
+    src = reinterpret_cast<const float4*>((own ? j.own_o : j.pre_o) + at * 128);
+  });
 }
 
 template <int NB, int kMode>
@@ -682,12 +829,16 @@ cudaError_t launch_attend_prefix(const AttendParams& p, int P, int max_rows, cud
 }
 
 cudaError_t launch_attend_join(const AttendParams& p, const JoinParams& j, cudaStream_t st) {
-  join_kernel<<<static_cast<unsigned>((j.rows + 7) / 8), 256, 0, st>>>(p, j);
+  join_kernel<<<static_cast<unsigned>((j.rows + 3) / 4), 128, 0, st>>>(p, j);
   return cudaGetLastError();
 }
 
 cudaError_t launch_attend_weights(const AttendParams& p, int U, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(U) * p.maxch, 1);
+  if (p.z) {
+    weights_kernel<<<grid, 256, 0, st>>>(p);
+    return cudaGetLastError();
+  }
   return launch_mode<kWeights>(p, p.R, grid, st);
 }
 

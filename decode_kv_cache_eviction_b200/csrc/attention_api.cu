@@ -55,28 +55,45 @@ int check_rows(const rkv_engine* e, const rkv_batch* b, Lengths* L) {
   return RKV_OK;
 }
 
-// Rows of query parts that the scratch of unsplit-prefix calls holds: eight
-// full waves of 32-row CTAs.
-constexpr int64_t kPartRows = 75776;
-constexpr int64_t kPartFloats = 130;   // 128 values, maximum and sum
+constexpr int64_t kPartFloats = 130;   // a part: 128 values, maximum and sum
 
-int64_t shared_rows(const rkv_engine* e) {
-  return std::max<int64_t>(2ll * e->cfg.max_units * e->cfg.group * e->cfg.window, kPartRows);
+// Query rows whose parts the scratch holds: eight waves of CTAs (two per SM)
+// of at most 32 rows; shared calls hold two parts of every query row at least.
+int64_t part_rows(const rkv_engine* e, bool shared) {
+  const int64_t all = static_cast<int64_t>(e->cfg.group) * e->cfg.window;
+  const int64_t split = 16ll * e->nsm * std::min<int64_t>(all, 32);
+  return shared ? std::max<int64_t>(2 * e->cfg.max_units * all, split) : split;
+}
+// Counters of split units: one per unit and 32 query rows.
+int64_t part_counts(const rkv_engine* e) {
+  return static_cast<int64_t>(e->cfg.max_units) * ((e->cfg.group * e->cfg.window + 31) / 32);
 }
 
-// Scratch of the attention calls, allocated once: `rows` parts, then the
-// rows' log2 sums.  Not while a stream is captured.
-int attend_scratch(rkv_engine* e, float** buf, int64_t rows, cudaStream_t st) {
-  if (*buf) return RKV_OK;
+// Scratch of the attention calls, allocated once: `rows` parts, the rows' log2
+// sums and the counters (zero between calls).  Not while a stream is captured.
+int attend_scratch(rkv_engine* e, float** buf, int64_t rows, bool logits, cudaStream_t st) {
+  if (*buf && (e->rf_z || !logits)) return RKV_OK;
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(st, &cs) != cudaSuccess) return cuda_fail(cudaErrorUnknown);
   if (cs != cudaStreamCaptureStatusNone) return RKV_ERR_INVALID_ARG;
-  const size_t n = static_cast<size_t>(rows) * kPartFloats +
-                   static_cast<size_t>(e->cfg.max_units) * e->cfg.group * e->cfg.window;
-  if (rkv_engine_alloc(e, reinterpret_cast<void**>(buf), n * sizeof(float)) != cudaSuccess) {
+  if (logits) {
+    const int rc = rkv_logit_scratch(e);
+    if (rc != RKV_OK) return rc;
+  }
+  if (*buf) return RKV_OK;
+  const size_t sums = static_cast<size_t>(rows) * kPartFloats +
+                      static_cast<size_t>(e->cfg.max_units) * e->cfg.group * e->cfg.window;
+  const size_t counts = static_cast<size_t>(part_counts(e));
+  if (rkv_engine_alloc(e, reinterpret_cast<void**>(buf), (sums + counts) * sizeof(float)) !=
+      cudaSuccess) {
     cudaGetLastError();
     *buf = nullptr;
     return RKV_ERR_OOM;
+  }
+  if (cudaMemsetAsync(*buf + sums, 0, counts * sizeof(int), st) != cudaSuccess) {
+    cudaFree(*buf);
+    *buf = nullptr;
+    return cuda_fail(cudaErrorUnknown);
   }
   return RKV_OK;
 }
@@ -182,12 +199,13 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
   DeviceGuard dev(e->device);
   if (!dev.ok) return cuda_fail(cudaErrorUnknown);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int64_t cap = x ? shared_rows(e) : kPartRows;
+  const int64_t cap = part_rows(e, x != nullptr);
   float** buf = x ? &e->at_shared : &e->at_part;
-  rc = attend_scratch(e, buf, cap, st);
-  if (rc != RKV_OK) return rc;
-
   const int R = e->cfg.group * a->num_queries;
+  // weights from stored logits: a row's logits are then all or none visible
+  const bool logits = a->acc_out && a->num_queries == 1 && R <= 8;
+  rc = attend_scratch(e, buf, cap, logits, st);
+  if (rc != RKV_OK) return rc;
   const int64_t rows = static_cast<int64_t>(U) * R;
   const int rg = (R + 31) / 32;
   AttendParams p = {};
@@ -209,7 +227,15 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
   float* part_o = *buf;
   float2* part_ml = reinterpret_cast<float2*>(part_o + cap * 128);
   float* lse2 = reinterpret_cast<float*>(part_ml + cap);
+  int* count = reinterpret_cast<int*>(
+      lse2 + static_cast<int64_t>(e->cfg.max_units) * e->cfg.group * e->cfg.window);
   p.lse2 = a->acc_out ? lse2 : nullptr;
+  p.acc_in = a->acc_in;
+  p.acc_out = a->acc_out;
+  if (logits) {
+    p.z = e->rf_z;
+    p.gp = refree_padded_group(e->cfg.group);
+  }
   if (x) {
     p.unit_prefix = x->unit_prefix;
     p.pre_off = x->off;
@@ -232,10 +258,11 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
   p.maxch = own;
   p.gpc = static_cast<int>((gmax + own - 1) / own);
   JoinParams j = {};
-  const bool join = x || own > 1;
+  const bool join = x || own > 1;   // rows have several parts
   if (join) {
     p.part_o = part_o;
     p.part_ml = part_ml;
+    p.count = x ? nullptr : count;
     j.rows = rows;
     j.own_chunks = own;
     j.own_o = part_o;
@@ -275,17 +302,15 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     if (err != cudaSuccess) return cuda_fail(err);
     ++e->launches;
   }
-  if (join) {
+  if (x) {
     t_begin(e, RKV_KERNEL_JOIN, st);
     err = launch_attend_join(p, j, st);
     t_end(e, st);
     if (err != cudaSuccess) return cuda_fail(err);
     ++e->launches;
   }
-  if (a->acc_out) {
+  if (a->acc_out && (join || !p.z)) {   // a unit of one chunk has done its weights
     AttendParams pw = p;
-    pw.acc_in = a->acc_in;
-    pw.acc_out = a->acc_out;
     const int64_t all = (static_cast<int64_t>(L.nmax) + 31) / 32;
     pw.maxch = pick_chunks(U, (L.T + 31) / 32 + U, std::max<int64_t>(all, 1), 2 * e->nsm,
                            std::max<int64_t>(1, (static_cast<int64_t>(1) << 30) / U));
@@ -355,9 +380,11 @@ int rkv_evict_accumulated(rkv_engine* e, const rkv_batch* b, const float* acc,
   p.acc_out = acc_out;
   p.idx = idx;
   p.n_kept = n_kept;
+  p.vec = aligned(acc, 16) && aligned(acc_out, 16) && aligned(pos, 16) && aligned(live, 4) &&
+          aligned(keep, 4);
   p.status = e->status;
   t_begin(e, RKV_KERNEL_DROP, st);
-  cudaError_t err = launch_drop(p, U, L.nmax, st);
+  cudaError_t err = launch_drop(p, U, L.nmax, e->nsm, st);
   t_end(e, st);
   if (err != cudaSuccess) return cuda_fail(err);
   ++e->launches;

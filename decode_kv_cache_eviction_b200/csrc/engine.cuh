@@ -105,6 +105,10 @@ inline void t_end(rkv_engine* e, cudaStream_t st) {
 // Frees everything rkv_compress_host allocated (called by rkv_destroy).
 void rkv_host_pipeline_free(rkv_engine* e);
 
+// The logit scratch of rkv_refree_budget and of the attention weights (rf_z:
+// max_tokens x padded G floats first), allocated by the first call that needs it.
+int rkv_logit_scratch(rkv_engine* e);
+
 // cudaMalloc for the engine's lazily grown buffers; fails (once) when an
 // allocation fault has been armed with rkv_inject_fault.
 cudaError_t rkv_engine_alloc(rkv_engine* e, void** p, size_t bytes);

@@ -319,6 +319,9 @@ struct AttendParams {
   float* acc_out;                // [T] or null
   float* part_o;                 // parts [.., 128], null: the chunk is the whole row
   float2* part_ml;               // parts' (maximum in log2 units, sum)
+  int* count;                    // [U * row groups] arrived chunks (0 between calls), or null
+  float* z;                      // [T, gp] logits for the weights, or null
+  int gp;                        // heads of a row of z: R rounded up to a power of two
   // shared prefixes
   int64_t rows;                  // U * R
   const int32_t* unit_prefix;    // [U] or null
@@ -356,9 +359,9 @@ struct DropParams {
   float* acc_out;                // [T] or null
   int32_t* idx;                  // [U, W] or null
   int32_t* n_kept;               // [U] or null
+  bool vec;                      // the arrays are aligned for vectors of four rows
   int* status;
 };
-cudaError_t drop_configure();
-cudaError_t launch_drop(const DropParams& p, int U, int nmax, cudaStream_t st);
+cudaError_t launch_drop(const DropParams& p, int U, int nmax, int nsm, cudaStream_t st);
 
 }  // namespace rkv
