@@ -20,18 +20,6 @@ size_t round_up(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 constexpr int kSmemCap = 227 * 1024;
 
-int make_map(rkv_engine* e, CUtensorMap* m, const void* ptr, uint64_t rows, uint32_t box_rows) {
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(kHeadDim) * 2};
-  cuuint32_t box[2] = {64, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = e->encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims,
-                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? RKV_OK : RKV_ERR_CUDA;
-}
-
 // Host-side checks of a batch against the engine; fills T and the largest N.
 int check_batch(const rkv_engine* e, const rkv_batch* b, int64_t* T, int* nmax, int* cmax) {
   if (!b) return RKV_ERR_INVALID_ARG;
@@ -211,7 +199,7 @@ int rkv_create(const rkv_config* cfg, rkv_engine** out) {
   e->max_chunks = score_max_chunks(cfg->max_tokens, cfg->max_units, e->score_ctas, e->rp);
 
   if (select_configure() != cudaSuccess || inplace_configure() != cudaSuccess ||
-      attend_configure() != cudaSuccess) {
+      attend_configure() != cudaSuccess || wide_configure() != cudaSuccess) {
     delete e;
     return cuda_fail(cudaErrorUnknown);
   }

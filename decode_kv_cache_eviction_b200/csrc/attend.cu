@@ -19,11 +19,7 @@
 // stage into its own shared-memory ring with cp.async.  Rows that no query
 // sees are never read, and missing rows of the last stage are zero-filled.
 // Only __syncwarp and cp.async.wait_group order the ring.
-#include <cuda_bf16.h>
-#include <limits.h>
-
-#include "ptx.cuh"
-#include "rkv_internal.cuh"
+#include "attend_common.cuh"
 
 namespace rkv {
 namespace {
@@ -86,78 +82,25 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ bool finite(float x) {
-  return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u;
-}
-__device__ __forceinline__ int clamp32(int64_t x) {
-  return x > INT_MAX ? INT_MAX : x < INT_MIN ? INT_MIN : static_cast<int>(x);
-}
-
-// A unit's prefix length (0 without one) and the position of its newest query.
-__device__ __forceinline__ int prefix_len(const AttendParams& p, int u) {
-  if (!p.unit_prefix) return 0;
-  const int x = __ldg(&p.unit_prefix[u]);
-  return x < 0 ? 0 : static_cast<int>(__ldg(&p.pre_off[x + 1]) - __ldg(&p.pre_off[x]));
-}
-__device__ __forceinline__ int64_t newest_query(const AttendParams& p, int u) {
-  if (p.q_pos) return __ldg(&p.q_pos[u]);
-  return prefix_len(p, u) + (__ldg(&p.tok_off[u + 1]) - __ldg(&p.tok_off[u])) - 1;
-}
-__device__ __forceinline__ bool sees(int pos, int qp, int lo, int sinks) {
-  return pos <= qp && (pos > lo || pos < sinks);
-}
-
-// The 32-row groups that can hold visible rows when row i sits at position
-// first + i: the sinks' groups [0, gs), then [start, start + nv - gs).
-struct Span {
-  int gs, start, nv;
+// A query row's state: maximum, sum and this lane's four dimensions.
+struct RowSum {
+  float M, L;
+  float4 o;
 };
-__device__ __forceinline__ Span visible_span(int n, int first, int64_t qmin, int64_t qmax,
-                                             int local, int sinks) {
-  Span s = {0, 0, 0};
-  const int64_t hi = min(static_cast<int64_t>(n), qmax - first + 1);   // rows past hi are later
-  if (hi <= 0) return s;
-  const int gh = static_cast<int>((hi + 31) >> 5);
-  if (local > 0) {
-    const int64_t ns = min(hi, max(static_cast<int64_t>(sinks) - first, static_cast<int64_t>(0)));
-    const int64_t lo = max(static_cast<int64_t>(0), qmin - local + 1 - first);
-    s.gs = static_cast<int>((ns + 31) >> 5);
-    s.start = max(s.gs, static_cast<int>(min(lo, hi) >> 5));
-  }
-  s.nv = s.gs + max(0, gh - s.start);
-  return s;
+__device__ __forceinline__ RowSum no_rows() {
+  return {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
 }
 
-// Writes four dimensions of a finished row: out = o / L (0 for a row that saw
-// nothing), and from the row's first lane its log-sum-exp.  log2(L) + M is the
-// sum's logarithm to base 2; a row without weight gets +inf in lse2, so that the
-// weights pass gives it p = 0.
-__device__ __forceinline__ void attend_store(const AttendParams& p, int64_t row, int d4, float M,
-                                             float L, float4 o) {
-  const bool none = L == 0.f;
-  const float f = none ? 0.f : 1.f / L;
-  if (none) o = make_float4(0.f, 0.f, 0.f, 0.f);
-  p.out[row * 32 + d4] = make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
-  if (d4 == 0) {
-    const float s = M + log2f(L);
-    if (p.lse) p.lse[row] = none ? -INFINITY : s * 0.6931471805599453f;
-    if (p.lse2) p.lse2[row] = none ? INFINITY : s;
-  }
-}
-
-// Joins the n parts of one query row and writes it, one warp: lane 4-dimension
-// groups, parts in order.  Part c is at index at(c) of o / ml.  The parts' (maximum,
+// Joins the n parts of one query row to `s` and writes it, one warp: lane = four
+// dimensions, parts in order.  Part c is at index at(c) of o / ml.  The parts' (maximum,
 // sum) pairs of 32 parts are loaded at once, one per lane, and four parts' values
 // are in flight.
 template <class At>
-__device__ __forceinline__ void join_row(const AttendParams& p, int64_t row, int n, At at) {
+__device__ __forceinline__ void join_row(const AttendParams& p, int64_t row, RowSum s, int n,
+                                         At at) {
   const int lane = threadIdx.x & 31;
-  float M = -INFINITY, L = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float M = s.M, L = s.L;
+  float4 o = s.o;
   for (int c0 = 0; c0 < n; c0 += 32) {
     float2 ml = make_float2(-INFINITY, 0.f);
     const float4* src = nullptr;
@@ -333,7 +276,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
     sp.gs = sp.start = 0;
     sp.nv = (N + 31) >> 5;
   } else {
-    sp = visible_span(N, first, qmin, qmax, p.local, p.sinks);
+    sp = visible_span<5>(N, first, qmin, qmax, p.local, p.sinks);
   }
   const int v_end = min(sp.nv, (chunk + 1) * p.gpc);
   const uint8_t* keep = kMode == kPrefix ? nullptr : p.keep;
@@ -400,8 +343,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
     int head = 0, cnt = 0;        // list: first entry, entries
     // rows of group v (virtual order: sinks' groups, then the window's)
     auto scan = [&]() {
-      const int grp = v < sp.gs ? v : sp.start + (v - sp.gs);
-      const int slot = 32 * grp + lane;
+      const int slot = 32 * sp.group(v) + lane;
       bool on = slot < N;
       int ps = first + slot;
       if (on && keep) on = __ldg(&keep[base + slot]) != 0;
@@ -736,7 +678,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
         if (tid == 0) *cnt = 0;   // ready for the next call
         const int64_t at0 = static_cast<int64_t>(item) * p.maxch * p.R + row0;
         for (int r = wp; r < nrow; r += kAtWarps)
-          join_row(p, row_of(r), p.maxch, [&](int c, float2& ml, const float4*& src) {
+          join_row(p, row_of(r), no_rows(), p.maxch, [&](int c, float2& ml, const float4*& src) {
             const int64_t at = at0 + static_cast<int64_t>(c) * p.R + r;
             ml = __ldcg(&p.part_ml[at]);
             src = reinterpret_cast<const float4*>(p.part_o + at * 128);
@@ -761,14 +703,55 @@ __global__ void __launch_bounds__(256) weights_kernel(const AttendParams p) {
               static_cast<int>(min(static_cast<int64_t>(N), i0 + static_cast<int64_t>(p.gpc) * 32)));
 }
 
+// A query row against its whole prefix, one warp, row by row: for rows whose
+// product met a value that is not finite, which need not be one that they see.
+__device__ __noinline__ RowSum prefix_row(const AttendParams& p, int64_t row, int u, int r) {
+  const int lane = threadIdx.x & 31;
+  const int x = p.unit_prefix[u];
+  const int64_t base = p.pre_off[x];
+  const int N = static_cast<int>(p.pre_off[x + 1] - base);
+  const int qp = clamp32(newest_query(p, u) - (p.nq - 1) + r % p.nq);
+  const int lo = p.local > 0 ? clamp32(static_cast<int64_t>(qp) - p.local) : INT_MIN;
+  auto four = [&](const uint32_t* src) {
+    const uint2 w = *reinterpret_cast<const uint2*>(src + 2 * lane);
+    return make_float4(bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y));
+  };
+  const float4 q = four(p.Q + row * 64);
+  RowSum s = no_rows();
+  for (int i = 0; i < N; ++i) {
+    if (!sees(i, qp, lo, p.sinks)) continue;
+    const float4 k = four(reinterpret_cast<const uint32_t*>(p.PK + (base + i) * 16));
+    const float4 v = four(reinterpret_cast<const uint32_t*>(p.PV + (base + i) * 16));
+    const float z = p.scale_log2 * warp_reduce_sum(q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w);
+    const float M = fmaxf(s.M, z);
+    const float f = s.M == M ? 1.f : ex2(s.M - M);
+    const float w = ex2(z - (M == -INFINITY ? 0.f : M));
+    s.M = M;
+    s.L = s.L * f + w;
+    s.o.x = s.o.x * f + w * v.x;
+    s.o.y = s.o.y * f + w * v.y;
+    s.o.z = s.o.z * f + w * v.z;
+    s.o.w = s.o.w * f + w * v.w;
+  }
+  return s;
+}
+
 // Joins the parts of every query row of a shared call, one warp per row: the
 // prefix's chunks, then the unit's own.
 __global__ void __launch_bounds__(128) join_kernel(const AttendParams p, const JoinParams j) {
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   if (row >= j.rows) return;
   const int u = static_cast<int>(row / p.R), r = static_cast<int>(row - static_cast<int64_t>(u) * p.R);
-  const int np = __ldg(&p.unit_prefix[u]) >= 0 ? j.pre_chunks : 0;
-  join_row(p, row, np + j.own_chunks, [&](int c, float2& ml, const float4*& src) {
+  int np = __ldg(&p.unit_prefix[u]) >= 0 ? j.pre_chunks : 0;
+  RowSum s = no_rows();
+  bool redo = false;
+  for (int c = threadIdx.x & 31; c < np; c += 32)
+    redo |= j.pre_ml[static_cast<int64_t>(c) * j.rows + row].y == kRedo;
+  if (__any_sync(0xffffffffu, redo)) {
+    s = prefix_row(p, row, u, r);
+    np = 0;
+  }
+  join_row(p, row, s, np + j.own_chunks, [&](int c, float2& ml, const float4*& src) {
     const bool own = c >= np;
     const int64_t at = own ? (static_cast<int64_t>(u) * j.own_chunks + (c - np)) * p.R + r
                            : static_cast<int64_t>(c) * j.rows + row;

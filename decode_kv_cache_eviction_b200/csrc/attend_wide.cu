@@ -1,0 +1,379 @@
+// Attention of many query rows over a shared prefix: all queries of a prefix's
+// units against its K and V at once, on the tensor cores.
+//
+// A CTA takes 128 or 256 query rows (one or two tiles of 128, gathered from their
+// units) and a run of 128-token tiles of the prefix:
+//   S = Q K^T        tcgen05.mma, Q and K from shared memory (128-byte swizzle),
+//                    S in tensor memory: lane = query row, column = token;
+//   p = 2^(S - m)    one thread per query row: no exchange between threads for the
+//                    maximum and the sum; p goes back over S as bf16;
+//   O += p V         tcgen05.mma with p as the A operand from tensor memory and V
+//                    (token rows) as an MN-major B operand: V is never transposed.
+// With two query tiles their steps alternate, S0 PV0 S1 PV1, so that the tensor
+// cores work on one tile while the other's p is formed, and each K/V tile in shared
+// memory serves 256 query rows.  The MMAs of one thread run in the order of their
+// issue; S of the next token tile, written over p, therefore follows the product
+// that reads p.
+//
+// The running maximum m is moved (and O, l rescaled by the same thread) only when
+// a row's maximum has grown by more than 2^8: p, l and O stay well inside fp32 and
+// bf16's relative precision does not depend on the scale, so the result is the
+// same and most tiles need no pass over O.
+//
+// p is rounded to bf16 (2^-9 relative, once per weight, of random sign): the
+// product needs V's type, and a second part would cost half as many MMAs again.
+//
+// Bound: at 256 rows and d = 128 a token tile takes 2048 tensor-core cycles and as
+// many for its 2^x (16 per cycle and SM).
+//
+// Roles: warp 0 TMA producer, warp 1 MMA issuer (one lane each), warps 4-7 and
+// 8-11 the rows of the first and second query tile.  Every wait is bounded.
+//
+// A row whose result is not finite is marked and computed again, token by token,
+// by the join: a value that is not finite in a row that it does not see (behind its
+// window, after the prefix's end) also meets its p = 0 in the product.
+#include "attend_common.cuh"
+
+namespace rkv {
+namespace {
+
+constexpr int kWTile = kWideTile;
+constexpr uint32_t kTileB = kWTile * 256;   // a K, V or Q tile: two halves of 64 columns
+constexpr uint32_t kHalfB = kTileB / 2;
+constexpr uint64_t kDrainNs = 100000000ull;
+constexpr float kSlack = 8.f;   // growth of a maximum (log2) that O is not rescaled for
+
+template <int QT>
+struct WideLayout {
+  static constexpr int kStages = QT == 2 ? 5 : 6;   // K and V tiles in turn
+  static constexpr uint32_t q = 0;
+  static constexpr uint32_t ring = QT * kTileB;
+  static constexpr uint32_t qp = ring + kStages * kTileB;      // [QT * 128]
+  static constexpr uint32_t bars = qp + QT * kWTile * 4;
+  static constexpr uint32_t misc = bars + (2 * kStages + 3 * 2 + 1) * 8;
+  static constexpr uint32_t total = misc + 48;
+  static constexpr uint32_t alloc = total + 1024;               // base aligned to 1024
+};
+
+// Teardown: wait (bounded, regardless of an abort) for a phase that is under way.
+__device__ __forceinline__ void wide_drain(uint64_t* bar, uint32_t par) {
+  const uint32_t a = smem_u32(bar);
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(a, par))
+    if (globaltimer_ns() - t0 > kDrainNs) return;
+}
+
+template <int QT>
+__global__ void __launch_bounds__(128 + 128 * QT, 1)
+    wide_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                const AttendParams p) {
+  using Lay = WideLayout<QT>;
+  constexpr int NS = Lay::kStages;
+  constexpr int kThreads = 128 + 128 * QT;
+  extern __shared__ uint8_t wide_raw[];
+  uint8_t* sm = wide_raw + ((1024u - (smem_u32(wide_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + Lay::bars);
+  uint64_t* empty = full + NS;
+  uint64_t* s_full = empty + NS;    // [2] S of a query tile is in tensor memory
+  uint64_t* p_full = s_full + 2;    // [2] its p is
+  uint64_t* o_done = p_full + 2;    // [2] its product with V is done
+  uint64_t* mdone = o_done + 2;     // teardown: every MMA has completed
+  int* s_qp = reinterpret_cast<int*>(sm + Lay::qp);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Lay::misc);
+  volatile int* abort = reinterpret_cast<volatile int*>(sm + Lay::misc + 4);
+  int* s_lim = reinterpret_cast<int*>(sm + Lay::misc + 8);            // smallest, largest qp
+  int8_t* lastp = reinterpret_cast<int8_t*>(sm + Lay::misc + 16);     // [NS] parity of the last copy
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  const int item = blockIdx.x / p.maxch, chunk = blockIdx.x - item * p.maxch;
+  const int row0 = blockIdx.y * QT * kWTile;
+  const int64_t base = __ldg(&p.pre_off[item]);
+  const int N = static_cast<int>(__ldg(&p.pre_off[item + 1]) - base);
+  const int mo = __ldg(&p.mem_off[item]);
+  const int total = (__ldg(&p.mem_off[item + 1]) - mo) * p.R;
+  if (row0 >= total) return;
+  const int nrow = min(QT * kWTile, total - row0);
+  auto row_of = [&](int r) -> int64_t {
+    const int m = (row0 + r) / p.R;
+    return static_cast<int64_t>(__ldg(&p.mem[mo + m])) * p.R + (row0 + r - m * p.R);
+  };
+
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      lastp[s] = -1;
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&o_done[i], 1);
+    }
+    mbar_init(mdone, 1);
+    *abort = 0;
+    s_lim[0] = INT_MAX;
+    s_lim[1] = INT_MIN;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  for (int r = tid; r < QT * kWTile; r += kThreads) {
+    int v = INT_MIN;
+    if (r < nrow) {
+      const int64_t rr = row_of(r);
+      const int u = static_cast<int>(rr / p.R);
+      const int t = static_cast<int>(rr - static_cast<int64_t>(u) * p.R) % p.nq;
+      v = clamp32(newest_query(p, u) - (p.nq - 1) + t);
+      atomicMin(&s_lim[0], v);
+      atomicMax(&s_lim[1], v);
+    }
+    s_qp[r] = v;
+  }
+  __syncthreads();
+  const int qmin = s_lim[0], qmax = s_lim[1];
+  const Span sp = visible_span<7>(N, 0, qmin, qmax, p.local, p.sinks);
+  const int v0 = chunk * p.gpc, nt = min(sp.nv, v0 + p.gpc) - v0;   // token tiles of this CTA
+  if (nt <= 0) {
+    for (int r = tid; r < nrow; r += kThreads)
+      p.part_ml[static_cast<int64_t>(chunk) * p.rows + row_of(r)] = make_float2(-INFINITY, 0.f);
+    return;
+  }
+  // query rows into the layout that TMA writes for K (zeros past the last row)
+  for (int i = tid; i < QT * kWTile * 16; i += kThreads) {
+    const int r = i >> 4, c = i & 15;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (r < nrow) x = __ldg(reinterpret_cast<const uint4*>(p.Q) + row_of(r) * 16 + c);
+    const int rt = r & (kWTile - 1);
+    *reinterpret_cast<uint4*>(sm + Lay::q + (r / kWTile) * kTileB + (c >> 3) * kHalfB + rt * 128 +
+                              (((c & 7) ^ (rt & 7)) << 4)) = x;
+  }
+  fence_proxy_async_smem();
+  if (warp == 1) {
+    tmem_alloc<1>(tmem_slot, 512);
+    tmem_relinquish<1>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;   // S0, S1, O0, O1: 128 columns each
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      prefetch_tmap(&kmap);
+      prefetch_tmap(&vmap);
+      const uint64_t pol = policy_evict_normal();
+      for (int i = 0; i < 2 * nt; ++i) {
+        const int s = i % NS;
+        const uint32_t ph = (i / NS) & 1;
+        if (!mbar_wait(&empty[s], ph ^ 1, abort, p.status)) break;
+        uint8_t* dst = sm + Lay::ring + s * kTileB;
+        const int y = static_cast<int>(base + static_cast<int64_t>(sp.group(v0 + i / 2)) * kWTile);
+        const CUtensorMap* map = (i & 1) ? &vmap : &kmap;
+        mbar_arrive_expect_tx(&full[s], kTileB);
+        tma_load_2d(dst, map, &full[s], 0, y, pol);
+        tma_load_2d(dst + kHalfB, map, &full[s], 64, y, pol);
+        lastp[s] = static_cast<int8_t>(ph);
+      }
+      // teardown: every copy issued has landed before the CTA exits
+      for (int s = 0; s < NS; ++s)
+        if (lastp[s] >= 0) wide_drain(&full[s], lastp[s]);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint32_t id_s = idesc_bf16_f32(128, 128);
+      const uint32_t id_o = idesc_bf16_f32(128, 128) | kIdescTransposeB;
+      auto slot = [&](int i) { return smem_u32(sm + Lay::ring + (i % NS) * kTileB); };
+      auto wait_tile = [&](int i) {
+        return mbar_wait(&full[i % NS], (i / NS) & 1, abort, p.status);
+      };
+      auto scores = [&](int t, int j) {   // S_t = Q_t K_j^T
+        const uint32_t qa = smem_u32(sm + Lay::q + t * kTileB), ka = slot(2 * j);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t o = (k >> 2) * kHalfB + (k & 3) * 32;
+          mma_bf16<1>(tmem + t * 128, desc_kmajor_sw128(qa + o), desc_kmajor_sw128(ka + o), id_s,
+                      k > 0);
+        }
+        mma_commit(&s_full[t]);
+      };
+      auto product = [&](int t, int j) {   // O_t += p_t V_j
+        const uint32_t va = slot(2 * j + 1);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * k,
+                      desc_mnmajor_sw128(va + k * 2048, kHalfB), id_o, j > 0 || k > 0);
+        mma_commit(&o_done[t]);
+      };
+      bool ok = wait_tile(0);
+      tc_fence_after();
+      if (ok) {
+        for (int t = 0; t < QT; ++t) scores(t, 0);
+        mma_commit(&empty[0]);
+      }
+      for (int j = 0; ok && j < nt; ++j) {
+        ok = wait_tile(2 * j + 1);
+        const bool more = j + 1 < nt;
+        for (int t = 0; ok && t < QT; ++t) {
+          ok = mbar_wait(&p_full[t], j & 1, abort, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          product(t, j);
+          if (t == QT - 1) mma_commit(&empty[(2 * j + 1) % NS]);
+          if (more) {
+            if (t == 0) ok = wait_tile(2 * j + 2);
+            if (!ok) break;
+            tc_fence_after();
+            scores(t, j + 1);
+            if (t == QT - 1) mma_commit(&empty[(2 * j + 2) % NS]);
+          }
+        }
+      }
+      // teardown: all MMAs (and their commits) are complete before TMEM is freed
+      mma_commit(mdone);
+      wide_drain(mdone, 0);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ rows
+    const int t = (warp - 4) >> 2;               // query tile
+    const int r = t * kWTile + (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
+    const int qp = s_qp[r];
+    const int lo = p.local > 0 ? clamp32(static_cast<int64_t>(qp) - p.local) : INT_MIN;
+    const int hi = min(qp, N - 1);
+    const int lo_all = p.local > 0 ? clamp32(static_cast<int64_t>(qmax) - p.local) : INT_MIN;
+    const float scale = p.scale_log2;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; ok && j < nt; ++j) {
+      const int t0 = sp.group(v0 + j) * kWTile;
+      ok = mbar_wait(&s_full[t], j & 1, abort, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, s[k]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tmem_wait_ld_dep(s[k]);
+      // all tokens of the tile seen by all rows of the CTA, or by each row on its own
+      const int t1 = t0 + kWTile - 1;
+      if (!(t1 < N && t1 <= qmin && (t0 > lo_all || t1 < p.sinks))) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const int x = t0 + 32 * k + c;
+            if (!(x <= hi && (x > lo || x < p.sinks))) s[k][c] = 0xff800000u;   // -inf
+          }
+      }
+      float mx[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        mx[k] = __uint_as_float(s[k][0]);
+#pragma unroll
+        for (int c = 1; c < 32; ++c) mx[k] = fmaxf(mx[k], __uint_as_float(s[k][c]));
+      }
+      const float top = fmaxf(m, scale * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+      const bool grew = top > m + kSlack;   // from -inf too
+      if (__any_sync(0xffffffffu, grew)) {
+        const float f = grew ? ex2(m - top) : 1.f;   // 0 from -inf: O and l are 0 then
+        if (grew) m = top;
+        l *= f;
+        if (j > 0) {
+          ok = mbar_wait(&o_done[t], (j - 1) & 1, abort, p.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            uint32_t o[16];
+            tmem_ld16(to + 16 * k, o);
+            tmem_wait_ld_dep(o);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+            tmem_st16(to + 16 * k, o);
+          }
+        }
+      }
+      const float ref = m == -INFINITY ? 0.f : m;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t w[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float x = ex2(fmaf(__uint_as_float(s[k][2 * c]), scale, -ref));
+          const float y = ex2(fmaf(__uint_as_float(s[k][2 * c + 1]), scale, -ref));
+          sum[c & 3] += x + y;
+          w[c] = pack_bf16(x, y);
+        }
+        tmem_st16(ts + 16 * k, w);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&p_full[t]);
+    }
+    // the row's part
+    if (ok) ok = mbar_wait(&o_done[t], (nt - 1) & 1, abort, p.status);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      tc_fence_after();
+      const bool mine = r < nrow;
+      const int64_t at = static_cast<int64_t>(chunk) * p.rows + (mine ? row_of(r) : 0);
+      bool fin = (__float_as_uint(l) & 0x7f800000u) != 0x7f800000u;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t o[32];
+        tmem_ld32(to + 32 * k, o);
+        tmem_wait_ld_dep(o);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) fin = fin && (o[c] & 0x7f800000u) != 0x7f800000u;
+        if (mine) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4*>(p.part_o + at * 128 + 32 * k + 4 * c) =
+                make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+        }
+      }
+      if (mine) p.part_ml[at] = make_float2(m, fin ? l : kRedo);
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<1>(tmem, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t wide_configure() {
+  cudaError_t e = cudaFuncSetAttribute(wide_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       WideLayout<1>::alloc);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(wide_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             WideLayout<2>::alloc);
+  return e;
+}
+
+cudaError_t launch_attend_wide(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                               const AttendParams& p, int P, int max_rows, cudaStream_t st) {
+  const unsigned x = static_cast<unsigned>(P) * p.maxch;
+  if (max_rows <= kWTile) {
+    wide_kernel<1><<<dim3(x, 1), 256, WideLayout<1>::alloc, st>>>(kmap, vmap, p);
+  } else {
+    const unsigned y = (max_rows + 2 * kWTile - 1) / (2 * kWTile);
+    wide_kernel<2><<<dim3(x, y), 384, WideLayout<2>::alloc, st>>>(kmap, vmap, p);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace rkv

@@ -98,19 +98,21 @@ int attend_scratch(rkv_engine* e, float** buf, int64_t rows, bool logits, cudaSt
   return RKV_OK;
 }
 
-// Chunks of an item of `groups` 32-row groups (nmax the longest, sum over all
-// items): the cheapest count by waves of resident CTAs, a CTA costing its
-// groups and about four more, at most `cap`.
-int pick_chunks(int64_t items, int64_t sum, int64_t nmax, int64_t slots, int64_t cap) {
+// Chunks per item, for items of groups of rows (nmax the longest, sum over all
+// items): the cheapest count by waves of `slots` resident CTAs, a CTA costing its
+// groups and about `extra` more, at most `cap` and at least `least_groups` each.
+int pick_chunks(int64_t items, int64_t sum, int64_t nmax, int64_t slots, int64_t cap,
+                int64_t least_groups = 4, double extra = 4.0) {
   const int64_t avg = std::max<int64_t>(1, (sum + items - 1) / std::max<int64_t>(items, 1));
-  const int64_t most = std::min<int64_t>(std::max<int64_t>(1, cap), std::max<int64_t>(1, nmax / 4));
+  const int64_t most =
+      std::min<int64_t>(std::max<int64_t>(1, cap), std::max<int64_t>(1, nmax / least_groups));
   int64_t best = 1;
   double least = 1e300;
   for (int64_t c = 1; c <= std::min<int64_t>(most, 4096); c += c < 32 ? 1 : c / 16) {
     const int64_t gpc = (nmax + c - 1) / c;
     const int64_t ctas = items * ((avg + gpc - 1) / gpc);
-    const double cost = static_cast<double>((ctas + slots - 1) / slots) * (gpc + 4.0) +
-                        (c > 1 ? 4.0 : 0.0);
+    const double cost = static_cast<double>((ctas + slots - 1) / slots) * (gpc + extra) +
+                        (c > 1 ? extra : 0.0);
     if (cost < least) {
       least = cost;
       best = c;
@@ -142,6 +144,7 @@ int check_prefix(const rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, i
     *most = std::max(*most, m1 - m0);
   }
   *sum = x->off_host[P];
+  if (*sum >= (static_cast<int64_t>(1) << 31)) return RKV_ERR_UNSUPPORTED;   // tile coordinates
   int with = 0;
   for (int u = 0; u < U; ++u) {
     const int k = x->unit_prefix_host[u];
@@ -278,26 +281,37 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
   if (x) {
     const int64_t used = static_cast<int64_t>(own) * rows;
     const int64_t mrows = static_cast<int64_t>(members) * R;
-    const int64_t blocks = (mrows + 31) / 32;
+    // up to 32 query rows per prefix: HBM-bound, the same kernel as the own rows;
+    // more: 128- or 256-row tiles on tcgen05
+    const bool wide = mrows > 32;
+    const int64_t tile = wide ? kWideTile : 32;
+    const int64_t blocks = wide ? (mrows + 255) / 256 : 1;
     int64_t pg = 0, pmax = 1;
     for (int k = 0; k < x->num_prefixes; ++k) {
-      const int64_t g = (x->off_host[k + 1] - x->off_host[k] + 31) / 32;
+      const int64_t g = (x->off_host[k + 1] - x->off_host[k] + tile - 1) / tile;
       pg += g;
       pmax = std::max(pmax, g);
     }
     AttendParams pp = p;
     pp.keep = nullptr;
     pp.pos = nullptr;
-    pp.maxch = pick_chunks(x->num_prefixes, pg, pmax,
-                           std::max<int64_t>(1, 2 * e->nsm / blocks), (cap - used) / rows);
+    pp.status = e->status;
+    const int64_t pslots = std::max<int64_t>(1, (wide ? 1 : 2) * e->nsm / blocks);
+    pp.maxch = pick_chunks(x->num_prefixes, pg, pmax, pslots, (cap - used) / rows, wide ? 1 : 4,
+                           wide ? 3.0 : 4.0);
     pp.gpc = static_cast<int>((pmax + pp.maxch - 1) / pp.maxch);
     pp.part_o = part_o + used * 128;
     pp.part_ml = part_ml + used;
     j.pre_chunks = pp.maxch;
     j.pre_o = pp.part_o;
     j.pre_ml = pp.part_ml;
+    CUtensorMap kmap, vmap;
+    if (wide && (make_map(e, &kmap, x->K, static_cast<uint64_t>(psum), kWideTile) != RKV_OK ||
+                 make_map(e, &vmap, x->V, static_cast<uint64_t>(psum), kWideTile) != RKV_OK))
+      return RKV_ERR_CUDA;
     t_begin(e, RKV_KERNEL_SHARED, st);
-    err = launch_attend_prefix(pp, x->num_prefixes, static_cast<int>(mrows), st);
+    err = wide ? launch_attend_wide(kmap, vmap, pp, x->num_prefixes, static_cast<int>(mrows), st)
+               : launch_attend_prefix(pp, x->num_prefixes, static_cast<int>(mrows), st);
     t_end(e, st);
     if (err != cudaSuccess) return cuda_fail(err);
     ++e->launches;

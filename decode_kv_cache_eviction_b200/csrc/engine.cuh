@@ -89,6 +89,18 @@ inline int cuda_fail(cudaError_t e) {
   cudaGetLastError();
   return RKV_ERR_CUDA;
 }
+// Tensor map of rows of 128 bf16, in boxes of 64 columns x box_rows rows.
+inline int make_map(rkv_engine* e, CUtensorMap* m, const void* ptr, uint64_t rows, uint32_t box_rows) {
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(128), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(128) * 2};
+  cuuint32_t box[2] = {64, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = e->encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? RKV_OK : RKV_ERR_CUDA;
+}
 // Record the start event of a launch of `kernel` (when timing is on).
 inline void t_begin(rkv_engine* e, int kernel, cudaStream_t st) {
   if (!e->timing || e->nev >= rkv_engine::kMaxEv) return;

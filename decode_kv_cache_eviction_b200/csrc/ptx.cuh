@@ -290,6 +290,20 @@ __device__ __forceinline__ uint64_t desc_kmajor_sw128(uint32_t saddr) {
   return d;
 }
 
+// The same for an MN-major operand (rows of 64 MN-elements, 128-byte swizzle, one row
+// per K-element): groups of 8 K-elements 1024 bytes apart, the next 64 MN-elements
+// `mn_stride` bytes on.
+__device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr, uint32_t mn_stride) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(mn_stride >> 4) << 16;        // leading offset: next MN block
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;             // stride offset: next 8 of K
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+constexpr uint32_t kIdescTransposeB = 1u << 16;            // B is MN-major
+
 // Instruction descriptor, kind::f16: bf16 x bf16 -> f32, both K-major.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
   return (1u << 4)                                  // D: f32
@@ -314,6 +328,15 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
         "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+// A from tensor memory (row = lane, 16-bit pairs along the columns).
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 // Arrive (once) on a local barrier when all prior MMAs of this thread finish.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
@@ -343,6 +366,10 @@ __device__ __forceinline__ void tmem_wait_ld_dep(uint32_t (&v)[32]) {
                : RKV_RW8(0), RKV_RW8(8), RKV_RW8(16), RKV_RW8(24)
                :
                : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_ld_dep(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : RKV_RW8(0), RKV_RW8(8) : : "memory");
 }
 
 #define RKV_R8(i) "=r"(v[i + 0]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), \
@@ -397,6 +424,28 @@ __device__ __forceinline__ void tmem_ld16x256b_x2(uint32_t taddr, uint32_t (&v)[
                : "r"(taddr));
 }
 #undef RKV_R8
+
+// Registers to tensor memory: 32 lanes x 32-bit, 32 or 16 consecutive columns.
+#define RKV_V8(i) "r"(v[i + 0]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), \
+                  "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      RKV_V8(0), RKV_V8(8), RKV_V8(16), RKV_V8(24)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      RKV_V8(0), RKV_V8(8)
+      : "memory");
+}
+#undef RKV_V8
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
 
 // ---------------------------------------------------------------- misc
 __device__ __forceinline__ float ex2(float x) {   // 2^x (hardware approximation)

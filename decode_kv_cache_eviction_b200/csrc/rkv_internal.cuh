@@ -330,6 +330,7 @@ struct AttendParams {
   const int32_t* mem;            // units of each prefix, ascending
   const uint4* PK;
   const uint4* PV;
+  int* status;
 };
 struct JoinParams {
   int64_t rows;                  // U * R
@@ -342,6 +343,11 @@ struct JoinParams {
 cudaError_t attend_configure();
 cudaError_t launch_attend(const AttendParams& p, int U, cudaStream_t st);
 cudaError_t launch_attend_prefix(const AttendParams& p, int P, int max_rows, cudaStream_t st);
+// Many query rows per prefix (tcgen05): 128-row K/V tiles, p.gpc tiles per chunk.
+constexpr int kWideTile = 128;
+cudaError_t wide_configure();
+cudaError_t launch_attend_wide(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                               const AttendParams& p, int P, int max_rows, cudaStream_t st);
 cudaError_t launch_attend_join(const AttendParams& p, const JoinParams& j, cudaStream_t st);
 cudaError_t launch_attend_weights(const AttendParams& p, int U, cudaStream_t st);
 

@@ -10,6 +10,8 @@ Tolerances, elementwise, from the arithmetic:
 * out adds the accumulation of the p v (N terms in fp32: at most N 2^-23 of
   sum p |v|, in practice far less; a warp adds 16 per step) and one rounding to
   bf16, 2^-8 of the value at most;
+* where a prefix has more than 32 query rows its p is one bf16: half a step,
+  2^-8 of each p at most, on the prefix's share of sum p |v|;
 * lse: dz + 2^-20 + 2^-22 |lse|;  acc: |p| times the factor above, and 2^-23 of
   the sum.
 """
@@ -118,7 +120,9 @@ class Case:
                 np.abs(q).reshape(-1, 128) @ np.abs(k).T) / np.sqrt(128)
             eps = 2 * dz + 2.0 ** -20 + N * 2.0 ** -30
             mass = p.reshape(-1, N) @ np.abs(v) if N else np.zeros((self.G * self.nq, 128))
+            pre = p[..., :P].reshape(-1, P) @ np.abs(v[:P]) if P else np.zeros_like(mass)
             tol = 2.0 ** -8 * np.abs(o) + (eps + 2.0 ** -16 + N * 2.0 ** -23) * mass.reshape(o.shape)
+            tol += 2.0 ** -8 * pre.reshape(o.shape)
             assert np.all(np.abs(out[u] - o) <= tol), (u, np.max(np.abs(out[u] - o) - tol))
             none = np.isneginf(s)
             assert np.array_equal(np.isneginf(lse[u]), none), u
