@@ -43,7 +43,7 @@ EXPORTS = ("rkv_create", "rkv_destroy", "rkv_score", "rkv_select", "rkv_compact"
            "rkv_debug_intermediates", "rkv_status_string", "rkv_version", "rkv_attend",
            "rkv_attend_shared", "rkv_evict_accumulated", "rkv_fill_slots_ex")
 KERNELS = ("score", "plan", "gemm", "select", "compact", "evict", "fill", "refree", "finish",
-           "attend", "shared", "join", "weight", "drop")
+           "attend", "shared", "weight", "drop")
 
 
 class RkvConfig(ctypes.Structure):

@@ -24,9 +24,6 @@
 namespace rkv {
 namespace {
 
-constexpr int kAtWarps = 4;
-constexpr int kAtThreads = 32 * kAtWarps;
-constexpr int kAtStages = 3;
 constexpr int kAtTok = 16;                     // rows per stage
 constexpr int kList = 64;                      // visible-row list (ring) of a warp
 constexpr int kRowBytes = 256;
@@ -39,11 +36,21 @@ __host__ __device__ constexpr int at_stage_bytes() {
   return kAtTok * kRowBytes * (kMode == kWeights ? 1 : 2);
 }
 
+// Ring depth and warps per SM.  Twelve warps with two stages each hide the steps'
+// latencies better than eight with three (2048 units x 2176 rows: 448 -> 394 us) and
+// keep 96 KB in flight per SM; 32 query rows need the registers.
+template <int NB>
+struct AtCfg {
+  static constexpr int kStages = NB == 4 ? 3 : 2;
+  static constexpr int kWarps = NB == 4 ? 8 : 12;
+};
+
+template <int NS>
 struct AtWarpShared {
   int slot[kList];
   int pos[kList];
-  int mslot[kAtStages][kAtTok];   // rows of each stage
-  int mpos[kAtStages][kAtTok];
+  int mslot[NS][kAtTok];   // rows of each stage
+  int mpos[NS][kAtTok];
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
@@ -91,13 +98,23 @@ __device__ __forceinline__ RowSum no_rows() {
   return {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
 }
 
-// Joins the n parts of one query row to `s` and writes it, one warp: lane = four
-// dimensions, parts in order.  Part c is at index at(c) of o / ml.  The parts' (maximum,
-// sum) pairs of 32 parts are loaded at once, one per lane, and four parts' values
+// Both states as one.
+__device__ __forceinline__ RowSum add_rows(const RowSum& a, const RowSum& b) {
+  if (a.M == -INFINITY && a.L == 0.f) return b;
+  if (b.M == -INFINITY && b.L == 0.f) return a;
+  const float M = fmaxf(a.M, b.M);
+  const float f = a.M == M ? 1.f : ex2(a.M - M), h = b.M == M ? 1.f : ex2(b.M - M);
+  return {M, a.L * f + b.L * h,
+          make_float4(a.o.x * f + b.o.x * h, a.o.y * f + b.o.y * h, a.o.z * f + b.o.z * h,
+                      a.o.w * f + b.o.w * h)};
+}
+
+// Joins the n parts of one query row to `s`, one warp: lane = four dimensions,
+// parts in order.  Part c is at index at(c) of o / ml.  The parts' (maximum,
+// sum) pairs of 32 parts are loaded at once, one per lane, and eight parts' values
 // are in flight.
 template <class At>
-__device__ __forceinline__ void join_row(const AttendParams& p, int64_t row, RowSum s, int n,
-                                         At at) {
+__device__ __forceinline__ RowSum join_row(RowSum s, int n, At at) {
   const int lane = threadIdx.x & 31;
   float M = s.M, L = s.L;
   float4 o = s.o;
@@ -123,19 +140,20 @@ __device__ __forceinline__ void join_row(const AttendParams& p, int64_t row, Row
     o.z *= f;
     o.w *= f;
     const int e = min(32, n - c0);
-    for (int k0 = 0; k0 < e; k0 += 4) {
-      float4 x[4];
-      float w[4];
+    for (int k0 = 0; k0 < e; k0 += 8) {
+      float4 x[8];
+      float w[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint64_t a = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), k0 + k);
-        w[k] = __shfl_sync(0xffffffffu, h, k0 + k);
+      for (int k = 0; k < 8; ++k) {
+        const int c = (k0 + k) & 31;
+        const uint64_t a = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), c);
+        w[k] = __shfl_sync(0xffffffffu, h, c);
         x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if ((some >> (k0 + k)) & 1u) x[k] = __ldcg(reinterpret_cast<const float4*>(a) + lane);
+        if ((some >> c) & 1u) x[k] = __ldcg(reinterpret_cast<const float4*>(a) + lane);
         else w[k] = 0.f;
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 8; ++k) {
         o.x = fmaf(x[k].x, w[k], o.x);
         o.y = fmaf(x[k].y, w[k], o.y);
         o.z = fmaf(x[k].z, w[k], o.z);
@@ -143,7 +161,57 @@ __device__ __forceinline__ void join_row(const AttendParams& p, int64_t row, Row
       }
     }
   }
-  attend_store(p, row, lane, M, L, o);
+  return {M, L, o};
+}
+
+// A query row against its whole prefix, one warp, row by row: for rows whose
+// product met a value that is not finite, which need not be one that they see.
+__device__ __noinline__ RowSum prefix_row(const AttendParams& p, int64_t row, int u, int r) {
+  const int lane = threadIdx.x & 31;
+  const int x = p.unit_prefix[u];
+  const int64_t base = p.pre_off[x];
+  const int N = static_cast<int>(p.pre_off[x + 1] - base);
+  const int qp = clamp32(newest_query(p, u) - (p.nq - 1) + r % p.nq);
+  const int lo = p.local > 0 ? clamp32(static_cast<int64_t>(qp) - p.local) : INT_MIN;
+  auto four = [&](const uint32_t* src) {
+    const uint2 w = *reinterpret_cast<const uint2*>(src + 2 * lane);
+    return make_float4(bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y));
+  };
+  const float4 q = four(p.Q + row * 64);
+  RowSum s = no_rows();
+  for (int i = 0; i < N; ++i) {
+    if (!sees(i, qp, lo, p.sinks)) continue;
+    const float4 k = four(reinterpret_cast<const uint32_t*>(p.PK + (base + i) * 16));
+    const float4 v = four(reinterpret_cast<const uint32_t*>(p.PV + (base + i) * 16));
+    const float z = p.scale_log2 * warp_reduce_sum(q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w);
+    const float M = fmaxf(s.M, z);
+    const float f = s.M == M ? 1.f : ex2(s.M - M);
+    const float w = ex2(z - (M == -INFINITY ? 0.f : M));
+    s.M = M;
+    s.L = s.L * f + w;
+    s.o.x = s.o.x * f + w * v.x;
+    s.o.y = s.o.y * f + w * v.y;
+    s.o.z = s.o.z * f + w * v.z;
+    s.o.w = s.o.w * f + w * v.w;
+  }
+  return s;
+}
+
+// Joins the parts that the prefix kernel left for a query row of unit u.
+__device__ __forceinline__ RowSum join_prefix(const AttendParams& p, RowSum s, int64_t row, int u) {
+  if (!p.pre_o || __ldg(&p.unit_prefix[u]) < 0) return s;
+  bool redo = false;
+  for (int c = threadIdx.x & 31; c < p.pre_chunks; c += 32)
+    redo |= __ldg(&p.pre_ml[c * p.rows + row]).y == kRedo;
+  if (__any_sync(0xffffffffu, redo)) {   // from the rows themselves, then the parts of s
+    const RowSum x = prefix_row(p, row, u, static_cast<int>(row - static_cast<int64_t>(u) * p.R));
+    return add_rows(x, s);
+  }
+  return join_row(s, p.pre_chunks, [&](int c, float2& ml, const float4*& src) {
+    const int64_t at = c * p.rows + row;
+    ml = __ldg(&p.pre_ml[at]);
+    src = reinterpret_cast<const float4*>(p.pre_o + at * 128);
+  });
 }
 
 // acc_out = acc_in + sum_r 2^(z_r - lse2_r) for rows i0 .. i1 of a unit, from the
@@ -202,18 +270,20 @@ __device__ __forceinline__ void weights_any(const AttendParams& p, int64_t base,
   }
 }
 
-// NB: query rows / 8 of this launch (1, 2 or 4).
-template <int NB, int kMode>
-__global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParams p) {
-  extern __shared__ __align__(128) uint8_t at_smem[];
-  __shared__ AtWarpShared wsh[kAtWarps];
+// NB: query rows / 8 of this launch (1, 2 or 4).  kOne: one query per head, so a row
+// is seen by all query rows of its unit or by none.
+template <int NB, int kMode, bool kOne, int W>
+__global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(const __grid_constant__ AttendParams p) {
+  constexpr int NS = AtCfg<NB>::kStages;
+  extern __shared__ __align__(256) uint8_t at_smem[];
+  __shared__ AtWarpShared<NS> wsh[W];
   __shared__ int s_qp[32];
-  __shared__ float s_ml[kAtWarps][2][32];
+  __shared__ float s_ml[W][2][32];
   __shared__ float s_lse2[32];
   __shared__ int s_last;
   const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
   const int g = lane >> 2, q = lane & 3;
-  AtWarpShared& ws = wsh[wp];
+  AtWarpShared<NS>& ws = wsh[wp];
 
   // what this CTA works on: rows [row0, row0 + nrow) of queries against groups
   // of the sequence of N rows at `base`
@@ -232,7 +302,6 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
     base = __ldg(&p.tok_off[item]);
     end = __ldg(&p.tok_off[item + 1]);
   }
-  const int N = static_cast<int>(end - base);
   const int nrow = min(32, total - row0);
   // query row r of this CTA: its unit and its row of Q
   auto row_of = [&](int r) -> int64_t {
@@ -240,6 +309,23 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
     const int m = (row0 + r) / p.R;
     return static_cast<int64_t>(__ldg(&p.mem[mo + m])) * p.R + (row0 + r - m * p.R);
   };
+  // query rows as B fragments: row 8 nb + g, dimensions 16 ks + 2q + {0, 1} and + 8
+  uint32_t bq[NB][8][2];
+  auto load_queries = [&](int r0) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int r = r0 + 8 * nb + g;
+      const bool on = kMode == kWeights ? r < p.R : r < nrow;
+      const uint32_t* src = p.Q + (on ? row_of(r) : 0) * 64;
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        bq[nb][ks][0] = on ? __ldg(&src[8 * ks + q]) : 0u;
+        bq[nb][ks][1] = on ? __ldg(&src[8 * ks + q + 4]) : 0u;
+      }
+    }
+  };
+  load_queries(0);
+  const int N = static_cast<int>(end - base);
   int first = 0;
   int64_t qmin, qmax;
   if (kMode == kPrefix) {
@@ -263,14 +349,12 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
     qmax = hi;
   } else {
     first = prefix_len(p, item);
-    qmax = newest_query(p, item);
+    qmax = p.q_pos ? static_cast<int64_t>(__ldg(&p.q_pos[item])) : static_cast<int64_t>(first) + N - 1;
     qmin = qmax - (p.nq - 1);
-    if (tid < 32)
-      s_qp[tid] = tid < nrow ? clamp32(qmin + (row0 + tid) % p.nq) : INT_MIN;
-    __syncthreads();
   }
-  const int qmax32 = clamp32(qmax);
+  const int qmax32 = clamp32(qmax), qmin32 = clamp32(qmin);
   const int lo_any = p.local > 0 ? clamp32(qmin - p.local) : INT_MIN;
+  const int lo_all = p.local > 0 ? clamp32(qmax - p.local) : INT_MIN;
   Span sp;
   if (kMode == kWeights || p.pos) {   // every row: all are written, or any may hold any position
     sp.gs = sp.start = 0;
@@ -284,44 +368,38 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
   const uint4* Kg = kMode == kPrefix ? p.PK : p.K;
   const uint4* Vg = kMode == kPrefix ? p.PV : p.V;
 
-  // query rows as B fragments: row 8 nb + g, dimensions 16 ks + 2q + {0, 1} and + 8
-  uint32_t bq[NB][8][2];
   int qp[NB][2], qlo[NB][2];    // limits of this lane's rows 8 nb + 2q + e
   float lse2[NB][2];            // weights pass: log2 of the rows' sums
-  auto load_rows = [&](int r0) {   // rows r0 .. of this CTA (the weights pass moves on in r0)
+  auto load_limits = [&](int r0) {   // rows r0 .. of this CTA (the weights pass moves on in r0)
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const int r = r0 + 8 * nb + g;
-      const bool on = kMode == kWeights ? r < p.R : r < nrow;
-      const uint32_t* src = p.Q + (on ? row_of(r) : 0) * 64;
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        bq[nb][ks][0] = on ? __ldg(&src[8 * ks + q]) : 0u;
-        bq[nb][ks][1] = on ? __ldg(&src[8 * ks + q + 4]) : 0u;
-      }
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int x = r0 + 8 * nb + 2 * q + e;
-        if (kMode == kWeights) {
-          const bool in = x < p.R;
-          qp[nb][e] = in ? clamp32(qmin + x % p.nq) : INT_MIN;
-          lse2[nb][e] = in ? __ldg(&p.lse2[static_cast<int64_t>(item) * p.R + x]) : 0.f;
-        } else {
+        if (kMode == kPrefix) {
           qp[nb][e] = s_qp[x];
+        } else {
+          const bool in = kMode == kWeights ? x < p.R : x < nrow;
+          qp[nb][e] = in ? clamp32(qmin + (row0 + x) % p.nq) : INT_MIN;
+          if (kMode == kWeights)
+            lse2[nb][e] = in ? __ldg(&p.lse2[static_cast<int64_t>(item) * p.R + x]) : INFINITY;
         }
         qlo[nb][e] = p.local > 0
                          ? clamp32(static_cast<int64_t>(qp[nb][e]) - p.local) : INT_MIN;
       }
-    }
   };
-  load_rows(0);
+  load_limits(0);
 
   constexpr int kStage = at_stage_bytes<kMode>();
-  uint8_t* ring = at_smem + wp * (kAtStages * kStage);
+  uint8_t* ring = at_smem + wp * (NS * kStage);
   const uint32_t ring_a = smem_u32(ring);
-  // ldmatrix lane offsets: K rows as A (tokens x d), V rows transposed (d x tokens)
+  // ldmatrix lane addresses within a stage, K rows as A (tokens x d) and V rows
+  // transposed (d x tokens): 16-byte piece c of row r lies at r 256 + 16 (c ^ (r & 7)),
+  // and piece 2 k + b of a lane's row at its piece b's address ^ 32 k
   const int kt = (lane & 7) + ((lane >> 3) & 1) * 8, kc = lane >> 4;
   const int vt = (lane & 7) + ((lane >> 4) & 1) * 8, vc = (lane >> 3) & 1;
+  const uint32_t kofs = kt * kRowBytes + ((kc ^ (kt & 7)) << 4);
+  const uint32_t vofs = kAtTok * kRowBytes + vt * kRowBytes + ((vc ^ (vt & 7)) << 4);
 
   float O[8][NB][4];
   float m[NB][2], l[NB][2];
@@ -329,6 +407,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
   // query of the unit may not see (0 x inf in the product), or from the split
   // of p into two parts.  The chunk is then done again with such V rows taken
   // out of the product and added one by one to the query rows that see them.
+#pragma unroll 1
   for (int careful = 0; careful < 2; ++careful) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
@@ -341,13 +420,26 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
     }
     int v = chunk * p.gpc + wp;   // next group of this warp
     int head = 0, cnt = 0;        // list: first entry, entries
+    // a group's live bytes and positions, loaded two groups ahead
+    auto fetch = [&](int vv, int& live, int& ps) {
+      const int slot = 32 * sp.group(vv) + lane;
+      const bool in = vv < v_end && slot < N;
+      live = in ? 1 : 0;
+      ps = first + slot;
+      if (keep && in) live = __ldg(&keep[base + slot]);
+      if (pos && in) ps = __ldg(&pos[base + slot]);
+    };
+    int live0, pos0, live1, pos1;
+    fetch(v, live0, pos0);
+    fetch(v + W, live1, pos1);
     // rows of group v (virtual order: sinks' groups, then the window's)
     auto scan = [&]() {
       const int slot = 32 * sp.group(v) + lane;
-      bool on = slot < N;
-      int ps = first + slot;
-      if (on && keep) on = __ldg(&keep[base + slot]) != 0;
-      if (pos && slot < N) ps = __ldg(&pos[base + slot]);
+      const int ps = pos0;
+      bool on = live0 != 0;
+      live0 = live1;
+      pos0 = pos1;
+      fetch(v + 2 * W, live1, pos1);
       if (kMode == kPrefix && p.local > 0) {
         bool any = false;
         for (int r = 0; r < nrow; ++r) {
@@ -367,50 +459,75 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
         ws.pos[at] = ps;
       }
       cnt += __popc(mask);
-      v += kAtWarps;
+      v += W;
     };
     int issued = 0, done = 0, last = kAtTok;   // stages; rows of the last stage
+    uint32_t some = 0;   // bit s: a query row does not see a row of stage s
+    int si = 0, sd = 0;  // their slots in the ring
     auto produce = [&]() {
       while (cnt < kAtTok && v < v_end) scan();
       __syncwarp();
       if (cnt > 0) {
         const int n = min(cnt, kAtTok);
-        const int s = issued % kAtStages;
-        const uint32_t dst = ring_a + s * kStage;
-        const int c = lane & 15;
+        const int s = si;
+        // lane: 64 bytes of rows lane / 4 and lane / 4 + 8, a quarter at a time
+        const uint32_t dst = ring_a + s * kStage + g * kRowBytes;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 2 * i + (lane >> 4);
+        for (int h = 0; h < 2; ++h) {
+          const int r = g + 8 * h;
           const bool on = r < n;
           const int64_t row = base + (on ? ws.slot[(head + r) & (kList - 1)] : 0);
-          const uint32_t d = dst + r * kRowBytes + ((c ^ (r & 7)) << 4);
-          cp16(d, Kg + row * 16 + c, on);
-          if (kMode != kWeights) cp16(d + kAtTok * kRowBytes, Vg + row * 16 + c, on);
+          const uint4* ks = Kg + row * 16 + q;
+          const uint4* vs = Vg + row * 16 + q;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t d = dst + 8 * h * kRowBytes + (((4 * c + q) ^ g) << 4);
+            cp16(d, ks + 4 * c, on);
+            if (kMode != kWeights) cp16(d + kAtTok * kRowBytes, vs + 4 * c, on);
+          }
         }
+        bool part = false;
         if (lane < kAtTok) {
+          const int ps = ws.pos[(head + lane) & (kList - 1)];
           ws.mslot[s][lane] = ws.slot[(head + lane) & (kList - 1)];
-          ws.mpos[s][lane] = ws.pos[(head + lane) & (kList - 1)];
+          if (!kOne) {
+            ws.mpos[s][lane] = ps;
+            part = lane >= n || !sees(ps, qmin32, lo_all, p.sinks);
+          }
+        }
+        if (!kOne) {
+          const bool any = __any_sync(0xffffffffu, part);
+          some = (some & ~(1u << s)) | ((any ? 1u : 0u) << s);
         }
         head = (head + n) & (kList - 1);
         cnt -= n;
         ++issued;
         last = n;
+        if (++si == NS) si = 0;
       }
       cp_commit();
       __syncwarp();
     };
-    for (int s = 0; s < kAtStages - 1; ++s) produce();
+#pragma unroll 1
+    for (int s = 0; s < NS - 1; ++s) produce();
+#pragma unroll 1
     for (;;) {
       produce();
-      cp_wait<kAtStages - 1>();
+      cp_wait<NS - 1>();
       __syncwarp();
       if (done == issued) break;
-      const int s = done % kAtStages;
+      const int s = sd;
+      if (++sd == NS) sd = 0;
       ++done;
       const int n = done == issued ? last : kAtTok;
-      const uint32_t ka = ring_a + s * kStage, va = ka + kAtTok * kRowBytes;
+      const uint32_t st_a = ring_a + s * kStage;
       const bool in0 = g < n, in1 = g + 8 < n;      // this lane's tokens g, g + 8
-      const int p0 = ws.mpos[s][g], p1 = ws.mpos[s][g + 8];
+      // which query rows see them
+      const bool masked = kOne ? n < kAtTok : ((some >> s) & 1u) != 0;
+      auto seen = [&](int nb, int e, int h) {   // query row 8 nb + 2q + e, token g + 8 h
+        const bool in = h ? in1 : in0;
+        return kOne ? in : in && sees(ws.mpos[s][g + 8 * h], qp[nb][e], qlo[nb][e], p.sinks);
+      };
       float wsum0 = 0.f, wsum1 = 0.f;
       for (int r0 = 0;;) {
         // logits of 16 tokens x 8 NB query rows
@@ -422,7 +539,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
           uint32_t a[4];
-          ldsm4(a, ka + kt * kRowBytes + (((2 * ks + kc) ^ (kt & 7)) << 4));
+          ldsm4(a, (st_a + kofs) ^ (ks << 5));
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) mma16816(c[nb], a, bq[nb][ks][0], bq[nb][ks][1]);
         }
@@ -431,17 +548,19 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              if (sees(p0, qp[nb][e], qlo[nb][e], p.sinks))
-                wsum0 += ex2(fmaf(c[nb][e], p.scale_log2, -lse2[nb][e]));
-              if (sees(p1, qp[nb][e], qlo[nb][e], p.sinks))
+              if (!masked || seen(nb, e, 0)) wsum0 += ex2(fmaf(c[nb][e], p.scale_log2, -lse2[nb][e]));
+              if (!masked || seen(nb, e, 1))
                 wsum1 += ex2(fmaf(c[nb][2 + e], p.scale_log2, -lse2[nb][e]));
             }
           r0 += 8 * NB;
-          if (8 * NB < p.R) load_rows(r0 < p.R ? r0 : 0);   // back to the first rows at the end
+          if (8 * NB < p.R) {   // the next rows, or back to the first ones
+            load_queries(r0 < p.R ? r0 : 0);
+            load_limits(r0 < p.R ? r0 : 0);
+          }
           if (r0 < p.R) continue;
           break;
         } else {
-          if constexpr (NB == 1 && kMode == kOwn) {
+          if constexpr (kOne && kMode == kOwn) {
             if (p.z && 2 * q < p.gp) {   // logits for the weights, before masks and scaling
               float* z0 = p.z + (base + ws.mslot[s][g]) * p.gp + 2 * q;
               float* z1 = p.z + (base + ws.mslot[s][g + 8]) * p.gp + 2 * q;
@@ -454,6 +573,15 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
               }
             }
           }
+          if (masked) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                if (!seen(nb, e, 0)) c[nb][e] = -INFINITY;
+                if (!seen(nb, e, 1)) c[nb][2 + e] = -INFINITY;
+              }
+          }
           uint32_t bh[NB][2], bl[NB][2];
           float mref[NB][2];
           bool grew = false;
@@ -461,8 +589,6 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              if (!(in0 && sees(p0, qp[nb][e], qlo[nb][e], p.sinks))) c[nb][e] = -INFINITY;
-              if (!(in1 && sees(p1, qp[nb][e], qlo[nb][e], p.sinks))) c[nb][2 + e] = -INFINITY;
               float x = fmaxf(c[nb][e], c[nb][2 + e]);
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
@@ -526,8 +652,8 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
             for (; bad; bad &= bad - 1u) {
               const int t = __ffs(bad) - 1;
               uint8_t* vr = ring + s * kStage + kAtTok * kRowBytes + t * kRowBytes;
-              const int pt = ws.mpos[s][t];
               float pv[NB][2];
+              bool on[NB][2];
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -535,6 +661,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
                   const float a = __shfl_sync(0xffffffffu, c[nb][e], (t & 7) * 4 + q);
                   const float b = __shfl_sync(0xffffffffu, c[nb][2 + e], (t & 7) * 4 + q);
                   pv[nb][e] = t < 8 ? a : b;
+                  on[nb][e] = kOne || sees(ws.mpos[s][t], qp[nb][e], qlo[nb][e], p.sinks);
                 }
 #pragma unroll
               for (int mb = 0; mb < 8; ++mb)
@@ -547,8 +674,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
                   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                      if (sees(pt, qp[nb][e], qlo[nb][e], p.sinks))
-                        O[mb][nb][2 * h + e] += pv[nb][e] * x;
+                      if (on[nb][e]) O[mb][nb][2 * h + e] += pv[nb][e] * x;
                 }
               __syncwarp();
               if (lane < 16) *reinterpret_cast<uint4*>(vr + lane * 16) = make_uint4(0, 0, 0, 0);
@@ -559,7 +685,7 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
 #pragma unroll
           for (int mb = 0; mb < 8; ++mb) {
             uint32_t a[4];
-            ldsm4_t(a, va + vt * kRowBytes + (((2 * mb + vc) ^ (vt & 7)) << 4));
+            ldsm4_t(a, (st_a + vofs) ^ (mb << 5));
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
               mma16816(O[mb][nb], a, bh[nb][0], bh[nb][1]);
@@ -630,27 +756,13 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
       }
     }
     __syncthreads();
-    const int nr = min(nrow, 8 * NB);
-    for (int i = tid; i < nr * 32; i += kAtThreads) {
-      const int r = i >> 5, d4 = i & 31;
-      float M = -INFINITY;
+    // one warp per query row, lane = four dimensions
+    for (int r = wp; r < min(nrow, 8 * NB); r += W) {
+      RowSum x = no_rows();
 #pragma unroll
-      for (int w = 0; w < kAtWarps; ++w) M = fmaxf(M, s_ml[w][0][r]);
-      float L = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kAtWarps; ++w) {
-        const float mw = s_ml[w][0][r], lw = s_ml[w][1][r];
-        // nothing seen by this warp (a row of NaN logits keeps m = -inf with l = NaN)
-        if (mw == -INFINITY && lw == 0.f) continue;
-        const float f = mw == M ? 1.f : ex2(mw - M);
-        const float4 x = *reinterpret_cast<const float4*>(
-            sO + (w * 8 * NB + r) * kOStride + 4 * d4);
-        L += f * lw;
-        o.x += f * x.x;
-        o.y += f * x.y;
-        o.z += f * x.z;
-        o.w += f * x.w;
+      for (int w = 0; w < W; ++w) {
+        const float4 o = *reinterpret_cast<const float4*>(sO + (w * 8 * NB + r) * kOStride + 4 * lane);
+        x = add_rows(x, {s_ml[w][0][r], s_ml[w][1][r], o});
       }
       const int64_t row = row_of(r);
       if (p.part_o) {
@@ -658,15 +770,16 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
             kMode == kPrefix
                 ? static_cast<int64_t>(chunk) * p.rows + row
                 : (static_cast<int64_t>(item) * p.maxch + chunk) * p.R + row0 + r;
-        __stcg(reinterpret_cast<float4*>(p.part_o + at * 128 + 4 * d4), o);
-        if (d4 == 0) __stcg(&p.part_ml[at], make_float2(M, L));
+        __stcg(reinterpret_cast<float4*>(p.part_o + at * 128 + 4 * lane), x.o);
+        if (lane == 0) __stcg(&p.part_ml[at], make_float2(x.M, x.L));
       } else {
-        attend_store(p, row, d4, M, L, o);
-        if (d4 == 0) s_lse2[r] = L == 0.f ? INFINITY : M + log2f(L);
+        x = join_prefix(p, x, row, item);
+        attend_store(p, row, lane, x.M, x.L, x.o);
+        if (lane == 0) s_lse2[r] = x.L == 0.f ? INFINITY : x.M + log2f(x.L);
       }
     }
     if constexpr (kMode == kOwn) {
-      if (p.count) {
+      if (p.part_o) {
         // the CTA that finishes a unit's rows last joins its parts
         __threadfence();
         __syncthreads();
@@ -677,13 +790,16 @@ __global__ void __launch_bounds__(kAtThreads, 2) attend_kernel(const AttendParam
         __threadfence();
         if (tid == 0) *cnt = 0;   // ready for the next call
         const int64_t at0 = static_cast<int64_t>(item) * p.maxch * p.R + row0;
-        for (int r = wp; r < nrow; r += kAtWarps)
-          join_row(p, row_of(r), no_rows(), p.maxch, [&](int c, float2& ml, const float4*& src) {
+        for (int r = wp; r < nrow; r += W) {
+          RowSum x = join_row(no_rows(), p.maxch, [&](int c, float2& ml, const float4*& src) {
             const int64_t at = at0 + static_cast<int64_t>(c) * p.R + r;
             ml = __ldcg(&p.part_ml[at]);
             src = reinterpret_cast<const float4*>(p.part_o + at * 128);
           });
-      } else if (NB == 1 && p.z && !p.part_o) {
+          x = join_prefix(p, x, row_of(r), item);
+          attend_store(p, row_of(r), lane, x.M, x.L, x.o);
+        }
+      } else if (kOne && p.z) {
         __syncthreads();   // all logits of the unit are written
         weights_any(p, base, first, qmax, s_lse2, 0, N);
       }
@@ -703,117 +819,65 @@ __global__ void __launch_bounds__(256) weights_kernel(const AttendParams p) {
               static_cast<int>(min(static_cast<int64_t>(N), i0 + static_cast<int64_t>(p.gpc) * 32)));
 }
 
-// A query row against its whole prefix, one warp, row by row: for rows whose
-// product met a value that is not finite, which need not be one that they see.
-__device__ __noinline__ RowSum prefix_row(const AttendParams& p, int64_t row, int u, int r) {
-  const int lane = threadIdx.x & 31;
-  const int x = p.unit_prefix[u];
-  const int64_t base = p.pre_off[x];
-  const int N = static_cast<int>(p.pre_off[x + 1] - base);
-  const int qp = clamp32(newest_query(p, u) - (p.nq - 1) + r % p.nq);
-  const int lo = p.local > 0 ? clamp32(static_cast<int64_t>(qp) - p.local) : INT_MIN;
-  auto four = [&](const uint32_t* src) {
-    const uint2 w = *reinterpret_cast<const uint2*>(src + 2 * lane);
-    return make_float4(bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y));
-  };
-  const float4 q = four(p.Q + row * 64);
-  RowSum s = no_rows();
-  for (int i = 0; i < N; ++i) {
-    if (!sees(i, qp, lo, p.sinks)) continue;
-    const float4 k = four(reinterpret_cast<const uint32_t*>(p.PK + (base + i) * 16));
-    const float4 v = four(reinterpret_cast<const uint32_t*>(p.PV + (base + i) * 16));
-    const float z = p.scale_log2 * warp_reduce_sum(q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w);
-    const float M = fmaxf(s.M, z);
-    const float f = s.M == M ? 1.f : ex2(s.M - M);
-    const float w = ex2(z - (M == -INFINITY ? 0.f : M));
-    s.M = M;
-    s.L = s.L * f + w;
-    s.o.x = s.o.x * f + w * v.x;
-    s.o.y = s.o.y * f + w * v.y;
-    s.o.z = s.o.z * f + w * v.z;
-    s.o.w = s.o.w * f + w * v.w;
-  }
-  return s;
-}
-
-// Joins the parts of every query row of a shared call, one warp per row: the
-// prefix's chunks, then the unit's own.
-__global__ void __launch_bounds__(128) join_kernel(const AttendParams p, const JoinParams j) {
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (row >= j.rows) return;
-  const int u = static_cast<int>(row / p.R), r = static_cast<int>(row - static_cast<int64_t>(u) * p.R);
-  int np = __ldg(&p.unit_prefix[u]) >= 0 ? j.pre_chunks : 0;
-  RowSum s = no_rows();
-  bool redo = false;
-  for (int c = threadIdx.x & 31; c < np; c += 32)
-    redo |= j.pre_ml[static_cast<int64_t>(c) * j.rows + row].y == kRedo;
-  if (__any_sync(0xffffffffu, redo)) {
-    s = prefix_row(p, row, u, r);
-    np = 0;
-  }
-  join_row(p, row, s, np + j.own_chunks, [&](int c, float2& ml, const float4*& src) {
-    const bool own = c >= np;
-    const int64_t at = own ? (static_cast<int64_t>(u) * j.own_chunks + (c - np)) * p.R + r
-                           : static_cast<int64_t>(c) * j.rows + row;
-    ml = own ? j.own_ml[at] : j.pre_ml[at];
-    src = reinterpret_cast<const float4*>((own ? j.own_o : j.pre_o) + at * 128);
-  });
-}
-
-template <int NB, int kMode>
+template <int NB, int kMode, int W>
 __host__ __device__ constexpr int at_smem_bytes() {
-  const int ring = kAtWarps * kAtStages * at_stage_bytes<kMode>();
-  const int fin = kMode == kWeights ? 0 : kAtWarps * 8 * NB * kOStride * 4;
+  const int ring = W * AtCfg<NB>::kStages * at_stage_bytes<kMode>();
+  const int fin = kMode == kWeights ? 0 : W * 8 * NB * kOStride * 4;
   return ring > fin ? ring : fin;
 }
 
-template <int NB, int kMode>
+template <int NB, int kMode, bool kOne, int W>
 cudaError_t configure_one() {
-  return cudaFuncSetAttribute(attend_kernel<NB, kMode>,
+  return cudaFuncSetAttribute(attend_kernel<NB, kMode, kOne, W>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              at_smem_bytes<NB, kMode>());
+                              at_smem_bytes<NB, kMode, W>());
 }
-template <int kMode>
+template <int kMode, int W>
 cudaError_t configure_mode() {
-  cudaError_t e = configure_one<1, kMode>();
-  if (e == cudaSuccess) e = configure_one<2, kMode>();
-  if (e == cudaSuccess) e = configure_one<4, kMode>();
+  cudaError_t e = configure_one<1, kMode, false, W>();
+  if (e == cudaSuccess) e = configure_one<2, kMode, false, W>();
+  if (e == cudaSuccess) e = configure_one<4, kMode, false, W>();
   return e;
 }
 
-template <int kMode>
-cudaError_t launch_mode(const AttendParams& p, int rows, dim3 grid, cudaStream_t st) {
-  if (rows <= 8)
-    attend_kernel<1, kMode><<<grid, kAtThreads, at_smem_bytes<1, kMode>(), st>>>(p);
-  else if (rows <= 16)
-    attend_kernel<2, kMode><<<grid, kAtThreads, at_smem_bytes<2, kMode>(), st>>>(p);
-  else
-    attend_kernel<4, kMode><<<grid, kAtThreads, at_smem_bytes<4, kMode>(), st>>>(p);
+template <int NB, int kMode, bool kOne, int W>
+cudaError_t launch_one(const AttendParams& p, dim3 grid, cudaStream_t st) {
+  attend_kernel<NB, kMode, kOne, W><<<grid, 32 * W, at_smem_bytes<NB, kMode, W>(), st>>>(p);
   return cudaGetLastError();
+}
+template <int kMode, int W>
+cudaError_t launch_mode(const AttendParams& p, int rows, dim3 grid, cudaStream_t st) {
+  if (rows <= 8) {
+    if (kMode == kOwn && p.nq == 1) return launch_one<1, kOwn, true, W>(p, grid, st);
+    return launch_one<1, kMode, false, W>(p, grid, st);
+  }
+  if (rows <= 16) return launch_one<2, kMode, false, W>(p, grid, st);
+  return launch_one<4, kMode, false, W>(p, grid, st);
 }
 
 }  // namespace
 
 cudaError_t attend_configure() {
-  cudaError_t e = configure_mode<kOwn>();
-  if (e == cudaSuccess) e = configure_mode<kPrefix>();
-  if (e == cudaSuccess) e = configure_mode<kWeights>();
+  cudaError_t e = configure_mode<kOwn, 4>();
+  if (e == cudaSuccess) e = configure_mode<kOwn, 2>();
+  if (e == cudaSuccess) e = configure_one<1, kOwn, true, 4>();
+  if (e == cudaSuccess) e = configure_one<1, kOwn, true, 2>();
+  if (e == cudaSuccess) e = configure_mode<kPrefix, 4>();
+  if (e == cudaSuccess) e = configure_mode<kWeights, 4>();
   return e;
 }
 
-cudaError_t launch_attend(const AttendParams& p, int U, cudaStream_t st) {
+int attend_warps_per_sm(int rows) { return rows <= 16 ? AtCfg<1>::kWarps : AtCfg<4>::kWarps; }
+
+cudaError_t launch_attend(const AttendParams& p, int U, int warps, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(U) * p.maxch, (p.R + 31) / 32);
-  return launch_mode<kOwn>(p, p.R, grid, st);
+  return warps == 2 ? launch_mode<kOwn, 2>(p, p.R, grid, st)
+                    : launch_mode<kOwn, 4>(p, p.R, grid, st);
 }
 
 cudaError_t launch_attend_prefix(const AttendParams& p, int P, int max_rows, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(P) * p.maxch, (max_rows + 31) / 32);
-  return launch_mode<kPrefix>(p, max_rows, grid, st);
-}
-
-cudaError_t launch_attend_join(const AttendParams& p, const JoinParams& j, cudaStream_t st) {
-  join_kernel<<<static_cast<unsigned>((j.rows + 3) / 4), 128, 0, st>>>(p, j);
-  return cudaGetLastError();
+  return launch_mode<kPrefix, 4>(p, max_rows, grid, st);
 }
 
 cudaError_t launch_attend_weights(const AttendParams& p, int U, cudaStream_t st) {
@@ -822,7 +886,7 @@ cudaError_t launch_attend_weights(const AttendParams& p, int U, cudaStream_t st)
     weights_kernel<<<grid, 256, 0, st>>>(p);
     return cudaGetLastError();
   }
-  return launch_mode<kWeights>(p, p.R, grid, st);
+  return launch_mode<kWeights, 4>(p, p.R, grid, st);
 }
 
 }  // namespace rkv

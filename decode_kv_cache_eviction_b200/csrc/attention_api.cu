@@ -57,12 +57,14 @@ int check_rows(const rkv_engine* e, const rkv_batch* b, Lengths* L) {
 
 constexpr int64_t kPartFloats = 130;   // a part: 128 values, maximum and sum
 
-// Query rows whose parts the scratch holds: eight waves of CTAs (two per SM)
-// of at most 32 rows; shared calls hold two parts of every query row at least.
+// Query rows whose parts the scratch holds: eight waves of CTAs (two per SM) of at
+// most 32 rows; for shared calls also every query row's own and prefix part, and
+// two waves of CTAs of at most 256 rows of a split prefix.
 int64_t part_rows(const rkv_engine* e, bool shared) {
-  const int64_t all = static_cast<int64_t>(e->cfg.group) * e->cfg.window;
-  const int64_t split = 16ll * e->nsm * std::min<int64_t>(all, 32);
-  return shared ? std::max<int64_t>(2 * e->cfg.max_units * all, split) : split;
+  const int64_t one = static_cast<int64_t>(e->cfg.group) * e->cfg.window;
+  const int64_t all = one * e->cfg.max_units;
+  const int64_t split = 16ll * e->nsm * std::min<int64_t>(one, 32);
+  return split + (shared ? 2 * all + 2ll * e->nsm * std::min<int64_t>(all, 256) : 0);
 }
 // Counters of split units: one per unit and 32 query rows.
 int64_t part_counts(const rkv_engine* e) {
@@ -102,7 +104,7 @@ int attend_scratch(rkv_engine* e, float** buf, int64_t rows, bool logits, cudaSt
 // items): the cheapest count by waves of `slots` resident CTAs, a CTA costing its
 // groups and about `extra` more, at most `cap` and at least `least_groups` each.
 int pick_chunks(int64_t items, int64_t sum, int64_t nmax, int64_t slots, int64_t cap,
-                int64_t least_groups = 4, double extra = 4.0) {
+                int64_t least_groups, double extra) {
   const int64_t avg = std::max<int64_t>(1, (sum + items - 1) / std::max<int64_t>(items, 1));
   const int64_t most =
       std::min<int64_t>(std::max<int64_t>(1, cap), std::max<int64_t>(1, nmax / least_groups));
@@ -119,6 +121,34 @@ int pick_chunks(int64_t items, int64_t sum, int64_t nmax, int64_t slots, int64_t
     }
   }
   return static_cast<int>(best);
+}
+
+// Warps per CTA and chunks per unit of the attention over own rows, by what a CTA
+// costs in us: about 4 for its start and end, 0.7 (alone) to 1.4 (on a full SM) per
+// 16-row stage of a warp, and 2.5 and 0.12 per chunk for the join.  `resident`:
+// warps that the GPU holds at once.
+void pick_shape(int64_t items, int64_t sum, int64_t nmax, int64_t resident, int64_t cap,
+                int* warps, int* chunks) {
+  const int64_t avg = std::max<int64_t>(1, (sum + items - 1) / items);
+  double least = 1e300;
+  for (int w = 4; w >= 2; w -= 2)
+    for (int64_t c = 1; c <= std::min<int64_t>(std::max<int64_t>(1, cap),
+                                               std::max<int64_t>(1, nmax / w));
+         c += c < 16 ? 1 : c / 8) {
+      const int64_t gpc = (nmax + c - 1) / c;
+      const double ctas = static_cast<double>(items) * ((avg + gpc - 1) / gpc);
+      const double full = std::min(1.0, ctas * w / resident);
+      const double one = 4.0 + (c > 1 ? 2.5 + 0.12 * c : 0.0) +
+                         2.0 * static_cast<double>((std::min(gpc, avg) + w - 1) / w) *
+                             (0.7 + 0.7 * full);
+      const double waves = ctas * w / resident;
+      const double cost = waves <= 1.0 ? one : one * (waves + 0.4);
+      if (cost < least) {
+        least = cost;
+        *warps = w;
+        *chunks = static_cast<int>(c);
+      }
+    }
 }
 
 int check_prefix(const rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, int64_t* sum,
@@ -256,30 +286,13 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     gsum += g;
     gmax = std::max(gmax, g);
   }
-  const int64_t slots = std::max(1, 2 * e->nsm / rg);
-  const int own = pick_chunks(U, gsum, gmax, slots, cap / rows - (x ? 1 : 0));
-  p.maxch = own;
-  p.gpc = static_cast<int>((gmax + own - 1) / own);
-  JoinParams j = {};
-  const bool join = x || own > 1;   // rows have several parts
-  if (join) {
-    p.part_o = part_o;
-    p.part_ml = part_ml;
-    p.count = x ? nullptr : count;
-    j.rows = rows;
-    j.own_chunks = own;
-    j.own_o = part_o;
-    j.own_ml = part_ml;
-  }
+  int own = 1, warps = 4;
+  pick_shape(rg * static_cast<int64_t>(U), rg * gsum, gmax,
+             static_cast<int64_t>(attend_warps_per_sm(R)) * e->nsm, cap / rows - (x ? 1 : 0),
+             &warps, &own);
+  const int64_t used = own > 1 ? static_cast<int64_t>(own) * rows : 0;   // parts of own chunks
   cudaError_t err;
-  t_begin(e, RKV_KERNEL_ATTEND, st);
-  err = launch_attend(p, U, st);
-  t_end(e, st);
-  if (err != cudaSuccess) return cuda_fail(err);
-  ++e->launches;
-
   if (x) {
-    const int64_t used = static_cast<int64_t>(own) * rows;
     const int64_t mrows = static_cast<int64_t>(members) * R;
     // up to 32 query rows per prefix: HBM-bound, the same kernel as the own rows;
     // more: 128- or 256-row tiles on tcgen05
@@ -296,15 +309,17 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     pp.keep = nullptr;
     pp.pos = nullptr;
     pp.status = e->status;
-    const int64_t pslots = std::max<int64_t>(1, (wide ? 1 : 2) * e->nsm / blocks);
+    const int64_t pslots =
+        std::max<int64_t>(1, (wide ? 1 : attend_warps_per_sm(static_cast<int>(mrows)) / 4) *
+                                 e->nsm / blocks);
     pp.maxch = pick_chunks(x->num_prefixes, pg, pmax, pslots, (cap - used) / rows, wide ? 1 : 4,
                            wide ? 3.0 : 4.0);
     pp.gpc = static_cast<int>((pmax + pp.maxch - 1) / pp.maxch);
     pp.part_o = part_o + used * 128;
     pp.part_ml = part_ml + used;
-    j.pre_chunks = pp.maxch;
-    j.pre_o = pp.part_o;
-    j.pre_ml = pp.part_ml;
+    p.pre_chunks = pp.maxch;
+    p.pre_o = pp.part_o;
+    p.pre_ml = pp.part_ml;
     CUtensorMap kmap, vmap;
     if (wide && (make_map(e, &kmap, x->K, static_cast<uint64_t>(psum), kWideTile) != RKV_OK ||
                  make_map(e, &vmap, x->V, static_cast<uint64_t>(psum), kWideTile) != RKV_OK))
@@ -316,18 +331,23 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     if (err != cudaSuccess) return cuda_fail(err);
     ++e->launches;
   }
-  if (x) {
-    t_begin(e, RKV_KERNEL_JOIN, st);
-    err = launch_attend_join(p, j, st);
-    t_end(e, st);
-    if (err != cudaSuccess) return cuda_fail(err);
-    ++e->launches;
+  p.maxch = own;
+  p.gpc = static_cast<int>((gmax + own - 1) / own);
+  if (own > 1) {
+    p.part_o = part_o;
+    p.part_ml = part_ml;
+    p.count = count;
   }
-  if (a->acc_out && (join || !p.z)) {   // a unit of one chunk has done its weights
+  t_begin(e, RKV_KERNEL_ATTEND, st);
+  err = launch_attend(p, U, warps, st);
+  t_end(e, st);
+  if (err != cudaSuccess) return cuda_fail(err);
+  ++e->launches;
+  if (a->acc_out && (own > 1 || !p.z)) {   // a unit of one chunk has done its weights
     AttendParams pw = p;
     const int64_t all = (static_cast<int64_t>(L.nmax) + 31) / 32;
-    pw.maxch = pick_chunks(U, (L.T + 31) / 32 + U, std::max<int64_t>(all, 1), 2 * e->nsm,
-                           std::max<int64_t>(1, (static_cast<int64_t>(1) << 30) / U));
+    pw.maxch = pick_chunks(U, (L.T + 31) / 32 + U, std::max<int64_t>(all, 1), 3 * e->nsm,
+                           std::max<int64_t>(1, (static_cast<int64_t>(1) << 30) / U), 4, 4.0);
     pw.gpc = static_cast<int>((std::max<int64_t>(all, 1) + pw.maxch - 1) / pw.maxch);
     t_begin(e, RKV_KERNEL_WEIGHT, st);
     err = launch_attend_weights(pw, U, st);

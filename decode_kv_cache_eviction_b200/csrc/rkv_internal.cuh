@@ -319,7 +319,7 @@ struct AttendParams {
   float* acc_out;                // [T] or null
   float* part_o;                 // parts [.., 128], null: the chunk is the whole row
   float2* part_ml;               // parts' (maximum in log2 units, sum)
-  int* count;                    // [U * row groups] arrived chunks (0 between calls), or null
+  int* count;                    // [U * row groups] arrived chunks (0 between calls)
   float* z;                      // [T, gp] logits for the weights, or null
   int gp;                        // heads of a row of z: R rounded up to a power of two
   // shared prefixes
@@ -330,25 +330,20 @@ struct AttendParams {
   const int32_t* mem;            // units of each prefix, ascending
   const uint4* PK;
   const uint4* PV;
+  int pre_chunks;                // parts per query row that the prefix kernel left
+  const float* pre_o;            // [pre_chunks, U * R, 128], or null
+  const float2* pre_ml;
   int* status;
 };
-struct JoinParams {
-  int64_t rows;                  // U * R
-  int own_chunks, pre_chunks;
-  const float* own_o;            // [U, own_chunks, R, 128]
-  const float2* own_ml;
-  const float* pre_o;            // [pre_chunks, U * R, 128]
-  const float2* pre_ml;
-};
+int attend_warps_per_sm(int rows);   // resident warps of a launch with this many query rows
 cudaError_t attend_configure();
-cudaError_t launch_attend(const AttendParams& p, int U, cudaStream_t st);
+cudaError_t launch_attend(const AttendParams& p, int U, int warps, cudaStream_t st);
 cudaError_t launch_attend_prefix(const AttendParams& p, int P, int max_rows, cudaStream_t st);
 // Many query rows per prefix (tcgen05): 128-row K/V tiles, p.gpc tiles per chunk.
 constexpr int kWideTile = 128;
 cudaError_t wide_configure();
 cudaError_t launch_attend_wide(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                const AttendParams& p, int P, int max_rows, cudaStream_t st);
-cudaError_t launch_attend_join(const AttendParams& p, const JoinParams& j, cudaStream_t st);
 cudaError_t launch_attend_weights(const AttendParams& p, int U, cudaStream_t st);
 
 // ---------------------------------------------------------------- eviction by weight

@@ -253,7 +253,8 @@ typedef struct {
 /* Attention over the batch's own rows (K, V, tok_off; the batch's Q is not used).
  * Units may have any length from 0 to the engine's limit.  Sums are held in
  * fp32 and results do not depend on timing.  The first call allocates a scratch
- * of about 40 MB, kept until rkv_destroy (RKV_ERR_OOM if that fails;
+ * of at most 40 MB (with acc_out, one query per head and G <= 8 also that of
+ * rkv_refree_budget), kept until rkv_destroy (RKV_ERR_OOM if that fails;
  * RKV_ERR_INVALID_ARG if `stream` is being captured then: make one call before a
  * capture).  Runs on the engine's device, whichever is current.  Captured calls
  * share the engine's scratch like eager ones: replays must be ordered with the
@@ -282,8 +283,8 @@ typedef struct {
  * row j sits at position j, own row i at prefix length + i (or pos[row]), and
  * the newest query at prefix length + N_u - 1 (or q_pos[u]).  All prefix rows are
  * live; keep, acc_in and acc_out cover the own rows (weights are those of the
- * softmax over both parts).  The first call allocates a scratch of
- * 520 * max(2 max_units G w, 75776) bytes, under the same conditions. */
+ * softmax over both parts).  The first call allocates a scratch of about
+ * 1040 max_units G w bytes and at most 80 MB, under the same conditions. */
 int rkv_attend_shared(rkv_engine* eng, const rkv_batch* batch, const rkv_prefix* prefix,
                       const rkv_attention* att, rkv_stream_t stream);
 
@@ -406,12 +407,11 @@ enum {
   RKV_KERNEL_FILL = 6,    /* new tokens into free slots */
   RKV_KERNEL_REFREE = 7,  /* adaptive budget (newest query's attention row) */
   RKV_KERNEL_FINISH = 8,  /* symmetric GEMM form: partial sums -> m, token softmax -> r */
-  RKV_KERNEL_ATTEND = 9,  /* attention over the units' own rows */
+  RKV_KERNEL_ATTEND = 9,  /* attention over the units' own rows, parts joined */
   RKV_KERNEL_SHARED = 10, /* attention over shared prefixes */
-  RKV_KERNEL_JOIN = 11,   /* parts of split rows joined */
-  RKV_KERNEL_WEIGHT = 12, /* accumulated attention weights */
-  RKV_KERNEL_DROP = 13,   /* eviction by accumulated weight */
-  RKV_NUM_KERNELS = 14
+  RKV_KERNEL_WEIGHT = 11, /* accumulated attention weights (a pass of their own) */
+  RKV_KERNEL_DROP = 12,   /* eviction by accumulated weight */
+  RKV_NUM_KERNELS = 13
 };
 
 /* Per-kernel timing.  While enabled, the engine records a pair of CUDA events
