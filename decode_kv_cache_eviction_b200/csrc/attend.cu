@@ -168,7 +168,7 @@ __device__ __forceinline__ RowSum join_row(RowSum s, int n, At at) {
 // product met a value that is not finite, which need not be one that they see.
 __device__ __noinline__ RowSum prefix_row(const AttendParams& p, int64_t row, int u, int r) {
   const int lane = threadIdx.x & 31;
-  const int x = p.unit_prefix[u];
+  const int x = p.unit_prefix ? p.unit_prefix[u] : u;
   const int64_t base = p.pre_off[x];
   const int N = static_cast<int>(p.pre_off[x + 1] - base);
   const int qp = clamp32(newest_query(p, u) - (p.nq - 1) + r % p.nq);
@@ -199,7 +199,7 @@ __device__ __noinline__ RowSum prefix_row(const AttendParams& p, int64_t row, in
 
 // Joins the parts that the prefix kernel left for a query row of unit u.
 __device__ __forceinline__ RowSum join_prefix(const AttendParams& p, RowSum s, int64_t row, int u) {
-  if (!p.pre_o || __ldg(&p.unit_prefix[u]) < 0) return s;
+  if (!p.pre_o || (p.unit_prefix && __ldg(&p.unit_prefix[u]) < 0)) return s;
   bool redo = false;
   for (int c = threadIdx.x & 31; c < p.pre_chunks; c += 32)
     redo |= __ldg(&p.pre_ml[c * p.rows + row]).y == kRedo;
@@ -819,6 +819,15 @@ __global__ void __launch_bounds__(256) weights_kernel(const AttendParams p) {
               static_cast<int>(min(static_cast<int64_t>(N), i0 + static_cast<int64_t>(p.gpc) * 32)));
 }
 
+// Query rows whose parts are all in p.pre_o: own rows that went through the wide
+// kernel, each unit as a prefix of its own.  One warp per query row.
+__global__ void __launch_bounds__(128) finish_kernel(const __grid_constant__ AttendParams p) {
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (row >= p.rows) return;
+  const RowSum x = join_prefix(p, no_rows(), row, static_cast<int>(row / p.R));
+  attend_store(p, row, threadIdx.x & 31, x.M, x.L, x.o);
+}
+
 template <int NB, int kMode, int W>
 __host__ __device__ constexpr int at_smem_bytes() {
   const int ring = W * AtCfg<NB>::kStages * at_stage_bytes<kMode>();
@@ -878,6 +887,11 @@ cudaError_t launch_attend(const AttendParams& p, int U, int warps, cudaStream_t 
 cudaError_t launch_attend_prefix(const AttendParams& p, int P, int max_rows, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(P) * p.maxch, (max_rows + 31) / 32);
   return launch_mode<kPrefix, 4>(p, max_rows, grid, st);
+}
+
+cudaError_t launch_attend_finish(const AttendParams& p, cudaStream_t st) {
+  finish_kernel<<<static_cast<unsigned>((p.rows + 3) / 4), 128, 0, st>>>(p);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_attend_weights(const AttendParams& p, int U, cudaStream_t st) {

@@ -24,7 +24,7 @@
 // product needs V's type, and a second part would cost half as many MMAs again.
 //
 // Bound: at 256 rows and d = 128 a token tile takes 2048 tensor-core cycles and as
-// many for its 2^x (16 per cycle and SM).
+// many for its 2^x (16 per cycle and SM); three in eight of those run on the FMA pipe.
 //
 // Roles: warp 0 TMA producer, warp 1 MMA issuer (one lane each), warps 4-7 and
 // 8-11 the rows of the first and second query tile.  Every wait is bounded.
@@ -50,10 +50,35 @@ struct WideLayout {
   static constexpr uint32_t ring = QT * kTileB;
   static constexpr uint32_t qp = ring + kStages * kTileB;      // [QT * 128]
   static constexpr uint32_t bars = qp + QT * kWTile * 4;
-  static constexpr uint32_t misc = bars + (2 * kStages + 3 * 2 + 1) * 8;
+  static constexpr uint32_t misc = bars + (2 * kStages + 4 * 2 + 1) * 8;
   static constexpr uint32_t total = misc + 48;
   static constexpr uint32_t alloc = total + 1024;               // base aligned to 1024
 };
+
+// 2^x for a pair of x in [-126, 127] on the FMA pipe (2^x has 16 lanes' worth of its
+// own per cycle and SM, as many as the tensor cores leave for it).  x = n + f with n
+// the nearest whole number, added as 1.5 2^23 + n so that its low bits are n; a
+// polynomial of degree 4 for 2^f, |f| <= 1/2, fitted for the smallest largest
+// relative error, 2.6e-6 (2^-18.5: far below the rounding to bf16 that follows); n is
+// added to the exponent.  Smaller x give 2^-126; NaN is caught by the row's maximum.
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
+  float x0, x1;
+  unpair(x, x0, x1);
+  x = pair(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
+  const uint64_t t = add_pair(x, pair(12582912.f, 12582912.f));
+  const uint64_t n = add_pair(t, pair(-12582912.f, -12582912.f));
+  const uint64_t f = fma_pair(n, pair(-1.f, -1.f), x);
+  uint64_t y = pair(0.009570101276040077f, 0.009570101276040077f);
+  y = fma_pair(y, f, pair(0.05591785907745361f, 0.05591785907745361f));
+  y = fma_pair(y, f, pair(0.240247443318367f, 0.240247443318367f));
+  y = fma_pair(y, f, pair(0.6931217908859253f, 0.6931217908859253f));
+  y = fma_pair(y, f, pair(0.9999992847442627f, 0.9999992847442627f));
+  float t0, t1, y0, y1;
+  unpair(t, t0, t1);
+  unpair(y, y0, y1);
+  return pair(__uint_as_float(__float_as_uint(y0) + (__float_as_uint(t0) << 23)),
+              __uint_as_float(__float_as_uint(y1) + (__float_as_uint(t1) << 23)));
+}
 
 // Teardown: wait (bounded, regardless of an abort) for a phase that is under way.
 __device__ __forceinline__ void wide_drain(uint64_t* bar, uint32_t par) {
@@ -75,8 +100,8 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + Lay::bars);
   uint64_t* empty = full + NS;
   uint64_t* s_full = empty + NS;    // [2] S of a query tile is in tensor memory
-  uint64_t* p_full = s_full + 2;    // [2] its p is
-  uint64_t* o_done = p_full + 2;    // [2] its product with V is done
+  uint64_t* p_full = s_full + 2;    // [2][2] its p is, the halves of 64 tokens
+  uint64_t* o_done = p_full + 4;    // [2] its product with V is done
   uint64_t* mdone = o_done + 2;     // teardown: every MMA has completed
   int* s_qp = reinterpret_cast<int*>(sm + Lay::qp);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Lay::misc);
@@ -89,14 +114,10 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
   const int row0 = blockIdx.y * QT * kWTile;
   const int64_t base = __ldg(&p.pre_off[item]);
   const int N = static_cast<int>(__ldg(&p.pre_off[item + 1]) - base);
-  const int mo = __ldg(&p.mem_off[item]);
-  const int total = (__ldg(&p.mem_off[item + 1]) - mo) * p.R;
+  const int mo = p.mem ? __ldg(&p.mem_off[item]) : item;
+  const int total = p.mem ? (__ldg(&p.mem_off[item + 1]) - mo) * p.R : p.R;
   if (row0 >= total) return;
   const int nrow = min(QT * kWTile, total - row0);
-  auto row_of = [&](int r) -> int64_t {
-    const int m = (row0 + r) / p.R;
-    return static_cast<int64_t>(__ldg(&p.mem[mo + m])) * p.R + (row0 + r - m * p.R);
-  };
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -106,7 +127,8 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&p_full[2 * i], 4);       // warps
+      mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&o_done[i], 1);
     }
     mbar_init(mdone, 1);
@@ -116,17 +138,19 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
     fence_mbar_init();
   }
   __syncthreads();
+  int* s_row = reinterpret_cast<int*>(sm + Lay::ring);   // rows of Q (before the ring fills)
   for (int r = tid; r < QT * kWTile; r += kThreads) {
-    int v = INT_MIN;
+    int v = INT_MIN, row = -1;
     if (r < nrow) {
-      const int64_t rr = row_of(r);
-      const int u = static_cast<int>(rr / p.R);
-      const int t = static_cast<int>(rr - static_cast<int64_t>(u) * p.R) % p.nq;
-      v = clamp32(newest_query(p, u) - (p.nq - 1) + t);
+      const int k = (row0 + r) / p.R, x = row0 + r - k * p.R;
+      const int u = p.mem ? __ldg(&p.mem[mo + k]) : item;
+      row = u * p.R + x;
+      v = clamp32(newest_query(p, u) - (p.nq - 1) + x % p.nq);
       atomicMin(&s_lim[0], v);
       atomicMax(&s_lim[1], v);
     }
     s_qp[r] = v;
+    s_row[r] = row;
   }
   __syncthreads();
   const int qmin = s_lim[0], qmax = s_lim[1];
@@ -134,14 +158,18 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
   const int v0 = chunk * p.gpc, nt = min(sp.nv, v0 + p.gpc) - v0;   // token tiles of this CTA
   if (nt <= 0) {
     for (int r = tid; r < nrow; r += kThreads)
-      p.part_ml[static_cast<int64_t>(chunk) * p.rows + row_of(r)] = make_float2(-INFINITY, 0.f);
+      p.part_ml[static_cast<int64_t>(chunk) * p.rows + s_row[r]] = make_float2(-INFINITY, 0.f);
     return;
   }
+  const int r_mine = warp >= 4 ? (warp - 4) * 32 + lane : 0;   // this thread's query row
+  const int row = s_row[r_mine];
   // query rows into the layout that TMA writes for K (zeros past the last row)
+#pragma unroll 4
   for (int i = tid; i < QT * kWTile * 16; i += kThreads) {
     const int r = i >> 4, c = i & 15;
     uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (r < nrow) x = __ldg(reinterpret_cast<const uint4*>(p.Q) + row_of(r) * 16 + c);
+    if (r < nrow)
+      x = __ldg(reinterpret_cast<const uint4*>(p.Q) + static_cast<int64_t>(s_row[r]) * 16 + c);
     const int rt = r & (kWTile - 1);
     *reinterpret_cast<uint4*>(sm + Lay::q + (r / kWTile) * kTileB + (c >> 3) * kHalfB + rt * 128 +
                               (((c & 7) ^ (rt & 7)) << 4)) = x;
@@ -198,13 +226,12 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
         }
         mma_commit(&s_full[t]);
       };
-      auto product = [&](int t, int j) {   // O_t += p_t V_j
+      auto product = [&](int t, int j, int half) {   // O_t += p_t V_j over 64 tokens
         const uint32_t va = slot(2 * j + 1);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 4 * half; k < 4 * half + 4; ++k)
           mma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * k,
                       desc_mnmajor_sw128(va + k * 2048, kHalfB), id_o, j > 0 || k > 0);
-        mma_commit(&o_done[t]);
       };
       bool ok = wait_tile(0);
       tc_fence_after();
@@ -216,10 +243,15 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
         ok = wait_tile(2 * j + 1);
         const bool more = j + 1 < nt;
         for (int t = 0; ok && t < QT; ++t) {
-          ok = mbar_wait(&p_full[t], j & 1, abort, p.status);
+          for (int half = 0; ok && half < 2; ++half) {
+            ok = mbar_wait(&p_full[2 * t + half], j & 1, abort, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            if (half == 0) product(t, j, 0);
+            else product(t, j, 1);
+          }
           if (!ok) break;
-          tc_fence_after();
-          product(t, j);
+          mma_commit(&o_done[t]);
           if (t == QT - 1) mma_commit(&empty[(2 * j + 1) % NS]);
           if (more) {
             if (t == 0) ok = wait_tile(2 * j + 2);
@@ -238,7 +270,7 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
   } else if (warp >= 4) {
     // ------------------------------------------------------------ rows
     const int t = (warp - 4) >> 2;               // query tile
-    const int r = t * kWTile + (warp & 3) * 32 + lane;
+    const int r = r_mine;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
     const int qp = s_qp[r];
@@ -247,7 +279,7 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
     const int lo_all = p.local > 0 ? clamp32(static_cast<int64_t>(qmax) - p.local) : INT_MIN;
     const float scale = p.scale_log2;
     float m = -INFINITY, l = 0.f;
-    bool ok = true;
+    bool ok = true, odd = false;
     for (int j = 0; ok && j < nt; ++j) {
       const int t0 = sp.group(v0 + j) * kWTile;
       ok = mbar_wait(&s_full[t], j & 1, abort, p.status);
@@ -275,9 +307,13 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
       for (int k = 0; k < 4; ++k) {
         mx[k] = __uint_as_float(s[k][0]);
 #pragma unroll
-        for (int c = 1; c < 32; ++c) mx[k] = fmaxf(mx[k], __uint_as_float(s[k][c]));
+        for (int c = 1; c < 31; c += 2)
+          mx[k] = max3_nan(mx[k], __uint_as_float(s[k][c]), __uint_as_float(s[k][c + 1]));
+        mx[k] = max3_nan(mx[k], mx[k], __uint_as_float(s[k][31]));
       }
-      const float top = fmaxf(m, scale * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+      const float high = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]);
+      odd = odd || !(high < INFINITY);   // NaN or +inf: the row is done again
+      const float top = fmaxf(m, scale * high);
       const bool grew = top > m + kSlack;   // from -inf too
       if (__any_sync(0xffffffffu, grew)) {
         const float f = grew ? ex2(m - top) : 1.f;   // 0 from -inf: O and l are 0 then
@@ -300,32 +336,48 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
         }
       }
       const float ref = m == -INFINITY ? 0.f : m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint64_t scale2 = pair(scale, scale), ref2 = pair(-ref, -ref);
+      uint64_t sum[2] = {0ull, 0ull};   // pairs of +0
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t w[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          const float x = ex2(fmaf(__uint_as_float(s[k][2 * c]), scale, -ref));
-          const float y = ex2(fmaf(__uint_as_float(s[k][2 * c + 1]), scale, -ref));
-          sum[c & 3] += x + y;
-          w[c] = pack_bf16(x, y);
+          const uint64_t x = fma_pair(
+              pair(__uint_as_float(s[k][2 * c]), __uint_as_float(s[k][2 * c + 1])), scale2, ref2);
+          float a, b;
+          // 6 of 16 pairs on the FMA pipe
+          if (c % 8 == 1 || c % 8 == 3 || c % 8 == 6) {
+            unpair(exp2_pair(x), a, b);
+          } else {
+            unpair(x, a, b);
+            a = ex2(a);
+            b = ex2(b);
+          }
+          sum[c & 1] = add_pair(sum[c & 1], pair(a, b));
+          w[c] = pack_bf16(a, b);
         }
         tmem_st16(ts + 16 * k, w);
+        if (k & 1) {   // 64 tokens: their product with V can start
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * t + (k >> 1)]);
+        }
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&p_full[t]);
+      float a, b;
+      unpair(add_pair(sum[0], sum[1]), a, b);
+      l += a + b;
     }
     // the row's part
+    if (m == -INFINITY) l = 0.f;   // a row that saw nothing (each unseen 2^x may be 2^-126)
     if (ok) ok = mbar_wait(&o_done[t], (nt - 1) & 1, abort, p.status);
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
       tc_fence_after();
       const bool mine = r < nrow;
-      const int64_t at = static_cast<int64_t>(chunk) * p.rows + (mine ? row_of(r) : 0);
-      bool fin = (__float_as_uint(l) & 0x7f800000u) != 0x7f800000u;
+      const int64_t at = static_cast<int64_t>(chunk) * p.rows + (mine ? row : 0);
+      bool fin = !odd && (__float_as_uint(l) & 0x7f800000u) != 0x7f800000u;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t o[32];

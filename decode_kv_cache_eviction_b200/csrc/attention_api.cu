@@ -196,13 +196,13 @@ int check_prefix(const rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, i
   return RKV_OK;
 }
 
-// Groups of a sequence of n rows that a window of `local` tokens and the sinks
-// can touch, at most.
-int64_t reach(int64_t n, int local, int sinks, int nq) {
-  const int64_t all = (n + 31) / 32;
+// Groups of `per` rows of a sequence of n that a window of `local` tokens and the
+// sinks can touch, at most.
+int64_t reach(int64_t n, int local, int sinks, int nq, int64_t per = 32) {
+  const int64_t all = (n + per - 1) / per;
   if (local <= 0) return all;
-  return std::min<int64_t>(all, (static_cast<int64_t>(sinks) + 31) / 32 +
-                                    (static_cast<int64_t>(local) + nq) / 32 + 2);
+  return std::min<int64_t>(all, (static_cast<int64_t>(sinks) + per - 1) / per +
+                                    (static_cast<int64_t>(local) + nq) / per + 2);
 }
 
 int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_attention* a,
@@ -331,18 +331,57 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     if (err != cudaSuccess) return cuda_fail(err);
     ++e->launches;
   }
-  p.maxch = own;
-  p.gpc = static_cast<int>((gmax + own - 1) / own);
-  if (own > 1) {
-    p.part_o = part_o;
-    p.part_ml = part_ml;
-    p.count = count;
+  // many query rows over whole units: each unit goes through the wide kernel as a
+  // prefix of its own
+  const bool wide_own = !x && R > 16 && !a->keep && !a->pos && L.T >= 512ll * U;
+  if (wide_own) {
+    const int64_t blocks = (R + 255) / 256;
+    int64_t tsum = 0, tmax = 1;
+    for (int u = 0; u < U; ++u) {
+      const int64_t n = b->tok_off_host[u + 1] - b->tok_off_host[u];
+      const int64_t t = reach(n, a->local, a->sinks, p.nq, kWideTile);
+      tsum += t;
+      tmax = std::max(tmax, t);
+    }
+    p.PK = p.K;
+    p.PV = p.V;
+    p.pre_off = p.tok_off;
+    p.maxch = pick_chunks(U, tsum, tmax, std::max<int64_t>(1, e->nsm / blocks), cap / rows, 1, 3.0);
+    if (static_cast<int64_t>(p.maxch) * rows <= cap) {
+      p.gpc = static_cast<int>((tmax + p.maxch - 1) / p.maxch);
+      p.part_o = part_o;
+      p.part_ml = part_ml;
+      p.status = e->status;
+      CUtensorMap kmap, vmap;
+      if (make_map(e, &kmap, b->K, static_cast<uint64_t>(L.T), kWideTile) != RKV_OK ||
+          make_map(e, &vmap, b->V, static_cast<uint64_t>(L.T), kWideTile) != RKV_OK)
+        return RKV_ERR_CUDA;
+      t_begin(e, RKV_KERNEL_ATTEND, st);
+      err = launch_attend_wide(kmap, vmap, p, U, R, st);
+      p.pre_chunks = p.maxch;
+      p.pre_o = part_o;
+      p.pre_ml = part_ml;
+      p.part_o = nullptr;
+      if (err == cudaSuccess) err = launch_attend_finish(p, st);
+      t_end(e, st);
+      if (err != cudaSuccess) return cuda_fail(err);
+      e->launches += 2;
+    }
   }
-  t_begin(e, RKV_KERNEL_ATTEND, st);
-  err = launch_attend(p, U, warps, st);
-  t_end(e, st);
-  if (err != cudaSuccess) return cuda_fail(err);
-  ++e->launches;
+  if (!wide_own || !p.pre_o) {
+    p.maxch = own;
+    p.gpc = static_cast<int>((gmax + own - 1) / own);
+    if (own > 1) {
+      p.part_o = part_o;
+      p.part_ml = part_ml;
+      p.count = count;
+    }
+    t_begin(e, RKV_KERNEL_ATTEND, st);
+    err = launch_attend(p, U, warps, st);
+    t_end(e, st);
+    if (err != cudaSuccess) return cuda_fail(err);
+    ++e->launches;
+  }
   if (a->acc_out && (own > 1 || !p.z)) {   // a unit of one chunk has done its weights
     AttendParams pw = p;
     const int64_t all = (static_cast<int64_t>(L.nmax) + 31) / 32;

@@ -327,7 +327,7 @@ struct AttendParams {
   const int32_t* unit_prefix;    // [U] or null
   const int64_t* pre_off;        // [P+1]
   const int32_t* mem_off;        // [P+1]
-  const int32_t* mem;            // units of each prefix, ascending
+  const int32_t* mem;            // units of each prefix, ascending; null: item i is unit i
   const uint4* PK;
   const uint4* PV;
   int pre_chunks;                // parts per query row that the prefix kernel left
@@ -344,6 +344,7 @@ constexpr int kWideTile = 128;
 cudaError_t wide_configure();
 cudaError_t launch_attend_wide(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                const AttendParams& p, int P, int max_rows, cudaStream_t st);
+cudaError_t launch_attend_finish(const AttendParams& p, cudaStream_t st);
 cudaError_t launch_attend_weights(const AttendParams& p, int U, cudaStream_t st);
 
 // ---------------------------------------------------------------- eviction by weight
