@@ -1,32 +1,35 @@
 // Attention of many query rows over a shared prefix: all queries of a prefix's
-// units against its K and V at once, on the tensor cores.
+// units against its K and V at once, on the tensor cores.  (A unit of many query
+// rows of its own is a prefix with itself as its only unit.)
 //
 // A CTA takes 128 or 256 query rows (one or two tiles of 128, gathered from their
-// units) and a run of 128-token tiles of the prefix:
+// units) and a run of 128-token tiles of the prefix, in steps of 64 tokens:
 //   S = Q K^T        tcgen05.mma, Q and K from shared memory (128-byte swizzle),
 //                    S in tensor memory: lane = query row, column = token;
 //   p = 2^(S - m)    one thread per query row: no exchange between threads for the
 //                    maximum and the sum; p goes back over S as bf16;
 //   O += p V         tcgen05.mma with p as the A operand from tensor memory and V
 //                    (token rows) as an MN-major B operand: V is never transposed.
-// With two query tiles their steps alternate, S0 PV0 S1 PV1, so that the tensor
-// cores work on one tile while the other's p is formed, and each K/V tile in shared
-// memory serves 256 query rows.  The MMAs of one thread run in the order of their
-// issue; S of the next token tile, written over p, therefore follows the product
-// that reads p.
+// Each query tile has two S buffers of 64 tokens, so the next S is computed while p
+// is formed from the last: with one buffer of 128 tokens a tile's S, p and product
+// followed each other, 3800 cycles per 128 tokens, although 64-token products read
+// Q more often (N = 64 takes 3/4 of the time of N = 128).  The MMAs of one thread run
+// in the order of their issue; S of a later step, written over p, therefore follows
+// the product that reads p.
 //
 // The running maximum m is moved (and O, l rescaled by the same thread) only when
 // a row's maximum has grown by more than 2^8: p, l and O stay well inside fp32 and
 // bf16's relative precision does not depend on the scale, so the result is the
-// same and most tiles need no pass over O.
+// same and most steps need no pass over O.
 //
-// p is rounded to bf16 (2^-9 relative, once per weight, of random sign): the
+// p is rounded to bf16 (2^-8 relative at most, once per weight, of random sign): the
 // product needs V's type, and a second part would cost half as many MMAs again.
 //
-// Bound: at 256 rows and d = 128 a token tile takes 2048 tensor-core cycles and as
+// Bound: at 256 rows and d = 128 a 128-token tile takes 2048 tensor-core cycles and as
 // many for its 2^x (16 per cycle and SM); three in eight of those run on the FMA pipe.
+// With one tile of rows it is HBM.
 //
-// Roles: warp 0 TMA producer, warp 1 MMA issuer (one lane each), warps 4-7 and
+// Roles: warp 0 TMA producer (one lane), warp 1 MMA issuer, warps 4-7 and
 // 8-11 the rows of the first and second query tile.  Every wait is bounded.
 //
 // A row whose result is not finite is marked and computed again, token by token,
@@ -48,10 +51,10 @@ struct WideLayout {
   static constexpr int kStages = QT == 2 ? 5 : 6;   // K and V tiles in turn
   static constexpr uint32_t q = 0;
   static constexpr uint32_t ring = QT * kTileB;
-  static constexpr uint32_t qp = ring + kStages * kTileB;      // [QT * 128]
-  static constexpr uint32_t bars = qp + QT * kWTile * 4;
-  static constexpr uint32_t misc = bars + (2 * kStages + 4 * 2 + 1) * 8;
-  static constexpr uint32_t total = misc + 48;
+  static constexpr uint32_t row = ring + kStages * kTileB;      // [QT * 128] rows of Q
+  static constexpr uint32_t bars = row + QT * kWTile * 4;
+  static constexpr uint32_t misc = bars + (2 * kStages + 14) * 8;
+  static constexpr uint32_t total = misc + 96;
   static constexpr uint32_t alloc = total + 1024;               // base aligned to 1024
 };
 
@@ -99,15 +102,16 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
   uint8_t* sm = wide_raw + ((1024u - (smem_u32(wide_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + Lay::bars);
   uint64_t* empty = full + NS;
-  uint64_t* s_full = empty + NS;    // [2] S of a query tile is in tensor memory
-  uint64_t* p_full = s_full + 2;    // [2][2] its p is, the halves of 64 tokens
-  uint64_t* o_done = p_full + 4;    // [2] its product with V is done
-  uint64_t* mdone = o_done + 2;     // teardown: every MMA has completed
-  int* s_qp = reinterpret_cast<int*>(sm + Lay::qp);
+  uint64_t* s_full = empty + NS;    // [tile][buffer] S is in tensor memory
+  uint64_t* p_full = s_full + 4;    // [tile][buffer] p is
+  uint64_t* o_done = p_full + 4;    // [tile][buffer] its product with V is done
+  uint64_t* q_full = o_done + 4;    // Q is in shared memory
+  uint64_t* mdone = q_full + 1;     // teardown: every MMA has completed
+  int* s_row = reinterpret_cast<int*>(sm + Lay::row);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Lay::misc);
   volatile int* abort = reinterpret_cast<volatile int*>(sm + Lay::misc + 4);
-  int* s_lim = reinterpret_cast<int*>(sm + Lay::misc + 8);            // smallest, largest qp
-  int8_t* lastp = reinterpret_cast<int8_t*>(sm + Lay::misc + 16);     // [NS] parity of the last copy
+  int8_t* lastp = reinterpret_cast<int8_t*>(sm + Lay::misc + 8);      // [NS] parity of the last copy
+  int* s_lim = reinterpret_cast<int*>(sm + Lay::misc + 16);           // [warp][2] smallest, largest qp
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   const int item = blockIdx.x / p.maxch, chunk = blockIdx.x - item * p.maxch;
@@ -119,70 +123,73 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
   if (row0 >= total) return;
   const int nrow = min(QT * kWTile, total - row0);
 
-  if (tid == 0) {
+  const int r = tid - 128;   // this thread's query row (warps 4 and up)
+  int row = -1, qp = INT_MIN;
+  if (warp >= 4) {
+    if (r < nrow) {
+      const int k = (row0 + r) / p.R, x = row0 + r - k * p.R;
+      const int u = p.mem ? __ldg(&p.mem[mo + k]) : item;
+      row = u * p.R + x;
+      qp = clamp32(newest_query(p, u) - (p.nq - 1) + x % p.nq);
+    }
+    s_row[r] = row;
+    const int lo = __reduce_min_sync(0xffffffffu, r < nrow ? qp : INT_MAX);
+    const int hi = __reduce_max_sync(0xffffffffu, qp);
+    if (lane == 0) {
+      s_lim[2 * (warp - 4)] = lo;
+      s_lim[2 * (warp - 4) + 1] = hi;
+    }
+  } else if (warp == 1) {
+    tmem_alloc<1>(tmem_slot, 512);
+    tmem_relinquish<1>();
+  } else if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
       lastp[s] = -1;
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[2 * i], 4);       // warps
-      mbar_init(&p_full[2 * i + 1], 4);
+      mbar_init(&p_full[i], 4);       // warps
       mbar_init(&o_done[i], 1);
     }
+    mbar_init(q_full, kThreads / 32 - 2);
     mbar_init(mdone, 1);
     *abort = 0;
-    s_lim[0] = INT_MAX;
-    s_lim[1] = INT_MIN;
     fence_mbar_init();
-  }
-  __syncthreads();
-  int* s_row = reinterpret_cast<int*>(sm + Lay::ring);   // rows of Q (before the ring fills)
-  for (int r = tid; r < QT * kWTile; r += kThreads) {
-    int v = INT_MIN, row = -1;
-    if (r < nrow) {
-      const int k = (row0 + r) / p.R, x = row0 + r - k * p.R;
-      const int u = p.mem ? __ldg(&p.mem[mo + k]) : item;
-      row = u * p.R + x;
-      v = clamp32(newest_query(p, u) - (p.nq - 1) + x % p.nq);
-      atomicMin(&s_lim[0], v);
-      atomicMax(&s_lim[1], v);
-    }
-    s_qp[r] = v;
-    s_row[r] = row;
-  }
-  __syncthreads();
-  const int qmin = s_lim[0], qmax = s_lim[1];
-  const Span sp = visible_span<7>(N, 0, qmin, qmax, p.local, p.sinks);
-  const int v0 = chunk * p.gpc, nt = min(sp.nv, v0 + p.gpc) - v0;   // token tiles of this CTA
-  if (nt <= 0) {
-    for (int r = tid; r < nrow; r += kThreads)
-      p.part_ml[static_cast<int64_t>(chunk) * p.rows + s_row[r]] = make_float2(-INFINITY, 0.f);
-    return;
-  }
-  const int r_mine = warp >= 4 ? (warp - 4) * 32 + lane : 0;   // this thread's query row
-  const int row = s_row[r_mine];
-  // query rows into the layout that TMA writes for K (zeros past the last row)
-#pragma unroll 4
-  for (int i = tid; i < QT * kWTile * 16; i += kThreads) {
-    const int r = i >> 4, c = i & 15;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (r < nrow)
-      x = __ldg(reinterpret_cast<const uint4*>(p.Q) + static_cast<int64_t>(s_row[r]) * 16 + c);
-    const int rt = r & (kWTile - 1);
-    *reinterpret_cast<uint4*>(sm + Lay::q + (r / kWTile) * kTileB + (c >> 3) * kHalfB + rt * 128 +
-                              (((c & 7) ^ (rt & 7)) << 4)) = x;
-  }
-  fence_proxy_async_smem();
-  if (warp == 1) {
-    tmem_alloc<1>(tmem_slot, 512);
-    tmem_relinquish<1>();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;   // S0, S1, O0, O1: 128 columns each
+  const uint32_t tmem = *tmem_slot;   // S of tile t, buffer h: 128 t + 64 h; O: 256 + 128 t
+  int qmin = INT_MAX, qmax = INT_MIN;
+#pragma unroll
+  for (int w = 0; w < 4 * QT; ++w) {
+    qmin = min(qmin, s_lim[2 * w]);
+    qmax = max(qmax, s_lim[2 * w + 1]);
+  }
+  const Span sp = visible_span<7>(N, 0, qmin, qmax, p.local, p.sinks);
+  const int v0 = chunk * p.gpc, nt = min(sp.nv, v0 + p.gpc) - v0;   // token tiles of this CTA
+  if (nt <= 0) {
+    if (row >= 0) p.part_ml[static_cast<int64_t>(chunk) * p.rows + row] = make_float2(-INFINITY, 0.f);
+    if (warp == 1) tmem_dealloc<1>(tmem, 512);
+    return;
+  }
+  if (warp >= 2) {
+    // query rows into the layout that TMA writes for K (zeros past the last row)
+#pragma unroll 8
+    for (int i = tid - 64; i < QT * kWTile * 16; i += kThreads - 64) {
+      const int x = i >> 4, c = i & 15, xt = x & (kWTile - 1);
+      const int src = s_row[x];
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (src >= 0) v = __ldg(reinterpret_cast<const uint4*>(p.Q) + static_cast<int64_t>(src) * 16 + c);
+      *reinterpret_cast<uint4*>(sm + Lay::q + (x / kWTile) * kTileB + (c >> 3) * kHalfB + xt * 128 +
+                                (((c & 7) ^ (xt & 7)) << 4)) = v;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_full);
+  }
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -209,93 +216,115 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t id_s = idesc_bf16_f32(128, 128);
-      const uint32_t id_o = idesc_bf16_f32(128, 128) | kIdescTransposeB;
-      auto slot = [&](int i) { return smem_u32(sm + Lay::ring + (i % NS) * kTileB); };
-      auto wait_tile = [&](int i) {
-        return mbar_wait(&full[i % NS], (i / NS) & 1, abort, p.status);
-      };
-      auto scores = [&](int t, int j) {   // S_t = Q_t K_j^T
-        const uint32_t qa = smem_u32(sm + Lay::q + t * kTileB), ka = slot(2 * j);
+    // (the whole warp runs this; one lane issues)
+    const uint32_t leader = elect_leader();
+    const uint32_t id_s = idesc_bf16_f32(128, 64);
+    const uint32_t id_o = idesc_bf16_f32(128, 128) | kIdescTransposeB;
+    const uint64_t qd = desc_kmajor_sw128(smem_u32(sm + Lay::q));
+    const uint64_t kd = desc_kmajor_sw128(smem_u32(sm + Lay::ring));
+    const uint64_t vd = desc_mnmajor_sw128(smem_u32(sm + Lay::ring), kHalfB);
+    const uint32_t a_sfull = smem_u32(s_full), a_odone = smem_u32(o_done), a_empty = smem_u32(empty);
+    // addresses in a descriptor count 16 bytes
+    auto scores = [&](int t, int i, int ks) {   // S_t of step i, K tile in ring slot ks
+        const uint64_t a = qd + t * (kTileB >> 4);
+        const uint64_t b = kd + ks * (kTileB >> 4) + (i & 1) * (64 * 128 >> 4);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint32_t o = (k >> 2) * kHalfB + (k & 3) * 32;
-          mma_bf16<1>(tmem + t * 128, desc_kmajor_sw128(qa + o), desc_kmajor_sw128(ka + o), id_s,
-                      k > 0);
+          const uint32_t o = ((k >> 2) * kHalfB + (k & 3) * 32) >> 4;
+          mma_bf16_by(leader, tmem + t * 128 + (i & 1) * 64, a + o, b + o, id_s, k > 0);
         }
-        mma_commit(&s_full[t]);
-      };
-      auto product = [&](int t, int j, int half) {   // O_t += p_t V_j over 64 tokens
-        const uint32_t va = slot(2 * j + 1);
+        mma_commit_by(leader, a_sfull + 8 * (2 * t + (i & 1)));
+    };
+    auto product = [&](int t, int i, int vs) {   // O_t += p_t V of step i, V tile in slot vs
+        const uint64_t b = vd + vs * (kTileB >> 4) + (i & 1) * (64 * 128 >> 4);
 #pragma unroll
-        for (int k = 4 * half; k < 4 * half + 4; ++k)
-          mma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * k,
-                      desc_mnmajor_sw128(va + k * 2048, kHalfB), id_o, j > 0 || k > 0);
-      };
-      bool ok = wait_tile(0);
-      tc_fence_after();
-      if (ok) {
-        for (int t = 0; t < QT; ++t) scores(t, 0);
-        mma_commit(&empty[0]);
+        for (int k = 0; k < 4; ++k)
+          mma_bf16_ts_by(leader, tmem + 256 + t * 128, tmem + t * 128 + (i & 1) * 64 + 8 * k,
+                         b + k * (2048 >> 4), id_o, i > 0 || k > 0);
+        mma_commit_by(leader, a_odone + 8 * (2 * t + (i & 1)));
+    };
+    // ring slots of the V tile in use and of the K tile after it, with their phases
+    int ks = 0, vs = 0;
+    uint32_t kph = 0, vph = 0;
+    auto next = [&](int& s, uint32_t& ph) {   // the slot after s
+      if (++s == NS) {
+        s = 0;
+        ph ^= 1;
       }
-      for (int j = 0; ok && j < nt; ++j) {
-        ok = wait_tile(2 * j + 1);
-        const bool more = j + 1 < nt;
-        for (int t = 0; ok && t < QT; ++t) {
-          for (int half = 0; ok && half < 2; ++half) {
-            ok = mbar_wait(&p_full[2 * t + half], j & 1, abort, p.status);
-            if (!ok) break;
-            tc_fence_after();
-            if (half == 0) product(t, j, 0);
-            else product(t, j, 1);
-          }
-          if (!ok) break;
-          mma_commit(&o_done[t]);
-          if (t == QT - 1) mma_commit(&empty[(2 * j + 1) % NS]);
-          if (more) {
-            if (t == 0) ok = wait_tile(2 * j + 2);
-            if (!ok) break;
-            tc_fence_after();
-            scores(t, j + 1);
-            if (t == QT - 1) mma_commit(&empty[(2 * j + 2) % NS]);
-          }
+    };
+    const int ni = 2 * nt;
+    bool ok = mbar_wait(q_full, 0, abort, p.status);
+    ok = ok && mbar_wait(&full[0], 0, abort, p.status);
+    ok = __all_sync(0xffffffffu, ok);
+    tc_fence_after();
+    if (ok) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int t = 0; t < QT; ++t) scores(t, i, 0);
+      mma_commit_by(leader, a_empty);
+    }
+    for (int i = 0; ok && i < ni; ++i) {
+      if ((i & 1) == 0) {
+        vs = ks;
+        vph = kph;
+        next(vs, vph);
+        ok = mbar_wait(&full[vs], vph, abort, p.status);
+        if (i + 2 < ni) {
+          ks = vs;
+          kph = vph;
+          next(ks, kph);
+          ok = ok && mbar_wait(&full[ks], kph, abort, p.status);
         }
       }
-      // teardown: all MMAs (and their commits) are complete before TMEM is freed
-      mma_commit(mdone);
-      wide_drain(mdone, 0);
+#pragma unroll
+      for (int t = 0; t < QT; ++t) {
+        ok = ok && mbar_wait(&p_full[2 * t + (i & 1)], (i >> 1) & 1, abort, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        product(t, i, vs);
+        if (t == QT - 1 && (i & 1)) mma_commit_by(leader, a_empty + 8 * vs);
+        if (i + 2 < ni) {
+          scores(t, i + 2, ks);
+          if (t == QT - 1 && (i & 1)) mma_commit_by(leader, a_empty + 8 * ks);
+        }
+      }
     }
+    // teardown: all MMAs (and their commits) are complete before TMEM is freed
+    mma_commit_by(leader, smem_u32(mdone));
+    wide_drain(mdone, 0);
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------ rows
     const int t = (warp - 4) >> 2;               // query tile
-    const int r = r_mine;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
-    const int qp = s_qp[r];
+    const uint32_t to = tmem + lanes + 256 + t * 128;
     const int lo = p.local > 0 ? clamp32(static_cast<int64_t>(qp) - p.local) : INT_MIN;
     const int hi = min(qp, N - 1);
     const int lo_all = p.local > 0 ? clamp32(static_cast<int64_t>(qmax) - p.local) : INT_MIN;
     const float scale = p.scale_log2;
-    float m = -INFINITY, l = 0.f;
+    const uint64_t scale2 = pair(scale, scale);
+    float m = -INFINITY;
+    uint64_t l2 = 0ull;   // a pair of partial sums
     bool ok = true, odd = false;
-    for (int j = 0; ok && j < nt; ++j) {
-      const int t0 = sp.group(v0 + j) * kWTile;
-      ok = mbar_wait(&s_full[t], j & 1, abort, p.status);
+    for (int i = 0; ok && i < 2 * nt; ++i) {
+      const int t0 = sp.group(v0 + (i >> 1)) * kWTile + (i & 1) * 64;
+      const uint32_t ts = tmem + lanes + t * 128 + (i & 1) * 64;
+      ok = mbar_wait(&s_full[2 * t + (i & 1)], (i >> 1) & 1, abort, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      uint32_t s[4][32];
+      uint32_t s[2][32];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, s[k]);
+      for (int k = 0; k < 2; ++k) tmem_ld32(ts + 32 * k, s[k]);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) tmem_wait_ld_dep(s[k]);
-      // all tokens of the tile seen by all rows of the CTA, or by each row on its own
-      const int t1 = t0 + kWTile - 1;
+      for (int k = 0; k < 2; ++k) tmem_wait_ld_dep(s[k]);
+      // all tokens of the step seen by all rows of the CTA, or by each row on its own
+      const int t1 = t0 + 63;
       if (!(t1 < N && t1 <= qmin && (t0 > lo_all || t1 < p.sinks))) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
             const int x = t0 + 32 * k + c;
@@ -305,11 +334,12 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
       float mx[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        mx[k] = __uint_as_float(s[k][0]);
+        const uint32_t* x = &s[k >> 1][16 * (k & 1)];
+        mx[k] = __uint_as_float(x[0]);
 #pragma unroll
-        for (int c = 1; c < 31; c += 2)
-          mx[k] = max3_nan(mx[k], __uint_as_float(s[k][c]), __uint_as_float(s[k][c + 1]));
-        mx[k] = max3_nan(mx[k], mx[k], __uint_as_float(s[k][31]));
+        for (int c = 1; c < 15; c += 2)
+          mx[k] = max3_nan(mx[k], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+        mx[k] = max3_nan(mx[k], mx[k], __uint_as_float(x[15]));
       }
       const float high = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]);
       odd = odd || !(high < INFINITY);   // NaN or +inf: the row is done again
@@ -318,9 +348,12 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
       if (__any_sync(0xffffffffu, grew)) {
         const float f = grew ? ex2(m - top) : 1.f;   // 0 from -inf: O and l are 0 then
         if (grew) m = top;
-        l *= f;
-        if (j > 0) {
-          ok = mbar_wait(&o_done[t], (j - 1) & 1, abort, p.status);
+        float a, b;
+        unpair(l2, a, b);
+        l2 = pair(a * f, b * f);
+        if (i > 0) {
+          // the product of step i - 1 (that of i - 2 is done: S of step i came after it)
+          ok = mbar_wait(&o_done[2 * t + ((i - 1) & 1)], ((i - 1) >> 1) & 1, abort, p.status);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -336,10 +369,10 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
         }
       }
       const float ref = m == -INFINITY ? 0.f : m;
-      const uint64_t scale2 = pair(scale, scale), ref2 = pair(-ref, -ref);
+      const uint64_t ref2 = pair(-ref, -ref);
       uint64_t sum[2] = {0ull, 0ull};   // pairs of +0
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 2; ++k) {
         uint32_t w[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
@@ -358,25 +391,23 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
           w[c] = pack_bf16(a, b);
         }
         tmem_st16(ts + 16 * k, w);
-        if (k & 1) {   // 64 tokens: their product with V can start
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[2 * t + (k >> 1)]);
-        }
       }
-      float a, b;
-      unpair(add_pair(sum[0], sum[1]), a, b);
-      l += a + b;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[2 * t + (i & 1)]);
+      l2 = add_pair(l2, add_pair(sum[0], sum[1]));
     }
     // the row's part
+    float l, l1;
+    unpair(l2, l, l1);
+    l += l1;
     if (m == -INFINITY) l = 0.f;   // a row that saw nothing (each unseen 2^x may be 2^-126)
-    if (ok) ok = mbar_wait(&o_done[t], (nt - 1) & 1, abort, p.status);
+    if (ok) ok = mbar_wait(&o_done[2 * t + 1], (nt - 1) & 1, abort, p.status);   // the last step
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
       tc_fence_after();
-      const bool mine = r < nrow;
-      const int64_t at = static_cast<int64_t>(chunk) * p.rows + (mine ? row : 0);
+      const int64_t at0 = static_cast<int64_t>(chunk) * p.rows;
       bool fin = !odd && (__float_as_uint(l) & 0x7f800000u) != 0x7f800000u;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -385,14 +416,29 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
         tmem_wait_ld_dep(o);
 #pragma unroll
         for (int c = 0; c < 32; ++c) fin = fin && (o[c] & 0x7f800000u) != 0x7f800000u;
-        if (mine) {
+      }
+      if (row >= 0) p.part_ml[at0 + row] = make_float2(m, fin ? l : kRedo);
+      // written four lanes to a row, 32 bytes at a time: whole sectors
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<uint4*>(p.part_o + at * 128 + 32 * k + 4 * c) =
-                make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+      for (int h = 0; h < 2; ++h) {
+        const int x = r - lane + 16 * h + (lane >> 2);   // rows x and x + 8 of this warp
+        const int ra = s_row[x], rb = s_row[x + 8];
+        float* da = p.part_o + (at0 + ra) * 128 + 2 * (lane & 3);
+        float* db = p.part_o + (at0 + rb) * 128 + 2 * (lane & 3);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t o[32];
+          tmem_ld16x256b_x8(to + (static_cast<uint32_t>(16 * h) << 16) + 64 * k, o);
+          tmem_wait_ld_dep(o);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            if (ra >= 0)
+              *reinterpret_cast<uint2*>(da + 64 * k + 8 * c) = make_uint2(o[4 * c], o[4 * c + 1]);
+            if (rb >= 0)
+              *reinterpret_cast<uint2*>(db + 64 * k + 8 * c) = make_uint2(o[4 * c + 2], o[4 * c + 3]);
+          }
         }
       }
-      if (mine) p.part_ml[at] = make_float2(m, fin ? l : kRedo);
     }
   }
 
