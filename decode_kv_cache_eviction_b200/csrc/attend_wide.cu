@@ -3,19 +3,21 @@
 // rows of its own is a prefix with itself as its only unit.)
 //
 // A CTA takes 128 or 256 query rows (one or two tiles of 128, gathered from their
-// units) and a run of 128-token tiles of the prefix, in steps of 64 tokens:
+// units) and a run of 128-token tiles of the prefix:
 //   S = Q K^T        tcgen05.mma, Q and K from shared memory (128-byte swizzle),
 //                    S in tensor memory: lane = query row, column = token;
 //   p = 2^(S - m)    one thread per query row: no exchange between threads for the
 //                    maximum and the sum; p goes back over S as bf16;
 //   O += p V         tcgen05.mma with p as the A operand from tensor memory and V
 //                    (token rows) as an MN-major B operand: V is never transposed.
-// Each query tile has two S buffers of 64 tokens, so the next S is computed while p
-// is formed from the last: with one buffer of 128 tokens a tile's S, p and product
-// followed each other, 3800 cycles per 128 tokens, although 64-token products read
-// Q more often (N = 64 takes 3/4 of the time of N = 128).  The MMAs of one thread run
-// in the order of their issue; S of a later step, written over p, therefore follows
-// the product that reads p.
+// With two query tiles their steps alternate, so the tensor cores work on one while
+// the other's p is formed, and each K/V tile in shared memory serves 256 query rows;
+// with one, it has two S buffers.  (Two buffers of 64 tokens for each of two tiles
+// fit as well, but products of N = 64 take as long as of N = 128: 3400 cycles per
+// 128 tokens instead of 2900.)  p is handed over in halves of 64 tokens, so the first
+// half's product runs while the second is formed.  The MMAs of one thread run in the
+// order of their issue; a later S, written over p, therefore follows the product that
+// reads p.
 //
 // The running maximum m is moved (and O, l rescaled by the same thread) only when
 // a row's maximum has grown by more than 2^8: p, l and O stay well inside fp32 and
@@ -49,11 +51,12 @@ constexpr float kSlack = 8.f;   // growth of a maximum (log2) that O is not resc
 template <int QT>
 struct WideLayout {
   static constexpr int kStages = QT == 2 ? 5 : 6;   // K and V tiles in turn
+  static constexpr int kBuf = QT == 2 ? 1 : 2;      // S buffers of a query tile
   static constexpr uint32_t q = 0;
   static constexpr uint32_t ring = QT * kTileB;
   static constexpr uint32_t row = ring + kStages * kTileB;      // [QT * 128] rows of Q
   static constexpr uint32_t bars = row + QT * kWTile * 4;
-  static constexpr uint32_t misc = bars + (2 * kStages + 14) * 8;
+  static constexpr uint32_t misc = bars + (2 * kStages + 10) * 8;
   static constexpr uint32_t total = misc + 96;
   static constexpr uint32_t alloc = total + 1024;               // base aligned to 1024
 };
@@ -96,16 +99,18 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
     wide_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                 const AttendParams p) {
   using Lay = WideLayout<QT>;
-  constexpr int NS = Lay::kStages;
+  constexpr int NS = Lay::kStages, kBuf = Lay::kBuf;
   constexpr int kThreads = 128 + 128 * QT;
   extern __shared__ uint8_t wide_raw[];
   uint8_t* sm = wide_raw + ((1024u - (smem_u32(wide_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + Lay::bars);
   uint64_t* empty = full + NS;
-  uint64_t* s_full = empty + NS;    // [tile][buffer] S is in tensor memory
-  uint64_t* p_full = s_full + 4;    // [tile][buffer] p is
-  uint64_t* o_done = p_full + 4;    // [tile][buffer] its product with V is done
-  uint64_t* q_full = o_done + 4;    // Q is in shared memory
+  // by tile and buffer (two of them in both forms): S is in tensor memory; the halves
+  // of p are; their product with V is done
+  uint64_t* s_full = empty + NS;    // [2]
+  uint64_t* p_full = s_full + 2;    // [2][2]
+  uint64_t* o_done = p_full + 4;    // [2]
+  uint64_t* q_full = o_done + 2;    // Q is in shared memory
   uint64_t* mdone = q_full + 1;     // teardown: every MMA has completed
   int* s_row = reinterpret_cast<int*>(sm + Lay::row);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Lay::misc);
@@ -130,9 +135,14 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
       const int k = (row0 + r) / p.R, x = row0 + r - k * p.R;
       const int u = p.mem ? __ldg(&p.mem[mo + k]) : item;
       row = u * p.R + x;
-      qp = clamp32(newest_query(p, u) - (p.nq - 1) + x % p.nq);
+      s_row[r] = row;
+      // the newest query stands behind the prefix and the unit's own rows
+      const int64_t own = p.mem ? __ldg(&p.tok_off[u + 1]) - __ldg(&p.tok_off[u]) : 0;
+      const int64_t newest = p.q_pos ? __ldg(&p.q_pos[u]) : N + own - 1;
+      qp = clamp32(newest - (p.nq - 1) + x % p.nq);
+    } else {
+      s_row[r] = -1;
     }
-    s_row[r] = row;
     const int lo = __reduce_min_sync(0xffffffffu, r < nrow ? qp : INT_MAX);
     const int hi = __reduce_max_sync(0xffffffffu, qp);
     if (lane == 0) {
@@ -143,14 +153,17 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
     tmem_alloc<1>(tmem_slot, 512);
     tmem_relinquish<1>();
   } else if (tid == 0) {
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
       lastp[s] = -1;
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);       // warps
+      mbar_init(&p_full[2 * i], 4);       // warps
+      mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&o_done[i], 1);
     }
     mbar_init(q_full, kThreads / 32 - 2);
@@ -161,7 +174,7 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;   // S of tile t, buffer h: 128 t + 64 h; O: 256 + 128 t
+  const uint32_t tmem = *tmem_slot;   // S of tile t or buffer t: 128 t; O of tile t: 256 + 128 t
   int qmin = INT_MAX, qmax = INT_MIN;
 #pragma unroll
   for (int w = 0; w < 4 * QT; ++w) {
@@ -194,8 +207,6 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      prefetch_tmap(&kmap);
-      prefetch_tmap(&vmap);
       const uint64_t pol = policy_evict_normal();
       for (int i = 0; i < 2 * nt; ++i) {
         const int s = i % NS;
@@ -218,78 +229,79 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
     // ------------------------------------------------------------ MMA issuer
     // (the whole warp runs this; one lane issues)
     const uint32_t leader = elect_leader();
-    const uint32_t id_s = idesc_bf16_f32(128, 64);
+    const uint32_t id_s = idesc_bf16_f32(128, 128);
     const uint32_t id_o = idesc_bf16_f32(128, 128) | kIdescTransposeB;
     const uint64_t qd = desc_kmajor_sw128(smem_u32(sm + Lay::q));
     const uint64_t kd = desc_kmajor_sw128(smem_u32(sm + Lay::ring));
     const uint64_t vd = desc_mnmajor_sw128(smem_u32(sm + Lay::ring), kHalfB);
     const uint32_t a_sfull = smem_u32(s_full), a_odone = smem_u32(o_done), a_empty = smem_u32(empty);
-    // addresses in a descriptor count 16 bytes
-    auto scores = [&](int t, int i, int ks) {   // S_t of step i, K tile in ring slot ks
-        const uint64_t a = qd + t * (kTileB >> 4);
-        const uint64_t b = kd + ks * (kTileB >> 4) + (i & 1) * (64 * 128 >> 4);
+    // addresses in a descriptor count 16 bytes; x: S tile or buffer
+    auto scores = [&](int t, int x, int ks) {   // S = Q_t K^T, K tile in ring slot ks
+      const uint64_t a = qd + t * (kTileB >> 4), b = kd + ks * (kTileB >> 4);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t o = ((k >> 2) * kHalfB + (k & 3) * 32) >> 4;
-          mma_bf16_by(leader, tmem + t * 128 + (i & 1) * 64, a + o, b + o, id_s, k > 0);
-        }
-        mma_commit_by(leader, a_sfull + 8 * (2 * t + (i & 1)));
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t o = ((k >> 2) * kHalfB + (k & 3) * 32) >> 4;
+        mma_bf16_by(leader, tmem + x * 128, a + o, b + o, id_s, k > 0);
+      }
+      mma_commit_by(leader, a_sfull + 8 * x);
     };
-    auto product = [&](int t, int i, int vs) {   // O_t += p_t V of step i, V tile in slot vs
-        const uint64_t b = vd + vs * (kTileB >> 4) + (i & 1) * (64 * 128 >> 4);
+    auto product = [&](int t, int x, int vs, int half, uint32_t more) {   // O_t += p V
+      const uint64_t b = vd + vs * (kTileB >> 4) + half * (64 * 128 >> 4);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_bf16_ts_by(leader, tmem + 256 + t * 128, tmem + t * 128 + (i & 1) * 64 + 8 * k,
-                         b + k * (2048 >> 4), id_o, i > 0 || k > 0);
-        mma_commit_by(leader, a_odone + 8 * (2 * t + (i & 1)));
+      for (int k = 0; k < 4; ++k)
+        mma_bf16_ts_by(leader, tmem + 256 + t * 128, tmem + x * 128 + 32 * half + 8 * k,
+                       b + k * (2048 >> 4), id_o, k > 0 ? 1u : more);
     };
-    // ring slots of the V tile in use and of the K tile after it, with their phases
-    int ks = 0, vs = 0;
-    uint32_t kph = 0, vph = 0;
-    auto next = [&](int& s, uint32_t& ph) {   // the slot after s
+    auto next = [&](int& s, uint32_t& ph) {   // the ring slot after s, and its phase
       if (++s == NS) {
         s = 0;
         ph ^= 1;
       }
     };
-    const int ni = 2 * nt;
+    // K tiles are used kBuf ahead of V tiles: ring index 2 (i + kBuf) and 2 i + 1
+    int ks = 0, vs = 1;
+    uint32_t kph = 0, vph = 0;
     bool ok = mbar_wait(q_full, 0, abort, p.status);
-    ok = ok && mbar_wait(&full[0], 0, abort, p.status);
-    ok = __all_sync(0xffffffffu, ok);
-    tc_fence_after();
-    if (ok) {
+    for (int i = 0; i < kBuf && i < nt; ++i) {
+      ok = ok && mbar_wait(&full[ks], kph, abort, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      if (ok) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int t = 0; t < QT; ++t) scores(t, i, 0);
-      mma_commit_by(leader, a_empty);
-    }
-    for (int i = 0; ok && i < ni; ++i) {
-      if ((i & 1) == 0) {
-        vs = ks;
-        vph = kph;
-        next(vs, vph);
-        ok = mbar_wait(&full[vs], vph, abort, p.status);
-        if (i + 2 < ni) {
-          ks = vs;
-          kph = vph;
-          next(ks, kph);
-          ok = ok && mbar_wait(&full[ks], kph, abort, p.status);
-        }
+        for (int t = 0; t < QT; ++t) scores(t, QT == 2 ? t : i, ks);
+        mma_commit_by(leader, a_empty + 8 * ks);
       }
+      next(ks, kph);
+      next(ks, kph);
+    }
+    for (int i = 0; ok && i < nt; ++i) {
+      const bool more = i + kBuf < nt;
+      ok = mbar_wait(&full[vs], vph, abort, p.status);
+      if (more) ok = ok && mbar_wait(&full[ks], kph, abort, p.status);
 #pragma unroll
       for (int t = 0; t < QT; ++t) {
-        ok = ok && mbar_wait(&p_full[2 * t + (i & 1)], (i >> 1) & 1, abort, p.status);
-        ok = __all_sync(0xffffffffu, ok);
+        const int x = QT == 2 ? t : (i & 1);
+        const uint32_t ph = (i / kBuf) & 1;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          ok = ok && mbar_wait(&p_full[2 * x + half], ph, abort, p.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          product(t, x, vs, half, half || i > 0);
+        }
         if (!ok) break;
-        tc_fence_after();
-        product(t, i, vs);
-        if (t == QT - 1 && (i & 1)) mma_commit_by(leader, a_empty + 8 * vs);
-        if (i + 2 < ni) {
-          scores(t, i + 2, ks);
-          if (t == QT - 1 && (i & 1)) mma_commit_by(leader, a_empty + 8 * ks);
+        mma_commit_by(leader, a_odone + 8 * x);
+        if (t == QT - 1) mma_commit_by(leader, a_empty + 8 * vs);
+        if (more) {
+          scores(t, x, ks);
+          if (t == QT - 1) mma_commit_by(leader, a_empty + 8 * ks);
         }
       }
+      next(vs, vph);
+      next(vs, vph);
+      next(ks, kph);
+      next(ks, kph);
     }
     // teardown: all MMAs (and their commits) are complete before TMEM is freed
     mma_commit_by(leader, smem_u32(mdone));
@@ -308,40 +320,42 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
     float m = -INFINITY;
     uint64_t l2 = 0ull;   // a pair of partial sums
     bool ok = true, odd = false;
-    for (int i = 0; ok && i < 2 * nt; ++i) {
-      const int t0 = sp.group(v0 + (i >> 1)) * kWTile + (i & 1) * 64;
-      const uint32_t ts = tmem + lanes + t * 128 + (i & 1) * 64;
-      ok = mbar_wait(&s_full[2 * t + (i & 1)], (i >> 1) & 1, abort, p.status);
+    for (int i = 0; ok && i < nt; ++i) {
+      const int t0 = sp.group(v0 + i) * kWTile;
+      const int x = QT == 2 ? t : (i & 1);          // S tile or buffer
+      const uint32_t ts = tmem + lanes + x * 128;
+      ok = mbar_wait(&s_full[x], (i / kBuf) & 1, abort, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      uint32_t s[2][32];
+      uint32_t s[4][32];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) tmem_ld32(ts + 32 * k, s[k]);
+      for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, s[k]);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) tmem_wait_ld_dep(s[k]);
-      // all tokens of the step seen by all rows of the CTA, or by each row on its own
-      const int t1 = t0 + 63;
+      for (int k = 0; k < 4; ++k) tmem_wait_ld_dep(s[k]);
+      // all tokens of the tile seen by all rows of the CTA, or by each row on its own
+      const int t1 = t0 + kWTile - 1;
       if (!(t1 < N && t1 <= qmin && (t0 > lo_all || t1 < p.sinks))) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            const int x = t0 + 32 * k + c;
-            if (!(x <= hi && (x > lo || x < p.sinks))) s[k][c] = 0xff800000u;   // -inf
+            const int y = t0 + 32 * k + c;
+            if (!(y <= hi && (y > lo || y < p.sinks))) s[k][c] = 0xff800000u;   // -inf
           }
       }
-      float mx[4];
+      float mx[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t* x = &s[k >> 1][16 * (k & 1)];
-        mx[k] = __uint_as_float(x[0]);
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t* y = &s[k >> 1][16 * (k & 1)];
+        mx[k] = __uint_as_float(y[0]);
 #pragma unroll
         for (int c = 1; c < 15; c += 2)
-          mx[k] = max3_nan(mx[k], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-        mx[k] = max3_nan(mx[k], mx[k], __uint_as_float(x[15]));
+          mx[k] = max3_nan(mx[k], __uint_as_float(y[c]), __uint_as_float(y[c + 1]));
+        mx[k] = max3_nan(mx[k], mx[k], __uint_as_float(y[15]));
       }
-      const float high = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]);
+      const float high = max3_nan(max3_nan(mx[0], mx[1], mx[2]), max3_nan(mx[3], mx[4], mx[5]),
+                                  max3_nan(mx[6], mx[7], mx[7]));
       odd = odd || !(high < INFINITY);   // NaN or +inf: the row is done again
       const float top = fmaxf(m, scale * high);
       const bool grew = top > m + kSlack;   // from -inf too
@@ -352,8 +366,9 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
         unpair(l2, a, b);
         l2 = pair(a * f, b * f);
         if (i > 0) {
-          // the product of step i - 1 (that of i - 2 is done: S of step i came after it)
-          ok = mbar_wait(&o_done[2 * t + ((i - 1) & 1)], ((i - 1) >> 1) & 1, abort, p.status);
+          // the product of step i - 1 (earlier ones are done: S of step i came after)
+          const int y = QT == 2 ? t : ((i - 1) & 1);
+          ok = mbar_wait(&o_done[y], ((i - 1) / kBuf) & 1, abort, p.status);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -372,18 +387,18 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
       const uint64_t ref2 = pair(-ref, -ref);
       uint64_t sum[2] = {0ull, 0ull};   // pairs of +0
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < 4; ++k) {
         uint32_t w[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          const uint64_t x = fma_pair(
+          const uint64_t y = fma_pair(
               pair(__uint_as_float(s[k][2 * c]), __uint_as_float(s[k][2 * c + 1])), scale2, ref2);
           float a, b;
           // 6 of 16 pairs on the FMA pipe
           if (c % 8 == 1 || c % 8 == 3 || c % 8 == 6) {
-            unpair(exp2_pair(x), a, b);
+            unpair(exp2_pair(y), a, b);
           } else {
-            unpair(x, a, b);
+            unpair(y, a, b);
             a = ex2(a);
             b = ex2(b);
           }
@@ -391,11 +406,13 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
           w[c] = pack_bf16(a, b);
         }
         tmem_st16(ts + 16 * k, w);
+        if (k & 1) {   // 64 tokens: their product with V can start
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * x + (k >> 1)]);
+        }
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[2 * t + (i & 1)]);
       l2 = add_pair(l2, add_pair(sum[0], sum[1]));
     }
     // the row's part
@@ -403,7 +420,8 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
     unpair(l2, l, l1);
     l += l1;
     if (m == -INFINITY) l = 0.f;   // a row that saw nothing (each unseen 2^x may be 2^-126)
-    if (ok) ok = mbar_wait(&o_done[2 * t + 1], (nt - 1) & 1, abort, p.status);   // the last step
+    if (ok)   // the last step
+      ok = mbar_wait(&o_done[QT == 2 ? t : ((nt - 1) & 1)], ((nt - 1) / kBuf) & 1, abort, p.status);
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
       tc_fence_after();
@@ -421,8 +439,8 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
       // written four lanes to a row, 32 bytes at a time: whole sectors
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int x = r - lane + 16 * h + (lane >> 2);   // rows x and x + 8 of this warp
-        const int ra = s_row[x], rb = s_row[x + 8];
+        const int y = r - lane + 16 * h + (lane >> 2);   // rows y and y + 8 of this warp
+        const int ra = s_row[y], rb = s_row[y + 8];
         float* da = p.part_o + (at0 + ra) * 128 + 2 * (lane & 3);
         float* db = p.part_o + (at0 + rb) * 128 + 2 * (lane & 3);
 #pragma unroll
