@@ -189,15 +189,25 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
     return;
   }
   if (warp >= 2) {
-    // query rows into the layout that TMA writes for K (zeros past the last row)
-#pragma unroll 8
-    for (int i = tid - 64; i < QT * kWTile * 16; i += kThreads - 64) {
+    // query rows into the layout that TMA writes for K (zeros past the last row), all of
+    // a thread's loads before its stores (one at a time they took 9 us)
+    constexpr int kCopies = (QT * kWTile * 16 + kThreads - 65) / (kThreads - 64);
+    uint4 v[kCopies];
+#pragma unroll
+    for (int k = 0; k < kCopies; ++k) {
+      const int i = tid - 64 + k * (kThreads - 64);
+      const int src = i < QT * kWTile * 16 ? s_row[i >> 4] : -1;
+      v[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (src >= 0)
+        v[k] = __ldg(reinterpret_cast<const uint4*>(p.Q) + static_cast<int64_t>(src) * 16 + (i & 15));
+    }
+#pragma unroll
+    for (int k = 0; k < kCopies; ++k) {
+      const int i = tid - 64 + k * (kThreads - 64);
       const int x = i >> 4, c = i & 15, xt = x & (kWTile - 1);
-      const int src = s_row[x];
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (src >= 0) v = __ldg(reinterpret_cast<const uint4*>(p.Q) + static_cast<int64_t>(src) * 16 + c);
-      *reinterpret_cast<uint4*>(sm + Lay::q + (x / kWTile) * kTileB + (c >> 3) * kHalfB + xt * 128 +
-                                (((c & 7) ^ (xt & 7)) << 4)) = v;
+      if (i < QT * kWTile * 16)
+        *reinterpret_cast<uint4*>(sm + Lay::q + (x / kWTile) * kTileB + (c >> 3) * kHalfB + xt * 128 +
+                                  (((c & 7) ^ (xt & 7)) << 4)) = v[k];
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -211,6 +221,9 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
       for (int i = 0; i < 2 * nt; ++i) {
         const int s = i % NS;
         const uint32_t ph = (i / NS) & 1;
+        // the first tiles only, until Q is there: its loads would wait behind the ring's
+        // (10 us instead of 2 at 148 CTAs x 160 KB)
+        if (i == 2 && !mbar_wait(q_full, 0, abort, p.status)) break;
         if (!mbar_wait(&empty[s], ph ^ 1, abort, p.status)) break;
         uint8_t* dst = sm + Lay::ring + s * kTileB;
         const int y = static_cast<int>(base + static_cast<int64_t>(sp.group(v0 + i / 2)) * kWTile);
