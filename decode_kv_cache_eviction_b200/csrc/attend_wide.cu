@@ -6,8 +6,8 @@
 // units) and a run of 128-token tiles of the prefix:
 //   S = Q K^T        tcgen05.mma, Q and K from shared memory (128-byte swizzle),
 //                    S in tensor memory: lane = query row, column = token;
-//   p = 2^(S - m)    one thread per query row: no exchange between threads for the
-//                    maximum and the sum; p goes back over S as bf16;
+//   p = 2^(S - m)    four threads per query row (two shuffles for its maximum), 16 rows
+//                    per warp; p goes back over S as bf16;
 //   O += p V         tcgen05.mma with p as the A operand from tensor memory and V
 //                    (token rows) as an MN-major B operand: V is never transposed.
 // With two query tiles their steps alternate, so the tensor cores work on one while
@@ -19,7 +19,10 @@
 // order of their issue; a later S, written over p, therefore follows the product that
 // reads p.
 //
-// The running maximum m is moved (and O, l rescaled by the same thread) only when
+// One thread per row, 128 tokens each, needs no shuffles, but with one or two warps per
+// scheduler its chain of loads, maximum and 2^x took 2300 of a step's 3500 cycles.
+//
+// The running maximum m is moved (and O, l rescaled by the same threads) only when
 // a row's maximum has grown by more than 2^8: p, l and O stay well inside fp32 and
 // bf16's relative precision does not depend on the scale, so the result is the
 // same and most steps need no pass over O.
@@ -28,11 +31,12 @@
 // product needs V's type, and a second part would cost half as many MMAs again.
 //
 // Bound: at 256 rows and d = 128 a 128-token tile takes 2048 tensor-core cycles and as
-// many for its 2^x (16 per cycle and SM); three in eight of those run on the FMA pipe.
+// many for its 2^x (16 per cycle and SM); a quarter of those run on the FMA pipe.
 // With one tile of rows it is HBM.
 //
-// Roles: warp 0 TMA producer (one lane), warp 1 MMA issuer, warps 4-7 and
-// 8-11 the rows of the first and second query tile.  Every wait is bounded.
+// Roles: warps 0-7 and 8-15 the rows of the first and second query tile (warp w: rows
+// 32 (w % 4) + 16 (w / 4 % 2) of its tile, the tensor-memory lanes that it may read),
+// then a TMA producer (one lane) and an MMA issuer.  Every wait is bounded.
 //
 // A row whose result is not finite is marked and computed again, token by token,
 // by the join: a value that is not finite in a row that it does not see (behind its
@@ -95,12 +99,12 @@ __device__ __forceinline__ void wide_drain(uint64_t* bar, uint32_t par) {
 }
 
 template <int QT>
-__global__ void __launch_bounds__(128 + 128 * QT, 1)
+__global__ void __launch_bounds__(64 + 256 * QT, 1)
     wide_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                const AttendParams p) {
+                const __grid_constant__ AttendParams p) {
   using Lay = WideLayout<QT>;
   constexpr int NS = Lay::kStages, kBuf = Lay::kBuf;
-  constexpr int kThreads = 128 + 128 * QT;
+  constexpr int kRowWarps = 8 * QT;
   extern __shared__ uint8_t wide_raw[];
   uint8_t* sm = wide_raw + ((1024u - (smem_u32(wide_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + Lay::bars);
@@ -128,31 +132,32 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
   if (row0 >= total) return;
   const int nrow = min(QT * kWTile, total - row0);
 
-  const int r = tid - 128;   // this thread's query row (warps 4 and up)
-  int row = -1, qp = INT_MIN;
-  if (warp >= 4) {
-    if (r < nrow) {
-      const int k = (row0 + r) / p.R, x = row0 + r - k * p.R;
-      const int u = p.mem ? __ldg(&p.mem[mo + k]) : item;
-      row = u * p.R + x;
-      s_row[r] = row;
-      // the newest query stands behind the prefix and the unit's own rows
-      const int64_t own = p.mem ? __ldg(&p.tok_off[u + 1]) - __ldg(&p.tok_off[u]) : 0;
-      const int64_t newest = p.q_pos ? __ldg(&p.q_pos[u]) : N + own - 1;
-      qp = clamp32(newest - (p.nq - 1) + x % p.nq);
-    } else {
-      s_row[r] = -1;
+  // position of query row `row` (of all units): the newest query of its unit stands behind
+  // the prefix and the unit's own rows
+  auto place = [&](int row) {
+    const int u = row / p.R, x = row - u * p.R;
+    const int64_t own = p.mem ? __ldg(&p.tok_off[u + 1]) - __ldg(&p.tok_off[u]) : 0;
+    const int64_t newest = p.q_pos ? __ldg(&p.q_pos[u]) : N + own - 1;
+    return clamp32(newest - (p.nq - 1) + x % p.nq);
+  };
+  if (tid < QT * kWTile) {
+    int row = -1, qp = INT_MIN;
+    if (tid < nrow) {
+      const int k = (row0 + tid) / p.R;
+      row = (p.mem ? __ldg(&p.mem[mo + k]) : item) * p.R + row0 + tid - k * p.R;
+      qp = place(row);
     }
-    const int lo = __reduce_min_sync(0xffffffffu, r < nrow ? qp : INT_MAX);
+    s_row[tid] = row;
+    const int lo = __reduce_min_sync(0xffffffffu, row >= 0 ? qp : INT_MAX);
     const int hi = __reduce_max_sync(0xffffffffu, qp);
     if (lane == 0) {
-      s_lim[2 * (warp - 4)] = lo;
-      s_lim[2 * (warp - 4) + 1] = hi;
+      s_lim[2 * warp] = lo;
+      s_lim[2 * warp + 1] = hi;
     }
-  } else if (warp == 1) {
+  } else if (warp == kRowWarps + 1) {
     tmem_alloc<1>(tmem_slot, 512);
     tmem_relinquish<1>();
-  } else if (tid == 0) {
+  } else if (tid == kRowWarps * 32) {
     prefetch_tmap(&kmap);
     prefetch_tmap(&vmap);
     for (int s = 0; s < NS; ++s) {
@@ -162,11 +167,11 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[2 * i], 4);       // warps
-      mbar_init(&p_full[2 * i + 1], 4);
+      mbar_init(&p_full[2 * i], 8);       // warps
+      mbar_init(&p_full[2 * i + 1], 8);
       mbar_init(&o_done[i], 1);
     }
-    mbar_init(q_full, kThreads / 32 - 2);
+    mbar_init(q_full, kRowWarps);
     mbar_init(mdone, 1);
     *abort = 0;
     fence_mbar_init();
@@ -184,37 +189,37 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
   const Span sp = visible_span<7>(N, 0, qmin, qmax, p.local, p.sinks);
   const int v0 = chunk * p.gpc, nt = min(sp.nv, v0 + p.gpc) - v0;   // token tiles of this CTA
   if (nt <= 0) {
-    if (row >= 0) p.part_ml[static_cast<int64_t>(chunk) * p.rows + row] = make_float2(-INFINITY, 0.f);
-    if (warp == 1) tmem_dealloc<1>(tmem, 512);
+    if (tid < nrow)
+      p.part_ml[static_cast<int64_t>(chunk) * p.rows + s_row[tid]] = make_float2(-INFINITY, 0.f);
+    if (warp == kRowWarps + 1) tmem_dealloc<1>(tmem, 512);
     return;
   }
-  if (warp >= 2) {
+  if (warp < kRowWarps) {
     // query rows into the layout that TMA writes for K (zeros past the last row), all of
     // a thread's loads before its stores (one at a time they took 9 us)
-    constexpr int kCopies = (QT * kWTile * 16 + kThreads - 65) / (kThreads - 64);
+    constexpr int kCopies = kWTile * 16 / 256;
     uint4 v[kCopies];
 #pragma unroll
     for (int k = 0; k < kCopies; ++k) {
-      const int i = tid - 64 + k * (kThreads - 64);
-      const int src = i < QT * kWTile * 16 ? s_row[i >> 4] : -1;
+      const int i = tid + k * kRowWarps * 32;
+      const int src = s_row[i >> 4];
       v[k] = make_uint4(0u, 0u, 0u, 0u);
       if (src >= 0)
         v[k] = __ldg(reinterpret_cast<const uint4*>(p.Q) + static_cast<int64_t>(src) * 16 + (i & 15));
     }
 #pragma unroll
     for (int k = 0; k < kCopies; ++k) {
-      const int i = tid - 64 + k * (kThreads - 64);
+      const int i = tid + k * kRowWarps * 32;
       const int x = i >> 4, c = i & 15, xt = x & (kWTile - 1);
-      if (i < QT * kWTile * 16)
-        *reinterpret_cast<uint4*>(sm + Lay::q + (x / kWTile) * kTileB + (c >> 3) * kHalfB + xt * 128 +
-                                  (((c & 7) ^ (xt & 7)) << 4)) = v[k];
+      *reinterpret_cast<uint4*>(sm + Lay::q + (x / kWTile) * kTileB + (c >> 3) * kHalfB + xt * 128 +
+                                (((c & 7) ^ (xt & 7)) << 4)) = v[k];
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(q_full);
   }
 
-  if (warp == 0) {
+  if (warp == kRowWarps) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       const uint64_t pol = policy_evict_normal();
@@ -238,7 +243,7 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
         if (lastp[s] >= 0) wide_drain(&full[s], lastp[s]);
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == kRowWarps + 1) {
     // ------------------------------------------------------------ MMA issuer
     // (the whole warp runs this; one lane issues)
     const uint32_t leader = elect_leader();
@@ -320,18 +325,27 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
     mma_commit_by(leader, smem_u32(mdone));
     wide_drain(mdone, 0);
     __syncwarp();
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------------------ rows
-    const int t = (warp - 4) >> 2;               // query tile
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int t = warp >> 3;                                   // query tile
+    const int l0 = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);   // first row (lane) of the warp
+    const int q = lane & 3;
+    const uint32_t lanes = static_cast<uint32_t>(l0) << 16;
     const uint32_t to = tmem + lanes + 256 + t * 128;
-    const int lo = p.local > 0 ? clamp32(static_cast<int64_t>(qp) - p.local) : INT_MIN;
-    const int hi = min(qp, N - 1);
+    // this thread's rows, lanes l0 + lane / 4 + 8 h, and columns 8 i + 2 q + {0, 1}
+    int row[2], lo[2], hi[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      row[h] = s_row[t * kWTile + l0 + (lane >> 2) + 8 * h];
+      const int qp = row[h] >= 0 ? place(row[h]) : INT_MIN;
+      lo[h] = p.local > 0 ? clamp32(static_cast<int64_t>(qp) - p.local) : INT_MIN;
+      hi[h] = min(qp, N - 1);
+    }
     const int lo_all = p.local > 0 ? clamp32(static_cast<int64_t>(qmax) - p.local) : INT_MIN;
     const float scale = p.scale_log2;
     const uint64_t scale2 = pair(scale, scale);
-    float m = -INFINITY;
-    uint64_t l2 = 0ull;   // a pair of partial sums
+    float m[2] = {-INFINITY, -INFINITY};
+    uint64_t l2[2] = {0ull, 0ull};   // pairs of partial sums
     bool ok = true, odd = false;
     for (int i = 0; ok && i < nt; ++i) {
       const int t0 = sp.group(v0 + i) * kWTile;
@@ -341,43 +355,63 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      uint32_t s[4][32];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, s[k]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) tmem_wait_ld_dep(s[k]);
       // all tokens of the tile seen by all rows of the CTA, or by each row on its own
       const int t1 = t0 + kWTile - 1;
-      if (!(t1 < N && t1 <= qmin && (t0 > lo_all || t1 < p.sinks))) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
+      const bool masked = !(t1 < N && t1 <= qmin && (t0 > lo_all || t1 < p.sinks));
+      // s[4 k + 2 h + e]: column 64 b + 8 k + 2 q + e of row h
+      uint32_t s[32];
+      auto load = [&](int b) {
+        tmem_ld16x256b_x8(ts + 64 * b, s);
+        tmem_wait_ld_dep(s);
+        if (masked) {
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            const int y = t0 + 32 * k + c;
-            if (!(y <= hi && (y > lo || y < p.sinks))) s[k][c] = 0xff800000u;   // -inf
+            const int y = t0 + 64 * b + 8 * (c >> 2) + 2 * q + (c & 1), h = (c >> 1) & 1;
+            if (!(y <= hi[h] && (y > lo[h] || y < p.sinks))) s[c] = 0xff800000u;   // -inf
           }
-      }
-      float mx[8];
+        }
+      };
+      // the maximum over both halves; the first stays in registers, the second is read
+      // again (all 128 columns of two rows do not fit into the registers of 18 warps)
+      float high[2];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t* y = &s[k >> 1][16 * (k & 1)];
-        mx[k] = __uint_as_float(y[0]);
+      for (int b = 1; b >= 0; --b) {
+        load(b);
 #pragma unroll
-        for (int c = 1; c < 15; c += 2)
-          mx[k] = max3_nan(mx[k], __uint_as_float(y[c]), __uint_as_float(y[c + 1]));
-        mx[k] = max3_nan(mx[k], mx[k], __uint_as_float(y[15]));
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t* y = &s[2 * h];   // columns 0, 1, 4, 5, ...
+          auto at = [&](int n) { return __uint_as_float(y[4 * (n >> 1) + (n & 1)]); };
+          float u = max3_nan(at(0), at(1), at(2)), v = max3_nan(at(3), at(4), at(5));
+          u = max3_nan(u, at(6), at(7));
+          v = max3_nan(v, at(8), at(9));
+          u = max3_nan(u, at(10), at(11));
+          v = max3_nan(v, at(12), at(13));
+          u = max3_nan(u, at(14), at(15));
+          high[h] = b == 1 ? max3_nan(u, v, v) : max3_nan(high[h], u, v);
+        }
       }
-      const float high = max3_nan(max3_nan(mx[0], mx[1], mx[2]), max3_nan(mx[3], mx[4], mx[5]),
-                                  max3_nan(mx[6], mx[7], mx[7]));
-      odd = odd || !(high < INFINITY);   // NaN or +inf: the row is done again
-      const float top = fmaxf(m, scale * high);
-      const bool grew = top > m + kSlack;   // from -inf too
-      if (__any_sync(0xffffffffu, grew)) {
-        const float f = grew ? ex2(m - top) : 1.f;   // 0 from -inf: O and l are 0 then
-        if (grew) m = top;
-        float a, b;
-        unpair(l2, a, b);
-        l2 = pair(a * f, b * f);
+      float top[2];
+      bool grew[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float o = __shfl_xor_sync(0xffffffffu, high[h], 1);
+        high[h] = max3_nan(high[h], o, o);
+        o = __shfl_xor_sync(0xffffffffu, high[h], 2);
+        high[h] = max3_nan(high[h], o, o);
+        odd = odd || !(high[h] < INFINITY);   // NaN or +inf: the row is done again
+        top[h] = fmaxf(m[h], scale * high[h]);
+        grew[h] = top[h] > m[h] + kSlack;   // from -inf too
+      }
+      if (__any_sync(0xffffffffu, grew[0] || grew[1])) {
+        float f[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          f[h] = grew[h] ? ex2(m[h] - top[h]) : 1.f;   // 0 from -inf: O and l are 0 then
+          if (grew[h]) m[h] = top[h];
+          float a, b;
+          unpair(l2[h], a, b);
+          l2[h] = pair(a * f[h], b * f[h]);
+        }
         if (i > 0) {
           // the product of step i - 1 (earlier ones are done: S of step i came after)
           const int y = QT == 2 ? t : ((i - 1) & 1);
@@ -385,90 +419,94 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            uint32_t o[16];
-            tmem_ld16(to + 16 * k, o);
+#pragma unroll 1
+          for (int b = 0; b < 2; ++b) {
+            uint32_t o[32];
+            tmem_ld16x256b_x8(to + 64 * b, o);
             tmem_wait_ld_dep(o);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
-            tmem_st16(to + 16 * k, o);
+            for (int c = 0; c < 32; ++c)
+              o[c] = __float_as_uint(__uint_as_float(o[c]) * f[(c >> 1) & 1]);
+            tmem_st16x256b_x8(to + 64 * b, o);
           }
         }
       }
-      const float ref = m == -INFINITY ? 0.f : m;
-      const uint64_t ref2 = pair(-ref, -ref);
-      uint64_t sum[2] = {0ull, 0ull};   // pairs of +0
+      uint64_t ref2[2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t w[16];
+      for (int h = 0; h < 2; ++h) {
+        const float ref = m[h] == -INFINITY ? 0.f : m[h];
+        ref2[h] = pair(-ref, -ref);
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if (b == 1) load(1);
+        uint32_t w[16];   // w[2 k + h]
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          const uint64_t y = fma_pair(
-              pair(__uint_as_float(s[k][2 * c]), __uint_as_float(s[k][2 * c + 1])), scale2, ref2);
-          float a, b;
-          // 6 of 16 pairs on the FMA pipe
-          if (c % 8 == 1 || c % 8 == 3 || c % 8 == 6) {
-            unpair(exp2_pair(y), a, b);
+          const int h = c & 1;
+          const uint64_t y =
+              fma_pair(pair(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), scale2,
+                       ref2[h]);
+          float u, v;
+          // one pair in four on the FMA pipe (none: 79 us for 64 sequences on 32 prefixes of
+          // 16384 tokens, one in four 71, three in eight 71, half 76)
+          if (c % 8 == 1 || c % 8 == 4) {
+            unpair(exp2_pair(y), u, v);
           } else {
-            unpair(y, a, b);
-            a = ex2(a);
-            b = ex2(b);
+            unpair(y, u, v);
+            u = ex2(u);
+            v = ex2(v);
           }
-          sum[c & 1] = add_pair(sum[c & 1], pair(a, b));
-          w[c] = pack_bf16(a, b);
+          l2[h] = add_pair(l2[h], pair(u, v));
+          w[c] = pack_bf16(u, v);
         }
-        tmem_st16(ts + 16 * k, w);
-        if (k & 1) {   // 64 tokens: their product with V can start
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[2 * x + (k >> 1)]);
-        }
+        tmem_st16x128b_x8(ts + 32 * b, w);
+        // 64 tokens: their product with V can start
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * x + b]);
       }
-      l2 = add_pair(l2, add_pair(sum[0], sum[1]));
     }
-    // the row's part
-    float l, l1;
-    unpair(l2, l, l1);
-    l += l1;
-    if (m == -INFINITY) l = 0.f;   // a row that saw nothing (each unseen 2^x may be 2^-126)
+    // the rows' parts
+    float l[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float a;
+      unpair(l2[h], l[h], a);
+      l[h] += a;
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      if (m[h] == -INFINITY) l[h] = 0.f;   // saw nothing (each unseen 2^x may be 2^-126)
+    }
     if (ok)   // the last step
       ok = mbar_wait(&o_done[QT == 2 ? t : ((nt - 1) & 1)], ((nt - 1) / kBuf) & 1, abort, p.status);
     ok = __all_sync(0xffffffffu, ok);
     if (ok) {
       tc_fence_after();
       const int64_t at0 = static_cast<int64_t>(chunk) * p.rows;
-      bool fin = !odd && (__float_as_uint(l) & 0x7f800000u) != 0x7f800000u;
+      bool fin[2] = {!odd, !odd};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int b = 0; b < 2; ++b) {
         uint32_t o[32];
-        tmem_ld32(to + 32 * k, o);
+        tmem_ld16x256b_x8(to + 64 * b, o);
         tmem_wait_ld_dep(o);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) fin = fin && (o[c] & 0x7f800000u) != 0x7f800000u;
+        for (int c = 0; c < 32; c += 2) {   // four lanes write 32 bytes of a row
+          const int h = (c >> 1) & 1;
+          fin[h] = fin[h] && (o[c] & 0x7f800000u) != 0x7f800000u &&
+                   (o[c + 1] & 0x7f800000u) != 0x7f800000u;
+          if (row[h] >= 0)
+            *reinterpret_cast<uint2*>(p.part_o + (at0 + row[h]) * 128 + 64 * b + 8 * (c >> 2) + 2 * q) =
+                make_uint2(o[c], o[c + 1]);
+        }
       }
-      if (row >= 0) p.part_ml[at0 + row] = make_float2(m, fin ? l : kRedo);
-      // written four lanes to a row, 32 bytes at a time: whole sectors
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int y = r - lane + 16 * h + (lane >> 2);   // rows y and y + 8 of this warp
-        const int ra = s_row[y], rb = s_row[y + 8];
-        float* da = p.part_o + (at0 + ra) * 128 + 2 * (lane & 3);
-        float* db = p.part_o + (at0 + rb) * 128 + 2 * (lane & 3);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t o[32];
-          tmem_ld16x256b_x8(to + (static_cast<uint32_t>(16 * h) << 16) + 64 * k, o);
-          tmem_wait_ld_dep(o);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            if (ra >= 0)
-              *reinterpret_cast<uint2*>(da + 64 * k + 8 * c) = make_uint2(o[4 * c], o[4 * c + 1]);
-            if (rb >= 0)
-              *reinterpret_cast<uint2*>(db + 64 * k + 8 * c) = make_uint2(o[4 * c + 2], o[4 * c + 3]);
-          }
-        }
+        const unsigned bad = __ballot_sync(0xffffffffu, !fin[h]);
+        const bool fine = ((bad >> (lane & ~3)) & 15u) == 0u &&
+                          (__float_as_uint(l[h]) & 0x7f800000u) != 0x7f800000u;
+        if (row[h] >= 0 && q == 0) p.part_ml[at0 + row[h]] = make_float2(m[h], fine ? l[h] : kRedo);
       }
     }
   }
@@ -476,7 +514,7 @@ __global__ void __launch_bounds__(128 + 128 * QT, 1)
   // ---------------------------------------------------------------- teardown
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == kRowWarps + 1) {
     tc_fence_after();
     tmem_dealloc<1>(tmem, 512);
   }
@@ -497,10 +535,10 @@ cudaError_t launch_attend_wide(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                const AttendParams& p, int P, int max_rows, cudaStream_t st) {
   const unsigned x = static_cast<unsigned>(P) * p.maxch;
   if (max_rows <= kWTile) {
-    wide_kernel<1><<<dim3(x, 1), 256, WideLayout<1>::alloc, st>>>(kmap, vmap, p);
+    wide_kernel<1><<<dim3(x, 1), 320, WideLayout<1>::alloc, st>>>(kmap, vmap, p);
   } else {
     const unsigned y = (max_rows + 2 * kWTile - 1) / (2 * kWTile);
-    wide_kernel<2><<<dim3(x, y), 384, WideLayout<2>::alloc, st>>>(kmap, vmap, p);
+    wide_kernel<2><<<dim3(x, y), 576, WideLayout<2>::alloc, st>>>(kmap, vmap, p);
   }
   return cudaGetLastError();
 }

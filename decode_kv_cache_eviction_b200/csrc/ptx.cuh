@@ -452,19 +452,21 @@ __device__ __forceinline__ void tmem_ld16x256b_x2(uint32_t taddr, uint32_t (&v)[
 }
 #undef RKV_R8
 
-// Registers to tensor memory: 32 lanes x 32-bit, 32 or 16 consecutive columns.
 #define RKV_V8(i) "r"(v[i + 0]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), \
                   "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+// Registers to tensor memory in the layouts of tmem_ld16x256b: 16 lanes x 8 groups of 8
+// columns, and 16 lanes x 8 groups of 4 columns (v[2i]: lane t/4, v[2i+1]: lane t/4 + 8,
+// column 4i + t%4).
+__device__ __forceinline__ void tmem_st16x256b_x8(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
       "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
       RKV_V8(0), RKV_V8(8), RKV_V8(16), RKV_V8(24)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+__device__ __forceinline__ void tmem_st16x128b_x8(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
       "%14,%15,%16};" ::"r"(taddr),
       RKV_V8(0), RKV_V8(8)
       : "memory");
