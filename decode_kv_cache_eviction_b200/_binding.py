@@ -88,6 +88,7 @@ class RkvError(RuntimeError):
 
 
 _lib = None
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def lib():
@@ -167,24 +168,26 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _tensor(t, name: str, dtype, shape, device, optional: bool = True):
-    """Pointer of a contiguous tensor of this type, shape and device (or None)."""
+def _tensor(t, name: str, dtype, shape, device: int, optional: bool = True):
+    """Pointer of a contiguous tensor of this type and shape on GPU ``device`` (or None)."""
     if t is None:
         if optional:
             return None
         raise ValueError(f"{name} is required")
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                         f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                     f"cuda:{device}, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                     f"{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-def _stream_on(device, stream) -> int:
-    """The stream's handle; by default the current stream of ``device``."""
+def _stream_on(device: int, stream) -> int:
+    """The stream's handle; by default the current stream of GPU ``device``."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError(f"the stream is on {stream.device}, the engine on cuda:{device}")
     return stream.cuda_stream
 
 
@@ -228,14 +231,8 @@ class Batch:
         self.tok_off = torch.from_numpy(off).to(dev)
         self.c = RkvBatch(len(off) - 1, self.tok_off.data_ptr(),
                           off.ctypes.data, _ptr(K), _ptr(V), _ptr(Q))
-
-    @property
-    def num_units(self):
-        return len(self.tok_off_host) - 1
-
-    @property
-    def num_tokens(self):
-        return int(self.tok_off_host[-1])
+        self.ref = ctypes.byref(self.c)
+        self.num_units, self.num_tokens = len(off) - 1, int(off[-1])
 
 
 class Offsets:
@@ -246,6 +243,9 @@ class Offsets:
         if self.host.ndim != 1 or len(self.host) < 1:
             raise ValueError("offsets are U + 1 values")
         self.dev = torch.from_numpy(self.host).to(device)
+        self.device = self.dev.get_device()
+        self.num_units, self.total = len(self.host) - 1, int(self.host[-1])
+        self.dev_ptr, self.host_ptr = self.dev.data_ptr(), self.host.ctypes.data
 
 
 class Prefix:
@@ -265,7 +265,7 @@ class Prefix:
         for name, t in (("K", K), ("V", V)):
             if not t.is_cuda:
                 raise ValueError(f"{name} must be a CUDA tensor")
-            _tensor(t, name, torch.bfloat16, (int(off[-1]), 128), K.device)
+            _tensor(t, name, torch.bfloat16, (int(off[-1]), 128), K.get_device())
         order = np.argsort(up, kind="stable").astype(np.int32)
         mem = np.ascontiguousarray(order[np.count_nonzero(up < 0):])
         mem_off = np.zeros(P + 1, dtype=np.int32)
@@ -279,6 +279,8 @@ class Prefix:
         self.c = RkvPrefix(P, len(up), d[0].data_ptr(), h[0].ctypes.data, K.data_ptr(),
                            V.data_ptr(), ptr(d[1], h[1]), h[1].ctypes.data, d[2].data_ptr(),
                            h[2].ctypes.data, ptr(d[3], h[3]), h[3].ctypes.data)
+        self.ref = ctypes.byref(self.c)
+        self.device = K.get_device()
 
 
 class Engine:
@@ -307,7 +309,7 @@ class Engine:
         h = ctypes.c_void_p()
         _check(lib().rkv_create(ctypes.byref(self.cfg), ctypes.byref(h)), "rkv_create")
         self.h = h
-        self.device = torch.device("cuda", torch.cuda.current_device())
+        self.device = torch.cuda.current_device()
 
     def close(self):
         if getattr(self, "h", None):
@@ -412,37 +414,39 @@ class Engine:
         local, sinks: sliding window and sinks; acc_out: fp32 [T], acc plus this
         call's weights (may be acc itself)."""
         args = self._attention(batch, Q, out, lse, keep, pos, q_pos, local, sinks, acc, acc_out)
-        _check(lib().rkv_attend(self.h, ctypes.byref(batch.c), ctypes.byref(args),
-                                _stream_on(self.device, stream)), "rkv_attend")
+        rc = _lib.rkv_attend(self.h, batch.ref, args, _stream_on(self.device, stream))
+        if rc:
+            raise RkvError(rc, "rkv_attend")
 
     def attend_shared(self, batch: Batch, prefix: Prefix, Q, out, lse=None, *, keep=None,
                       pos=None, q_pos=None, local: int = 0, sinks: int = 0, acc=None,
                       acc_out=None, stream=None):
         """``attend`` where the units' rows follow a prefix that several of them
         share and that is read once for all (``rkv_attend_shared``)."""
-        if prefix.K.device != self.device:
-            raise ValueError(f"the prefix is on {prefix.K.device}, the engine on {self.device}")
+        if prefix.device != self.device:
+            raise ValueError(f"the prefix is on cuda:{prefix.device}, the engine on "
+                             f"cuda:{self.device}")
         args = self._attention(batch, Q, out, lse, keep, pos, q_pos, local, sinks, acc, acc_out)
-        _check(lib().rkv_attend_shared(self.h, ctypes.byref(batch.c), ctypes.byref(prefix.c),
-                                       ctypes.byref(args), _stream_on(self.device, stream)),
-               "rkv_attend_shared")
+        rc = _lib.rkv_attend_shared(self.h, batch.ref, prefix.ref, args,
+                                    _stream_on(self.device, stream))
+        if rc:
+            raise RkvError(rc, "rkv_attend_shared")
 
     def _attention(self, batch, Q, out, lse, keep, pos, q_pos, local, sinks, acc, acc_out):
         U, T, dev = batch.num_units, batch.num_tokens, self.device
         if Q.dim() != 4:
             raise ValueError("Q must be [U, G, n_q, 128]")
         nq = Q.shape[2]
-        shape = (U, self.group, nq, 128)
-        bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
-        for name, t in (("K", batch.K), ("V", batch.V)):
-            _tensor(t, name, bf, (T, 128), dev, optional=False)
-        return RkvAttention(
-            nq, int(local), int(sinks), _tensor(Q, "Q", bf, shape, dev),
-            _tensor(keep, "keep", torch.uint8, (T,), dev), _tensor(pos, "pos", i32, (T,), dev),
-            _tensor(q_pos, "q_pos", i32, (U,), dev), _tensor(acc, "acc", f32, (T,), dev),
-            _tensor(acc_out, "acc_out", f32, (T,), dev),
-            _tensor(out, "out", bf, shape, dev, optional=False),
-            _tensor(lse, "lse", f32, shape[:3], dev))
+        shape, rows, kv = (U, self.group, nq, 128), (T,), (T, 128)
+        _tensor(batch.K, "K", _BF16, kv, dev, False)
+        _tensor(batch.V, "V", _BF16, kv, dev, False)
+        return ctypes.byref(RkvAttention(
+            nq, local, sinks, _tensor(Q, "Q", _BF16, shape, dev, False),
+            _tensor(keep, "keep", _U8, rows, dev), _tensor(pos, "pos", _I32, rows, dev),
+            _tensor(q_pos, "q_pos", _I32, (U,), dev), _tensor(acc, "acc", _F32, rows, dev),
+            _tensor(acc_out, "acc_out", _F32, rows, dev),
+            _tensor(out, "out", _BF16, shape, dev, False),
+            _tensor(lse, "lse", _F32, shape[:3], dev)))
 
     def evict_accumulated(self, batch: Batch, acc, budget: int, keep, free_slots, n_free, *,
                           live=None, pos=None, budgets=None, sinks: int = 0, acc_out=None,
@@ -450,19 +454,20 @@ class Engine:
         """Keep the sinks, the w newest and the ``budget`` heaviest other live rows
         of every unit (``rkv_evict_accumulated``).  live: uint8 [T] before the call
         (may be keep); idx int32 [U, budget + sinks + w] with n_kept int32 [U]."""
-        U, T, dev = batch.num_units, batch.num_tokens, self.device
-        u8, f32, i32 = torch.uint8, torch.float32, torch.int32
-        W = int(budget) + int(sinks) + self.window
-        _check(lib().rkv_evict_accumulated(
-            self.h, ctypes.byref(batch.c), _tensor(acc, "acc", f32, (T,), dev, optional=False),
-            _tensor(live, "live", u8, (T,), dev), _tensor(pos, "pos", i32, (T,), dev),
-            int(budget), _tensor(budgets, "budgets", i32, (U,), dev), int(sinks),
-            _tensor(keep, "keep", u8, (T,), dev, optional=False),
-            _tensor(free_slots, "free_slots", i32, (T,), dev, optional=False),
-            _tensor(n_free, "n_free", i32, (U,), dev, optional=False),
-            _tensor(acc_out, "acc_out", f32, (T,), dev), _tensor(idx, "idx", i32, (U, W), dev),
-            _tensor(n_kept, "n_kept", i32, (U,), dev), _stream_on(dev, stream)),
-            "rkv_evict_accumulated")
+        U, dev = batch.num_units, self.device
+        rows, units = (batch.num_tokens,), (U,)
+        rc = _lib.rkv_evict_accumulated(
+            self.h, batch.ref, _tensor(acc, "acc", _F32, rows, dev, False),
+            _tensor(live, "live", _U8, rows, dev), _tensor(pos, "pos", _I32, rows, dev),
+            budget, _tensor(budgets, "budgets", _I32, units, dev), sinks,
+            _tensor(keep, "keep", _U8, rows, dev, False),
+            _tensor(free_slots, "free_slots", _I32, rows, dev, False),
+            _tensor(n_free, "n_free", _I32, units, dev, False),
+            _tensor(acc_out, "acc_out", _F32, rows, dev),
+            _tensor(idx, "idx", _I32, (U, budget + sinks + self.window), dev),
+            _tensor(n_kept, "n_kept", _I32, units, dev), _stream_on(dev, stream))
+        if rc:
+            raise RkvError(rc, "rkv_evict_accumulated")
 
     def fill_slots_ex(self, batch: Batch, new_off: Offsets, K_new, V_new, keep, free_slots,
                       n_free, *, pos=None, pos_new=None, acc=None, free_out=None,
@@ -471,28 +476,29 @@ class Engine:
         pos_new) and zeroes their accumulated weight (acc), and can leave the
         remaining list in other buffers (``rkv_fill_slots_ex``)."""
         U, T, dev = batch.num_units, batch.num_tokens, self.device
-        n = int(new_off.host[-1])
-        bf, u8, f32, i32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
-        if len(new_off.host) != U + 1 or new_off.dev.device != dev:
-            raise ValueError(f"new_off must hold {U + 1} offsets on {dev}")
+        if new_off.num_units != U or new_off.device != dev:
+            raise ValueError(f"new_off must hold {U + 1} offsets on cuda:{dev}")
         if (free_out is None) != (n_free_out is None):
             raise ValueError("free_out and n_free_out go together")
         if (pos is None) != (pos_new is None):
             raise ValueError("pos and pos_new go together")
-        free = _tensor(free_slots, "free_slots", i32, (T,), dev, optional=False)
-        count = _tensor(n_free, "n_free", i32, (U,), dev, optional=False)
-        _check(lib().rkv_fill_slots_ex(
-            self.h, ctypes.byref(batch.c),
-            _tensor(batch.K, "K", bf, (T, 128), dev, optional=False),
-            _tensor(batch.V, "V", bf, (T, 128), dev, optional=False), new_off.dev.data_ptr(),
-            new_off.host.ctypes.data, _tensor(K_new, "K_new", bf, (n, 128), dev, optional=False),
-            _tensor(V_new, "V_new", bf, (n, 128), dev, optional=False),
-            _tensor(pos_new, "pos_new", i32, (n,), dev),
-            _tensor(keep, "keep", u8, (T,), dev, optional=False), free, count,
-            _tensor(pos, "pos", i32, (T,), dev), _tensor(acc, "acc", f32, (T,), dev),
-            free if free_out is None else _tensor(free_out, "free_out", i32, (T,), dev),
-            count if n_free_out is None else _tensor(n_free_out, "n_free_out", i32, (U,), dev),
-            _stream_on(dev, stream)), "rkv_fill_slots_ex")
+        n = new_off.total
+        rows, units, kv, new = (T,), (U,), (T, 128), (n, 128)
+        free = _tensor(free_slots, "free_slots", _I32, rows, dev, False)
+        count = _tensor(n_free, "n_free", _I32, units, dev, False)
+        rc = _lib.rkv_fill_slots_ex(
+            self.h, batch.ref, _tensor(batch.K, "K", _BF16, kv, dev, False),
+            _tensor(batch.V, "V", _BF16, kv, dev, False), new_off.dev_ptr, new_off.host_ptr,
+            _tensor(K_new, "K_new", _BF16, new, dev, False),
+            _tensor(V_new, "V_new", _BF16, new, dev, False),
+            _tensor(pos_new, "pos_new", _I32, (n,), dev),
+            _tensor(keep, "keep", _U8, rows, dev, False), free, count,
+            _tensor(pos, "pos", _I32, rows, dev), _tensor(acc, "acc", _F32, rows, dev),
+            free if free_out is None else _tensor(free_out, "free_out", _I32, rows, dev),
+            count if n_free_out is None else _tensor(n_free_out, "n_free_out", _I32, units, dev),
+            _stream_on(dev, stream))
+        if rc:
+            raise RkvError(rc, "rkv_fill_slots_ex")
 
     def check_status(self, stream=None):
         _check(lib().rkv_check_status(self.h, _stream(stream)), "device status")

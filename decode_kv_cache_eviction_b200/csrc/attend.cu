@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
   const int g = lane >> 2, q = lane & 3;
   AtWarpShared<NS>& ws = wsh[wp];
 
+  if (kMode != kWeights) allow_next_launch();   // the own rows' kernel, or the weights'
   // what this CTA works on: rows [row0, row0 + nrow) of queries against groups
   // of the sequence of N rows at `base`
   const int item = blockIdx.x / p.maxch, chunk = blockIdx.x - item * p.maxch;
@@ -756,6 +757,8 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
       }
     }
     __syncthreads();
+    // the prefix's parts: this launch may have started while they were computed
+    if (kMode == kOwn && p.pre_o) wait_for_previous_launch();
     // one warp per query row, lane = four dimensions
     for (int r = wp; r < min(nrow, 8 * NB); r += W) {
       RowSum x = no_rows();
@@ -808,11 +811,12 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
 }
 
 // The weights pass from stored logits: chunks of gpc groups of one unit per CTA.
-__global__ void __launch_bounds__(256) weights_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(256) weights_kernel(const __grid_constant__ AttendParams p) {
   const int item = blockIdx.x / p.maxch, chunk = blockIdx.x - item * p.maxch;
   const int64_t base = __ldg(&p.tok_off[item]);
   const int N = static_cast<int>(__ldg(&p.tok_off[item + 1]) - base);
   const int64_t i0 = static_cast<int64_t>(chunk) * p.gpc * 32;
+  wait_for_previous_launch();
   if (i0 >= N) return;
   weights_any(p, base, prefix_len(p, item), newest_query(p, item),
               p.lse2 + static_cast<int64_t>(item) * p.R, static_cast<int>(i0),
@@ -823,6 +827,7 @@ __global__ void __launch_bounds__(256) weights_kernel(const AttendParams p) {
 // kernel, each unit as a prefix of its own.  One warp per query row.
 __global__ void __launch_bounds__(128) finish_kernel(const __grid_constant__ AttendParams p) {
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  wait_for_previous_launch();
   if (row >= p.rows) return;
   const RowSum x = join_prefix(p, no_rows(), row, static_cast<int>(row / p.R));
   attend_store(p, row, threadIdx.x & 31, x.M, x.L, x.o);
@@ -849,19 +854,36 @@ cudaError_t configure_mode() {
   return e;
 }
 
+// early: the launch may start when the one before it on the stream lets it
+// (allow_next_launch); it waits for that one's results where it reads them.
+cudaError_t launch_early(void (*kernel)(const AttendParams), const AttendParams& p, dim3 grid,
+                         int threads, int smem, bool early, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = early ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
 template <int NB, int kMode, bool kOne, int W>
-cudaError_t launch_one(const AttendParams& p, dim3 grid, cudaStream_t st) {
-  attend_kernel<NB, kMode, kOne, W><<<grid, 32 * W, at_smem_bytes<NB, kMode, W>(), st>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_one(const AttendParams& p, dim3 grid, bool early, cudaStream_t st) {
+  return launch_early(attend_kernel<NB, kMode, kOne, W>, p, grid, 32 * W, at_smem_bytes<NB, kMode, W>(),
+                      early, st);
 }
 template <int kMode, int W>
-cudaError_t launch_mode(const AttendParams& p, int rows, dim3 grid, cudaStream_t st) {
+cudaError_t launch_mode(const AttendParams& p, int rows, dim3 grid, bool early, cudaStream_t st) {
   if (rows <= 8) {
-    if (kMode == kOwn && p.nq == 1) return launch_one<1, kOwn, true, W>(p, grid, st);
-    return launch_one<1, kMode, false, W>(p, grid, st);
+    if (kMode == kOwn && p.nq == 1) return launch_one<1, kOwn, true, W>(p, grid, early, st);
+    return launch_one<1, kMode, false, W>(p, grid, early, st);
   }
-  if (rows <= 16) return launch_one<2, kMode, false, W>(p, grid, st);
-  return launch_one<4, kMode, false, W>(p, grid, st);
+  if (rows <= 16) return launch_one<2, kMode, false, W>(p, grid, early, st);
+  return launch_one<4, kMode, false, W>(p, grid, early, st);
 }
 
 }  // namespace
@@ -878,29 +900,26 @@ cudaError_t attend_configure() {
 
 int attend_warps_per_sm(int rows) { return rows <= 16 ? AtCfg<1>::kWarps : AtCfg<4>::kWarps; }
 
-cudaError_t launch_attend(const AttendParams& p, int U, int warps, cudaStream_t st) {
+cudaError_t launch_attend(const AttendParams& p, int U, int warps, bool early, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(U) * p.maxch, (p.R + 31) / 32);
-  return warps == 2 ? launch_mode<kOwn, 2>(p, p.R, grid, st)
-                    : launch_mode<kOwn, 4>(p, p.R, grid, st);
+  return warps == 2 ? launch_mode<kOwn, 2>(p, p.R, grid, early, st)
+                    : launch_mode<kOwn, 4>(p, p.R, grid, early, st);
 }
 
 cudaError_t launch_attend_prefix(const AttendParams& p, int P, int max_rows, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(P) * p.maxch, (max_rows + 31) / 32);
-  return launch_mode<kPrefix, 4>(p, max_rows, grid, st);
+  return launch_mode<kPrefix, 4>(p, max_rows, grid, false, st);
 }
 
 cudaError_t launch_attend_finish(const AttendParams& p, cudaStream_t st) {
-  finish_kernel<<<static_cast<unsigned>((p.rows + 3) / 4), 128, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_early(finish_kernel, p, dim3(static_cast<unsigned>((p.rows + 3) / 4)), 128, 0, true,
+                      st);
 }
 
 cudaError_t launch_attend_weights(const AttendParams& p, int U, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(U) * p.maxch, 1);
-  if (p.z) {
-    weights_kernel<<<grid, 256, 0, st>>>(p);
-    return cudaGetLastError();
-  }
-  return launch_mode<kWeights, 4>(p, p.R, grid, st);
+  if (p.z) return launch_early(weights_kernel, p, grid, 256, 0, true, st);
+  return launch_mode<kWeights, 4>(p, p.R, grid, false, st);
 }
 
 }  // namespace rkv

@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(64 + 256 * QT, 1)
   constexpr int NS = Lay::kStages, kBuf = Lay::kBuf;
   constexpr int kRowWarps = 8 * QT;
   extern __shared__ uint8_t wide_raw[];
+  allow_next_launch();   // the units' own rows, on SMs that have none of this
   uint8_t* sm = wide_raw + ((1024u - (smem_u32(wide_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + Lay::bars);
   uint64_t* empty = full + NS;

@@ -110,7 +110,7 @@ int pick_chunks(int64_t items, int64_t sum, int64_t nmax, int64_t slots, int64_t
       std::min<int64_t>(std::max<int64_t>(1, cap), std::max<int64_t>(1, nmax / least_groups));
   int64_t best = 1;
   double least = 1e300;
-  for (int64_t c = 1; c <= std::min<int64_t>(most, 4096); c += c < 32 ? 1 : c / 16) {
+  for (int64_t c = 1; c <= std::min<int64_t>(most, 4096); c += c < 16 ? 1 : c / 8) {
     const int64_t gpc = (nmax + c - 1) / c;
     const int64_t ctas = items * ((avg + gpc - 1) / gpc);
     const double cost = static_cast<double>((ctas + slots - 1) / slots) * (gpc + extra) +
@@ -123,26 +123,37 @@ int pick_chunks(int64_t items, int64_t sum, int64_t nmax, int64_t slots, int64_t
   return static_cast<int>(best);
 }
 
-// Warps per CTA and chunks per unit of the attention over own rows, by what a CTA
-// costs in us: about 4 for its start and end, 0.7 (alone) to 1.4 (on a full SM) per
-// 16-row stage of a warp, and 2.5 and 0.12 per chunk for the join.  `resident`:
-// warps that the GPU holds at once.
-void pick_shape(int64_t items, int64_t sum, int64_t nmax, int64_t resident, int64_t cap,
-                int* warps, int* chunks) {
-  const int64_t avg = std::max<int64_t>(1, (sum + items - 1) / items);
+// Warps per CTA and chunks per unit of the attention over own rows, by waves of CTAs on
+// the `resident` warps that the GPU holds at once.  In us: a CTA costs 5 for its start
+// and end, and per 16-row stage of a warp `step` when few run beside it and the stage's
+// share of HBM (8 KB at 6.5 TB/s) when many do; joining c parts costs 3 + 0.1 c, and the
+// weights 5 in a launch of their own or 0.3 per 32 rows and warp at the unit's end.  Measured: 128 units of 32768
+// rows 401 / 324 / 402 / 334 us in 1 / 2 / 4 / 6 chunks (modelled 389 / 340 / 395 / 344),
+// 509 windows of 1028 rows 50 us with two warps and 59 with four (50 / 62).
+void pick_shape(int64_t items, int64_t sum, int64_t nmax, int64_t resident, double step,
+                int64_t cap, bool weights, int* warps, int* chunks) {
+  const double avg = std::max(1.0, static_cast<double>(sum) / static_cast<double>(items));
+  const double share = resident * 8192.0 / 6.5e6;
+  auto stage = [&](double part) { return std::max(step, share * part); };
   double least = 1e300;
   for (int w = 4; w >= 2; w -= 2)
     for (int64_t c = 1; c <= std::min<int64_t>(std::max<int64_t>(1, cap),
                                                std::max<int64_t>(1, nmax / w));
-         c += c < 16 ? 1 : c / 8) {
+         c += c < 4 ? 1 : c / 4) {
       const int64_t gpc = (nmax + c - 1) / c;
-      const double ctas = static_cast<double>(items) * ((avg + gpc - 1) / gpc);
-      const double full = std::min(1.0, ctas * w / resident);
-      const double one = 4.0 + (c > 1 ? 2.5 + 0.12 * c : 0.0) +
-                         2.0 * static_cast<double>((std::min(gpc, avg) + w - 1) / w) *
-                             (0.7 + 0.7 * full);
-      const double waves = ctas * w / resident;
-      const double cost = waves <= 1.0 ? one : one * (waves + 0.4);
+      // CTAs of an average unit: exact for equal lengths, else a half one more
+      const double per = c == 1 ? 1.0
+                         : avg > 0.99 * nmax ? static_cast<double>(c)
+                                             : std::max(1.0, avg / gpc + 0.5);
+      const double waves = static_cast<double>(items) * per * w / resident;
+      const double full = std::floor(waves), rest = waves - full;
+      const double mean = 2.0 * avg / per / w + 0.5;
+      const double most = 2.0 * static_cast<double>((gpc + w - 1) / w);
+      double cost = c > 1 ? 3.0 + 0.1 * c + (weights ? 5.0 : 0.0) : 0.0;
+      const double fixed = 5.0 + (weights && c == 1 ? 0.3 * avg / w : 0.0);
+      if (full > 0) cost += full * (mean * stage(1.0) + fixed);
+      cost += full == 0 || rest > 0.02 ? most * stage(rest) + fixed : (most - mean) * step;
+      if (w == 2) cost *= 1.05;   // measured beyond the model
       if (cost < least) {
         least = cost;
         *warps = w;
@@ -288,8 +299,8 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
   }
   int own = 1, warps = 4;
   pick_shape(rg * static_cast<int64_t>(U), rg * gsum, gmax,
-             static_cast<int64_t>(attend_warps_per_sm(R)) * e->nsm, cap / rows - (x ? 1 : 0),
-             &warps, &own);
+             static_cast<int64_t>(attend_warps_per_sm(R)) * e->nsm, R <= 16 ? 0.75 : 2.5,
+             cap / rows - (x ? 1 : 0), logits, &warps, &own);
   const int64_t used = own > 1 ? static_cast<int64_t>(own) * rows : 0;   // parts of own chunks
   cudaError_t err;
   if (x) {
@@ -377,7 +388,7 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
       p.count = count;
     }
     t_begin(e, RKV_KERNEL_ATTEND, st);
-    err = launch_attend(p, U, warps, st);
+    err = launch_attend(p, U, warps, x != nullptr, st);
     t_end(e, st);
     if (err != cudaSuccess) return cuda_fail(err);
     ++e->launches;

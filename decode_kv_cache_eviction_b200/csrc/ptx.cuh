@@ -476,6 +476,17 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// ---------------------------------------------------------------- launches
+// The next launch on the stream may start (if it was launched for that) once every CTA
+// has said so or exited; its CTAs wait for this launch's end and results with
+// wait_for_previous_launch, at the latest before they exit.
+__device__ __forceinline__ void allow_next_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous_launch() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- misc
 __device__ __forceinline__ float ex2(float x) {   // 2^x (hardware approximation)
   float y;
