@@ -16,6 +16,8 @@
 //   and a tile only reads positions that no earlier tile wrote).  Optionally
 //   the filled slots get their tokens' positions and a zero accumulated weight,
 //   and the list that is left goes to another buffer.
+#include <algorithm>
+
 #include "ptx.cuh"
 #include "rkv_internal.cuh"
 
@@ -140,8 +142,9 @@ __global__ void __launch_bounds__(kIpThreads)
 }
 
 constexpr int kFillThreads = 256;
+constexpr int kFillRows = 4;   // rows and list entries of a thread in flight
 
-__global__ void __launch_bounds__(kFillThreads)
+__global__ void __launch_bounds__(kFillThreads, 4)
     fill_slots_kernel(const int64_t* __restrict__ tok_off, int U,
                       const int64_t* __restrict__ new_off, const uint4* __restrict__ Kn,
                       const uint4* __restrict__ Vn, uint4* __restrict__ K, uint4* __restrict__ V,
@@ -151,46 +154,76 @@ __global__ void __launch_bounds__(kFillThreads)
                       float* __restrict__ acc, int* status) {
   const int tid = threadIdx.x;
   const int sub = tid & 15;            // 16-byte word of the 256-byte row
-  const int rsub = tid >> 4;           // one of 16 rows in flight
+  // a list that moves elsewhere is not in the rows' way: gridDim.y CTAs share a unit
+  const int parts = gridDim.y, part = blockIdx.y;
+  const int rsub = part * (kFillThreads / 16) + (tid >> 4);   // row of a pass
+  const int step = parts * (kFillThreads / 16);
   for (int u = blockIdx.x; u < U; u += gridDim.x) {
     const int64_t base = tok_off[u];
     const int N = static_cast<int>(tok_off[u + 1] - base);
     const int64_t nb = new_off[u];
     const int want = static_cast<int>(new_off[u + 1] - nb);
     int nf = n_free[u];
+    __syncthreads();   // n_free_out may be n_free
     if (nf < 0 || nf > N) nf = 0;      // not produced by evict_in_place: take nothing
     const int n = want < nf ? want : nf;
     if (want > nf && tid == 0) atomicOr(status, kStatusBadIndex);
     const int32_t* fu = free_slots + base;
     int32_t* fo = free_out + base;
-    for (int t = rsub; t < n; t += kFillThreads / 16) {
-      const int slot = fu[t];
-      if (slot < 0 || slot >= N) {
-        if (sub == 0) atomicOr(status, kStatusBadIndex);
-        continue;
+    // four rows per 16 threads in flight
+    for (int t0 = rsub; t0 < n; t0 += kFillRows * step) {
+      int slot[kFillRows];
+      uint4 k[kFillRows], v[kFillRows];
+#pragma unroll
+      for (int x = 0; x < kFillRows; ++x) {
+        const int t = t0 + x * step;
+        slot[x] = t < n ? fu[t] : -1;
+        if (t < n) {
+          k[x] = __ldcs(&Kn[(nb + t) * 16 + sub]);
+          v[x] = __ldcs(&Vn[(nb + t) * 16 + sub]);
+        }
       }
-      const int64_t dst = (base + slot) * 16 + sub;
-      const int64_t src = (nb + t) * 16 + sub;
-      K[dst] = __ldcs(&Kn[src]);
-      V[dst] = __ldcs(&Vn[src]);
-      if (sub == 0) {
-        keep[base + slot] = 1;
-        if (pos) pos[base + slot] = pos_new[nb + t];
-        if (acc) acc[base + slot] = 0.f;
+#pragma unroll
+      for (int x = 0; x < kFillRows; ++x) {
+        const int t = t0 + x * step;
+        if (t >= n) break;
+        if (slot[x] < 0 || slot[x] >= N) {
+          if (sub == 0) atomicOr(status, kStatusBadIndex);
+          continue;
+        }
+        const int64_t row = base + slot[x];
+        K[row * 16 + sub] = k[x];
+        V[row * 16 + sub] = v[x];
+        if (sub == 0) {
+          keep[row] = 1;
+          if (pos) pos[row] = pos_new[nb + t];
+          if (acc) acc[row] = 0.f;
+        }
       }
     }
-    __syncthreads();   // every used slot has been read from the list
     // the remaining nf - n free slots move to the front; the tail becomes -1
-    // (a list written elsewhere is written whole)
-    const int wn = fo == fu ? nf : N;
-    for (int t0 = 0; t0 < wn; t0 += kFillThreads) {
-      const int t = t0 + tid;
-      const int v = t + n < nf ? fu[t + n] : -1;
-      __syncthreads();
-      if (t < wn) fo[t] = v;
-      __syncthreads();
+    if (fo != fu) {   // elsewhere: the whole list is written
+#pragma unroll 4
+      for (int t = part * kFillThreads + tid; t < N; t += parts * kFillThreads) fo[t] = t + n < nf ? fu[t + n] : -1;
+    } else if (n > 0) {
+      __syncthreads();   // every used slot has been read from the list
+      for (int t0 = 0; t0 < nf; t0 += kFillRows * kFillThreads) {
+        int x[kFillRows];
+#pragma unroll
+        for (int k = 0; k < kFillRows; ++k) {
+          const int t = t0 + k * kFillThreads + tid;
+          x[k] = t + n < nf ? fu[t + n] : -1;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kFillRows; ++k) {
+          const int t = t0 + k * kFillThreads + tid;
+          if (t < nf) fo[t] = x[k];
+        }
+        __syncthreads();
+      }
     }
-    if (tid == 0) n_free_out[u] = nf - n;
+    if (tid == 0 && part == 0) n_free_out[u] = nf - n;
     __syncthreads();
   }
 }
@@ -218,8 +251,7 @@ cudaError_t launch_fill_slots(const int64_t* tok_off, int U, const int64_t* new_
                               const void* K_new, const void* V_new, void* K, void* V,
                               uint8_t* keep, const int32_t* free_slots, const int32_t* n_free,
                               const FillExtra& x, int* status, int nsm, cudaStream_t st) {
-  int grid = nsm * 4;
-  if (grid > U) grid = U;
+  const dim3 grid(std::min(U, nsm * 4), x.free_out == free_slots ? 1 : 4);
   fill_slots_kernel<<<grid, kFillThreads, 0, st>>>(
       tok_off, U, new_off, static_cast<const uint4*>(K_new), static_cast<const uint4*>(V_new),
       static_cast<uint4*>(K), static_cast<uint4*>(V), keep, free_slots, n_free, x.free_out,
