@@ -2,19 +2,20 @@
 // (position < sinks) and the w newest positions stay, and of the others the
 // `budget` rows of largest weight (ties: lowest row first; -0 = +0; NaN last).
 //
-// One cluster of 1 to 8 CTAs per unit, each with a run of the unit's rows in its
-// registers (V vectors of four consecutive rows per thread), so acc, live and pos
-// are read once.  Weights become order-preserving 32-bit keys; histograms of 512
-// bins over the range of the keys that are left (added over distributed shared
-// memory in a cluster) narrow it down to the threshold key, and stop as soon as a
-// bin is taken whole.  Starting from the keys' own range spreads them over the
-// bins, so few of the shared-memory additions meet, and two or three rounds are
-// enough where weights differ.  Ballots then give every row its place among the
-// kept and the free rows of the unit.
+// One cluster of 1 to 8 CTAs per unit, each with the keys of a run of the unit's rows
+// in shared memory (order-preserving 32-bit keys of the weights; 0 for dead rows, the
+// largest for rows that stay unranked).  Histograms of 512 bins over the range of the
+// keys that are left (added over distributed shared memory in a cluster) narrow it down
+// to the threshold key, and stop as soon as a bin is taken whole; a unit in one CTA ends
+// with the few rows of one bin compared with each other, and a bin of equal weights is
+// seen by its range.  Starting from the keys' own range spreads them over the bins, so
+// few of the shared-memory additions meet.  Ballots then give every row its place among
+// the kept and the free rows of the unit.
 //
-// Bound: instruction issue and the latency of a few dependent block reductions
-// at small units, HBM beyond; hence the vectors, and short runs on 128-thread
-// CTAs, which keep many units in flight.
+// Bound: instruction issue and the latency of a few dependent block reductions at small
+// units, HBM beyond; hence vectors of four rows, loops that stay rolled and few registers
+// (keys in registers and unrolled loops took 46 us instead of 39 for 2048 units of 2176
+// rows, at half the resident warps).
 #include <limits.h>
 
 #include "ptx.cuh"
@@ -49,6 +50,8 @@ __device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
   return v;
 }
 
+constexpr int kList = 128;
+
 template <int T>
 struct DropShared {
   uint4 hist[2][kBins / 4];      // two in turn
@@ -56,6 +59,9 @@ struct DropShared {
   uint32_t total[2][4];          // this CTA's
   uint32_t wsum[T / 32];
   uint32_t found[3];             // bin, its rows, rows wanted of it
+  uint2 list[kList];             // keys and rows of a small bin
+  uint32_t listed;
+  uint2 last;                    // the last of them that stays
 };
 
 // Exchanges of up to 4 values over the CTA and the cluster.
@@ -103,11 +109,12 @@ struct Exchange {
   }
 };
 
-template <int T, int V, bool kPos>
-__global__ void __launch_bounds__(T) drop_kernel(const DropParams p, int cs) {
+template <int T, bool kPos>
+__global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, int cs) {
   constexpr int kWarps = T / 32;
+  constexpr uint32_t kSafe = 0xffffffffu;   // above every key: +inf has 0xff800000
+  extern __shared__ uint4 keys[];           // [nv] vectors of four rows, then the places
   __shared__ DropShared<T> sh;
-  __shared__ uint32_t cnt[V * kWarps + 1];
   const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
   const unsigned below = (1u << lane) - 1u;
   const int rank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -115,94 +122,85 @@ __global__ void __launch_bounds__(T) drop_kernel(const DropParams p, int cs) {
   const int64_t base = p.tok_off[u];
   const int N = static_cast<int>(p.tok_off[u + 1] - base);
   // this CTA's rows lo .. lo + n - 1 of the unit, in vectors that start at rows of
-  // the whole arrays that are multiples of four: row 4 (v T + tid) + c - skew of
-  // the run is element c of vector v
+  // the whole arrays that are multiples of four: row 4 v + c - skew of the run is
+  // element c of vector v; thread t has the vectors t, t + T, ...
   const int run = (N + cs - 1) / cs;
   const int lo = min(N, rank * run), n = min(N, lo + run) - lo;
   const int skew = static_cast<int>((base + lo) & 3);
   const int nv = (n + skew + 3) >> 2;
+  const int nr = (nv + T - 1) / T;        // rounds over the vectors
+  uint32_t* cnt = reinterpret_cast<uint32_t*>(keys + nv);   // [nr * kWarps + 1]
   const int64_t at0 = base + lo - skew;   // row of element 0 of vector 0
   Exchange<T> ex = {sh, cs, rank, 0};
   if (tid < kBins / 4) sh.hist[0][tid] = sh.hist[1][tid] = make_uint4(0u, 0u, 0u, 0u);
-  auto first = [&](int v) { return 4 * (v * T + tid) - skew; };
-  auto whole = [&](int j) { return p.vec && j >= 0 && j + 4 <= n; };
+  if (tid == 0) sh.listed = 0u;
+  auto whole = [&](int v) { return p.vec && 4 * v >= skew && 4 * v + 4 <= n + skew; };
+  auto inside = [&](int v, int c) { return 4 * v + c >= skew && 4 * v + c < n + skew; };
+  auto live4 = [&](int v) -> uint32_t {   // live bytes of a vector's rows
+    if (whole(v))
+      return p.live ? *reinterpret_cast<const uint32_t*>(p.live + at0 + 4 * v) : 0x01010101u;
+    uint32_t x = 0u;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (inside(v, c))
+        x |= (p.live ? static_cast<uint32_t>(p.live[at0 + 4 * v + c]) : 1u) << (8 * c);
+    return x;
+  };
+  auto pos4 = [&](int v) -> int4 {
+    if (!kPos) {
+      const int x = lo - skew + 4 * v;
+      return make_int4(x, x + 1, x + 2, x + 3);
+    }
+    if (whole(v)) return *reinterpret_cast<const int4*>(p.pos + at0 + 4 * v);
+    int x[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (inside(v, c)) x[c] = p.pos[at0 + 4 * v + c];
+    return make_int4(x[0], x[1], x[2], x[3]);
+  };
+  auto acc4 = [&](int v) -> float4 {
+    if (whole(v)) return *reinterpret_cast<const float4*>(p.acc + at0 + 4 * v);
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (inside(v, c)) x[c] = p.acc[at0 + 4 * v + c];
+    return make_float4(x[0], x[1], x[2], x[3]);
+  };
 
-  uint32_t key[V][4];
-  int ps[kPos ? V : 1][4];
-  uint32_t lv[V];   // live bytes of a vector's rows (kept packed: nothing waits for the loads yet)
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      key[v][c] = 0u;
-      if (kPos) ps[v][c] = 0;
-    }
-    lv[v] = 0u;
-    if (v * T < nv) {
-      const int j = first(v);
-      const int64_t at = at0 + 4 * (v * T + tid);
-      if (whole(j)) {
-        const uint4 x = *reinterpret_cast<const uint4*>(p.acc + at);
-        key[v][0] = x.x;
-        key[v][1] = x.y;
-        key[v][2] = x.z;
-        key[v][3] = x.w;
-        lv[v] = p.live ? *reinterpret_cast<const uint32_t*>(p.live + at) : 0x01010101u;
-        if (kPos) {
-          const int4 z = *reinterpret_cast<const int4*>(p.pos + at);
-          ps[v][0] = z.x;
-          ps[v][1] = z.y;
-          ps[v][2] = z.z;
-          ps[v][3] = z.w;
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (j + c >= 0 && j + c < n) {
-            key[v][c] = __float_as_uint(p.acc[at + c]);
-            lv[v] |= (p.live ? static_cast<uint32_t>(p.live[at + c]) : 1u) << (8 * c);
-            if (kPos) ps[v][c] = p.pos[at + c];
-          }
-      }
-    }
-  }
-  auto place = [&](int v, int c) { return kPos ? ps[v][c] : lo + first(v) + c; };
   // the newest live position
   int newest = N - 1;
   if (kPos || p.live) {
     int x = INT_MIN;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v * T < nv) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if ((lv[v] >> (8 * c)) & 0xffu) x = max(x, place(v, c));
-      }
+#pragma unroll 4
+    for (int v = tid; v < nv; v += T) {
+      const uint32_t l = live4(v);
+      const int4 y = pos4(v);
+      if (l & 0xffu) x = max(x, y.x);
+      if (l & 0xff00u) x = max(x, y.y);
+      if (l & 0xff0000u) x = max(x, y.z);
+      if (l & 0xff000000u) x = max(x, y.w);
+    }
     uint32_t m[1] = {static_cast<uint32_t>(__reduce_max_sync(0xffffffffu, x)) ^ 0x80000000u}, b[1];
     ex.all(m, b, [](int, uint32_t a, uint32_t x) { return a > x ? a : x; });
     newest = static_cast<int>(m[0] ^ 0x80000000u);
   }
-  // positions above it stay (a position is at least INT_MIN + 1 here or nothing is live)
-  const int recent = newest < INT_MIN + p.w ? INT_MIN : newest - p.w;
+  const int recent = newest < INT_MIN + p.w ? INT_MIN : newest - p.w;   // positions above stay
   uint32_t kmax = 0u, kinv = 0u, count = 0u;   // kinv: complement of the smallest key
-  uint32_t safe[V];                            // bit c: element c stays unranked
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    safe[v] = 0u;
-    if (v * T < nv) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int x = place(v, c);
-        const bool s = x < p.sinks || x > recent;
-        const bool on = ((lv[v] >> (8 * c)) & 0xffu) != 0u;
-        if (on && s) safe[v] |= 1u << c;
-        const uint32_t k = on && !s ? weight_key(__uint_as_float(key[v][c])) : 0u;
-        key[v][c] = k;
-        kmax = max(kmax, k);
-        kinv = max(kinv, k ? ~k : 0u);
-        count += k ? 1u : 0u;
-      }
-    }
+#pragma unroll 4
+  for (int v = tid; v < nv; v += T) {
+    const float4 a = acc4(v);
+    const uint32_t l = live4(v);
+    const int4 y = pos4(v);
+    auto one = [&](float w, int x, int c) -> uint32_t {
+      if (!((l >> (8 * c)) & 0xffu)) return 0u;
+      if (x < p.sinks || x > recent) return kSafe;
+      const uint32_t k = weight_key(w);
+      kmax = max(kmax, k);
+      kinv = max(kinv, ~k);
+      ++count;
+      return k;
+    };
+    keys[v] = make_uint4(one(a.x, y.x, 0), one(a.y, y.y, 1), one(a.z, y.z, 2), one(a.w, y.w, 3));
   }
   uint32_t m[3] = {__reduce_max_sync(0xffffffffu, kmax), __reduce_max_sync(0xffffffffu, kinv),
                    __reduce_add_sync(0xffffffffu, count)};
@@ -212,29 +210,30 @@ __global__ void __launch_bounds__(T) drop_kernel(const DropParams p, int cs) {
   int budget = p.budget;
   if (p.budgets) budget = min(max(p.budgets[u], 0), p.budget);
 
-  // ranked rows with key > thr stay, and the first `ties` rows with key = thr
+  // rows with key > thr stay, and of those with key = thr the rows of the run up to
+  // `cut`, or (some_ties) the unit's first `ties`
   uint32_t thr = 0u, ties = 0u;
+  int cut = INT_MIN;
   bool some_ties = false;
   if (budget == 0) {
-    thr = 0xffffffffu;
+    thr = kSafe - 1u;
   } else if (ranked > static_cast<uint32_t>(budget)) {
     uint32_t want = budget;
-    uint32_t low = ~m[1];              // the keys that are left: low .. low + 2^bits - 1
-    int bits = 32 - __clz(m[0] - low);
+    const uint32_t high = m[0];
+    uint32_t low = ~m[1];              // the keys that are left: low .. low + span
+    uint32_t span = high - low;
     some_ties = true;
-    for (int round = 0; bits > 0; ++round) {
-      const int shift = max(0, bits - kBinBits);
-      const uint32_t bins = 1u << (bits - shift);
+    for (int round = 0; span > 0u; ++round) {
+      const int shift = max(0, 32 - __clz(span) - kBinBits);
       uint32_t* hist = reinterpret_cast<uint32_t*>(sh.hist[round & 1]);
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (v * T < nv) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t x = (key[v][c] - low) >> shift;
-            if (key[v][c] >= low && key[v][c] != 0u && x < bins) atomicAdd(&hist[x], 1u);
-          }
-        }
+#pragma unroll 2
+      for (int v = tid; v < nv; v += T) {
+        const uint4 k = keys[v];
+        if (k.x - low <= span) atomicAdd(&hist[(k.x - low) >> shift], 1u);
+        if (k.y - low <= span) atomicAdd(&hist[(k.y - low) >> shift], 1u);
+        if (k.z - low <= span) atomicAdd(&hist[(k.z - low) >> shift], 1u);
+        if (k.w - low <= span) atomicAdd(&hist[(k.w - low) >> shift], 1u);
+      }
       if (cs > 1) cluster_sync_all();
       else __syncthreads();
       // thread t < 128: bins kBins - 1 - 4 t downwards
@@ -290,14 +289,66 @@ __global__ void __launch_bounds__(T) drop_kernel(const DropParams p, int cs) {
         }
       }
       __syncthreads();
-      const uint32_t bin = sh.found[0], in_bin = sh.found[1];
+      const uint32_t in_bin = sh.found[1];
+      low += sh.found[0] << shift;
       want = sh.found[2];
-      low += bin << shift;
-      bits = shift;
+      span = min((1u << shift) - 1u, high - low);
       if (want == in_bin) {   // the whole bin stays
         thr = low - 1u;
         some_ties = false;
         break;
+      }
+      if (span == 0u) break;
+      if (cs == 1 && in_bin <= kList) {
+        // few rows left: each one's rank by comparing it with the others
+        for (int v = tid; v < nv; v += T) {
+          const uint4 k = keys[v];
+          auto put = [&](uint32_t x, int c) {
+            if (x - low <= span)
+              sh.list[atomicAdd(&sh.listed, 1u)] = make_uint2(x, static_cast<uint32_t>(4 * v + c));
+          };
+          put(k.x, 0);
+          put(k.y, 1);
+          put(k.z, 2);
+          put(k.w, 3);
+        }
+        __syncthreads();
+        if (tid < static_cast<int>(in_bin)) {
+          const uint2 own = sh.list[tid];
+          uint32_t above_own = 0;
+          for (uint32_t k = 0; k < in_bin; ++k) {
+            const uint2 x = sh.list[k];
+            above_own += x.x > own.x || (x.x == own.x && x.y < own.y) ? 1u : 0u;
+          }
+          if (above_own == want - 1u) sh.last = own;
+        }
+        __syncthreads();
+        thr = sh.last.x;
+        cut = static_cast<int>(sh.last.y);
+        some_ties = false;
+        break;
+      }
+      if (in_bin * 16u > ranked) {
+        // so many rows in one bin are likely equal: the range of their keys
+        uint32_t x[2] = {0u, 0u}, b[2];
+        for (int v = tid; v < nv; v += T) {
+          const uint4 k = keys[v];
+          auto see = [&](uint32_t y) {
+            if (y - low <= span) {
+              x[0] = max(x[0], y);
+              x[1] = max(x[1], ~y);
+            }
+          };
+          see(k.x);
+          see(k.y);
+          see(k.z);
+          see(k.w);
+        }
+        x[0] = __reduce_max_sync(0xffffffffu, x[0]);
+        x[1] = __reduce_max_sync(0xffffffffu, x[1]);
+        ex.all(x, b, [](int, uint32_t a, uint32_t y) { return a > y ? a : y; });
+        low = ~x[1];
+        span = x[0] - low;
       }
     }
     if (some_ties) {
@@ -306,31 +357,37 @@ __global__ void __launch_bounds__(T) drop_kernel(const DropParams p, int cs) {
     }
   }
 
-  uint32_t kept[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    kept[v] = safe[v];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) kept[v] |= (key[v][c] > thr ? 1u : 0u) << c;
-  }
-  // Of one bit per row: the number set in lower lanes' elements of vector v, and in
-  // cnt[v kWarps + warp] (after scan) the number set in warps before.
+  // bits of a vector's rows: kept, or equal to the threshold
+  auto kept4 = [&](int v) -> uint32_t {
+    const uint4 k = keys[v];
+    auto one = [&](uint32_t x, int c) {
+      return (x > thr || (x == thr && 4 * v + c <= cut) ? 1u : 0u) << c;
+    };
+    return one(k.x, 0) | one(k.y, 1) | one(k.z, 2) | one(k.w, 3);
+  };
+  auto tied4 = [&](int v) -> uint32_t {
+    const uint4 k = keys[v];
+    return (k.x == thr ? 1u : 0u) | (k.y == thr ? 2u : 0u) | (k.z == thr ? 4u : 0u) |
+           (k.w == thr ? 8u : 0u);
+  };
+  // Of one bit per row: the number set in lower lanes' elements of a round, and in
+  // cnt[round kWarps + warp] (after scan) the number set in warps before.
   auto lower = [&](uint32_t b) {
     int k = 0;
 #pragma unroll
     for (int c = 0; c < 4; ++c) k += __popc(__ballot_sync(0xffffffffu, (b >> c) & 1u) & below);
     return k;
   };
-  auto scan = [&](const uint32_t (&b)[V], uint32_t& total) {
+  auto scan = [&](auto bits, uint32_t& total) {
     __syncthreads();
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v * T < nv) {
-        const uint32_t k = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(__popc(b[v])));
-        if (lane == 0) cnt[v * kWarps + wp] = k;
-      }
+    for (int r = 0; r < nr; ++r) {
+      const int v = r * T + tid;
+      const uint32_t k =
+          __reduce_add_sync(0xffffffffu, v < nv ? static_cast<uint32_t>(__popc(bits(v))) : 0u);
+      if (lane == 0) cnt[r * kWarps + wp] = k;
+    }
     __syncthreads();
-    const int used = ((nv + T - 1) / T) * kWarps;
+    const int used = nr * kWarps;
     if (wp == 0) {
       uint32_t carry = 0;
       for (int k0 = 0; k0 < used; k0 += 32) {
@@ -344,10 +401,10 @@ __global__ void __launch_bounds__(T) drop_kernel(const DropParams p, int cs) {
         if (k0 + lane < used) cnt[k0 + lane] = carry + y - x;
         carry += __shfl_sync(0xffffffffu, y, 31);
       }
-      if (lane == 0) cnt[V * kWarps] = carry;
+      if (lane == 0) cnt[used] = carry;
     }
     __syncthreads();
-    total = cnt[V * kWarps];
+    total = cnt[used];
   };
   // the CTAs' totals: over the cluster, and of the CTAs before this one
   auto across = [&](uint32_t mine, uint32_t& total, uint32_t& before) {
@@ -362,69 +419,62 @@ __global__ void __launch_bounds__(T) drop_kernel(const DropParams p, int cs) {
   };
   uint32_t total, all, before;
   if (some_ties) {
-    uint32_t tb[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      tb[v] = 0u;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tb[v] |= (key[v][c] == thr ? 1u : 0u) << c;
-    }
-    scan(tb, total);
+    // the first `ties` of the equal rows become unranked ones that stay
+    scan(tied4, total);
     across(total, all, before);
+    for (int r = 0; r < nr; ++r) {
+      const int v = r * T + tid;
+      const uint32_t b = v < nv ? tied4(v) : 0u;
+      uint32_t at = before + cnt[r * kWarps + wp] + lower(b);
+      uint32_t* k = reinterpret_cast<uint32_t*>(keys + v);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v * T < nv) {
-        uint32_t at = before + cnt[v * kWarps + wp] + lower(tb[v]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if ((tb[v] >> c) & 1u) {
-            if (at < ties) kept[v] |= 1u << c;
-            ++at;
-          }
-      }
+      for (int c = 0; c < 4; ++c)
+        if ((b >> c) & 1u) {
+          if (at < ties) k[c] = kSafe;
+          ++at;
+        }
+    }
   }
-  scan(kept, total);
+  scan(kept4, total);
   across(total, all, before);
   int32_t* idx = p.idx ? p.idx + static_cast<int64_t>(u) * p.W : nullptr;
   int32_t* fs = p.free_slots + base;
-  float4 a[V];   // the weights again (a key does not tell -0 from 0), all loads at once
-  if (p.acc_out) {
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v * T < nv && whole(first(v)))
-        a[v] = *reinterpret_cast<const float4*>(p.acc + at0 + 4 * (v * T + tid));
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-    if (v * T < nv) {
-      int at = static_cast<int>(before + cnt[v * kWarps + wp]) + lower(kept[v]);
-      const int j = first(v);
-      const int64_t g = at0 + 4 * (v * T + tid);
-      const bool full = whole(j);
-      const uint32_t k = kept[v];
-      if (full) {
-        *reinterpret_cast<uchar4*>(p.keep + g) =
-            make_uchar4(k & 1u, (k >> 1) & 1u, (k >> 2) & 1u, (k >> 3) & 1u);
-        if (p.acc_out) {
-          *reinterpret_cast<float4*>(p.acc_out + g) =
-              make_float4(k & 1u ? a[v].x : 0.f, k & 2u ? a[v].y : 0.f, k & 4u ? a[v].z : 0.f,
-                          k & 8u ? a[v].w : 0.f);
-        }
-      }
+#pragma unroll 2
+  for (int r = 0; r < nr; ++r) {
+    const int v = r * T + tid;
+    const uint32_t k = v < nv ? kept4(v) : 0u;
+    int at = static_cast<int>(before + cnt[r * kWarps + wp]) + lower(k);
+    if (v >= nv) continue;
+    const int64_t g = at0 + 4 * v;
+    const bool full = whole(v);
+    const int row0 = lo - skew + 4 * v;
+    // the weights again (a key does not tell -0 from 0)
+    const float4 a = p.acc_out ? acc4(v) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 o = make_float4(k & 1u ? a.x : 0.f, k & 2u ? a.y : 0.f, k & 4u ? a.z : 0.f,
+                                 k & 8u ? a.w : 0.f);
+    if (full) {
+      // bits 0..3 to bytes
+      *reinterpret_cast<uint32_t*>(p.keep + g) =
+          (k & 1u) | (k & 2u) << 7 | (k & 4u) << 14 | (k & 8u) << 21;
+      if (p.acc_out) *reinterpret_cast<float4*>(p.acc_out + g) = o;
+    } else {
+      const float w[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (j + c >= 0 && j + c < n) {
-          const bool stays = (k >> c) & 1u;
-          const int row = lo + j + c;
-          if (!full) {
-            p.keep[g + c] = stays ? 1 : 0;
-            if (p.acc_out) p.acc_out[g + c] = stays ? p.acc[g + c] : 0.f;
-          }
-          if (!stays) fs[row - at] = row;
-          else if (idx && at < p.W) idx[at] = row;
-          at += stays ? 1 : 0;
+        if (inside(v, c)) {
+          p.keep[g + c] = (k >> c) & 1u;
+          if (p.acc_out) p.acc_out[g + c] = w[c];
         }
     }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (full || inside(v, c)) {
+        const bool stays = (k >> c) & 1u;
+        if (!stays) fs[row0 + c - at] = row0 + c;
+        else if (idx && at < p.W) idx[at] = row0 + c;
+        at += stays ? 1 : 0;
+      }
+  }
   // what is left of the list and of idx
   const int nk = static_cast<int>(all);
   for (int i = N - nk + rank * T + tid; i < N; i += cs * T) fs[i] = -1;
@@ -439,11 +489,19 @@ __global__ void __launch_bounds__(T) drop_kernel(const DropParams p, int cs) {
   if (cs > 1) cluster_sync_all();   // a CTA's shared memory is read until here
 }
 
-template <int T, int V, bool kPos>
-cudaError_t launch_one(const DropParams& p, int U, int cs, cudaStream_t st) {
+// Dynamic shared memory of a run of r rows: up to (r + 6) / 4 vectors, and their places.
+template <int T>
+int drop_smem(int run) {
+  const int nv = (run + 6) / 4;
+  return nv * 16 + ((nv + T - 1) / T * (T / 32) + 1) * 4;
+}
+
+template <int T, bool kPos>
+cudaError_t launch_one(const DropParams& p, int U, int run, int cs, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(U) * cs);
   cfg.blockDim = dim3(T);
+  cfg.dynamicSmemBytes = drop_smem<T>(run);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -452,38 +510,50 @@ cudaError_t launch_one(const DropParams& p, int U, int cs, cudaStream_t st) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = cs > 1 ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, drop_kernel<T, V, kPos>, p, cs);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, drop_kernel<T, kPos>, p, cs);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// A run of r rows takes up to (r + 6) / 4 vectors.  With at most one CTA per SM a run is
-// spread over more threads: eight units of 32768 rows take 12.7 us instead of 19.3, but
-// 64 units 32.4 instead of 25.8, since their CTAs no longer fit on the SMs at once.
-template <bool kPos>
-cudaError_t launch_pos(const DropParams& p, int U, int run, int cs, bool few, cudaStream_t st) {
-  if (few) {
-    if (run + 6 <= 4 * 1 * 512) return launch_one<512, 1, kPos>(p, U, cs, st);
-    if (run + 6 <= 4 * 3 * 512) return launch_one<512, 3, kPos>(p, U, cs, st);
-  }
-  if (run + 6 <= 4 * 2 * 128) return launch_one<128, 2, kPos>(p, U, cs, st);
-  if (run + 6 <= 4 * 5 * 128) return launch_one<128, 5, kPos>(p, U, cs, st);
-  if (run + 6 <= 4 * 9 * 128) return launch_one<128, 9, kPos>(p, U, cs, st);
-  return launch_one<512, 9, kPos>(p, U, cs, st);
+constexpr int kMaxRun = 16384;   // rows of a CTA, 64 KB of keys
+
+template <int T, bool kPos>
+cudaError_t configure_one() {
+  return cudaFuncSetAttribute(drop_kernel<T, kPos>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              drop_smem<T>(kMaxRun));
 }
 
 }  // namespace
 
-// CTAs per unit: as many as fill the GPU twice, with runs of 1024 rows at least,
-// and at most 16384 rows a CTA (512 threads, nine vectors each).
+cudaError_t drop_configure() {
+  cudaError_t e = configure_one<128, false>();
+  if (e == cudaSuccess) e = configure_one<128, true>();
+  if (e == cudaSuccess) e = configure_one<256, false>();
+  if (e == cudaSuccess) e = configure_one<256, true>();
+  if (e == cudaSuccess) e = configure_one<512, false>();
+  if (e == cudaSuccess) e = configure_one<512, true>();
+  return e;
+}
+
+// As many threads per unit as the GPU holds for all units at once (1024 per SM at 64
+// registers), at least 128, with a vector each in one CTA and two in a cluster, and at
+// most kMaxRun rows a CTA.  Measured: 2048 units of 2176 rows 33 / 40 / 57 us with 128 /
+// 256 / 512 threads, 148 units 12.6 / 9.5 / 8.4; 64 units of 32768 rows 63 / 36 / 24 us in
+// one CTA, 23 in four of 512 threads and 34 in eight; 8 units 24 us in one, 13 in eight.
 cudaError_t launch_drop(const DropParams& p, int U, int nmax, int nsm, cudaStream_t st) {
-  int cs = 1;
-  while (cs < 8 && ((static_cast<int64_t>(U) * cs < 2 * nsm && nmax > 1024 * cs) ||
-                    nmax > 16384 * cs))
+  const int64_t threads = 1024ll * nsm / U, nv = (nmax + 3) / 4;
+  int T = 128, cs = 1;
+  while (T < 512 && 2 * T <= threads && 2 * T <= nv) T *= 2;
+  while (cs < 8 && ((T == 512 && 2 * cs * T <= threads && 4 * cs * T <= nv) || nmax > kMaxRun * cs))
     cs *= 2;
   const int run = (nmax + cs - 1) / cs;
-  const bool few = static_cast<int64_t>(U) * cs <= nsm;
-  return p.pos ? launch_pos<true>(p, U, run, cs, few, st)
-               : launch_pos<false>(p, U, run, cs, few, st);
+  if (T == 128)
+    return p.pos ? launch_one<128, true>(p, U, run, cs, st)
+                 : launch_one<128, false>(p, U, run, cs, st);
+  if (T == 256)
+    return p.pos ? launch_one<256, true>(p, U, run, cs, st)
+                 : launch_one<256, false>(p, U, run, cs, st);
+  return p.pos ? launch_one<512, true>(p, U, run, cs, st)
+               : launch_one<512, false>(p, U, run, cs, st);
 }
 
 }  // namespace rkv

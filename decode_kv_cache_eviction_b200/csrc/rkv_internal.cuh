@@ -364,6 +364,7 @@ struct DropParams {
   bool vec;                      // the arrays are aligned for vectors of four rows
   int* status;
 };
+cudaError_t drop_configure();
 cudaError_t launch_drop(const DropParams& p, int U, int nmax, int nsm, cudaStream_t st);
 
 }  // namespace rkv
