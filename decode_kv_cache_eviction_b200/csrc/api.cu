@@ -199,7 +199,8 @@ int rkv_create(const rkv_config* cfg, rkv_engine** out) {
   e->max_chunks = score_max_chunks(cfg->max_tokens, cfg->max_units, e->score_ctas, e->rp);
 
   if (select_configure() != cudaSuccess || inplace_configure() != cudaSuccess ||
-      attend_configure() != cudaSuccess || wide_configure() != cudaSuccess || drop_configure() != cudaSuccess) {
+      attend_configure() != cudaSuccess || wide_configure() != cudaSuccess || tile_weights_configure() != cudaSuccess ||
+      drop_configure() != cudaSuccess) {
     delete e;
     return cuda_fail(cudaErrorUnknown);
   }

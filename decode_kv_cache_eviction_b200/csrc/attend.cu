@@ -29,12 +29,9 @@ constexpr int kList = 64;                      // visible-row list (ring) of a w
 constexpr int kRowBytes = 256;
 constexpr int kOStride = 132;                  // floats per output row in shared memory
 
-enum AtMode { kOwn = 0, kPrefix = 1, kWeights = 2 };
+enum AtMode { kOwn = 0, kPrefix = 1 };
 
-template <int kMode>
-__host__ __device__ constexpr int at_stage_bytes() {
-  return kAtTok * kRowBytes * (kMode == kWeights ? 1 : 2);
-}
+constexpr int kStageBytes = 2 * kAtTok * kRowBytes;   // K and V
 
 // Ring depth and warps per SM.  Twelve warps with two stages each hide the steps'
 // latencies better than eight with three (2048 units x 2176 rows: 448 -> 394 us) and
@@ -277,7 +274,7 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
   constexpr int NS = AtCfg<NB>::kStages;
   extern __shared__ __align__(256) uint8_t at_smem[];
   __shared__ AtWarpShared<NS> wsh[W];
-  __shared__ int s_qp[32];
+  __shared__ int s_qp[32];   // positions of the query rows
   __shared__ float s_ml[W][2][32];
   __shared__ float s_lse2[32];
   __shared__ int s_last;
@@ -285,11 +282,11 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
   const int g = lane >> 2, q = lane & 3;
   AtWarpShared<NS>& ws = wsh[wp];
 
-  if (kMode != kWeights) allow_next_launch();   // the own rows' kernel, or the weights'
+  allow_next_launch();   // the own rows' kernel, or the weights'
   // what this CTA works on: rows [row0, row0 + nrow) of queries against groups
   // of the sequence of N rows at `base`
   const int item = blockIdx.x / p.maxch, chunk = blockIdx.x - item * p.maxch;
-  const int row0 = kMode == kWeights ? 0 : static_cast<int>(blockIdx.y) * 32;
+  const int row0 = static_cast<int>(blockIdx.y) * 32;
   int total = p.R;   // query rows of the item
   int64_t base, end;
   int mo = 0;
@@ -312,20 +309,17 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
   };
   // query rows as B fragments: row 8 nb + g, dimensions 16 ks + 2q + {0, 1} and + 8
   uint32_t bq[NB][8][2];
-  auto load_queries = [&](int r0) {
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const int r = r0 + 8 * nb + g;
-      const bool on = kMode == kWeights ? r < p.R : r < nrow;
-      const uint32_t* src = p.Q + (on ? row_of(r) : 0) * 64;
+  for (int nb = 0; nb < NB; ++nb) {
+    const int r = 8 * nb + g;
+    const bool on = r < nrow;
+    const uint32_t* src = p.Q + (on ? row_of(r) : 0) * 64;
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        bq[nb][ks][0] = on ? __ldg(&src[8 * ks + q]) : 0u;
-        bq[nb][ks][1] = on ? __ldg(&src[8 * ks + q + 4]) : 0u;
-      }
+    for (int ks = 0; ks < 8; ++ks) {
+      bq[nb][ks][0] = on ? __ldg(&src[8 * ks + q]) : 0u;
+      bq[nb][ks][1] = on ? __ldg(&src[8 * ks + q + 4]) : 0u;
     }
-  };
-  load_queries(0);
+  }
   const int N = static_cast<int>(end - base);
   int first = 0;
   int64_t qmin, qmax;
@@ -352,12 +346,16 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
     first = prefix_len(p, item);
     qmax = p.q_pos ? static_cast<int64_t>(__ldg(&p.q_pos[item])) : static_cast<int64_t>(first) + N - 1;
     qmin = qmax - (p.nq - 1);
+    if (!kOne) {
+      if (tid < 32) s_qp[tid] = tid < nrow ? clamp32(qmin + (row0 + tid) % p.nq) : INT_MIN;
+      __syncthreads();
+    }
   }
   const int qmax32 = clamp32(qmax), qmin32 = clamp32(qmin);
   const int lo_any = p.local > 0 ? clamp32(qmin - p.local) : INT_MIN;
   const int lo_all = p.local > 0 ? clamp32(qmax - p.local) : INT_MIN;
   Span sp;
-  if (kMode == kWeights || p.pos) {   // every row: all are written, or any may hold any position
+  if (p.pos) {   // any row may hold any position
     sp.gs = sp.start = 0;
     sp.nv = (N + 31) >> 5;
   } else {
@@ -370,28 +368,15 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
   const uint4* Vg = kMode == kPrefix ? p.PV : p.V;
 
   int qp[NB][2], qlo[NB][2];    // limits of this lane's rows 8 nb + 2q + e
-  float lse2[NB][2];            // weights pass: log2 of the rows' sums
-  auto load_limits = [&](int r0) {   // rows r0 .. of this CTA (the weights pass moves on in r0)
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+  for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int x = r0 + 8 * nb + 2 * q + e;
-        if (kMode == kPrefix) {
-          qp[nb][e] = s_qp[x];
-        } else {
-          const bool in = kMode == kWeights ? x < p.R : x < nrow;
-          qp[nb][e] = in ? clamp32(qmin + (row0 + x) % p.nq) : INT_MIN;
-          if (kMode == kWeights)
-            lse2[nb][e] = in ? __ldg(&p.lse2[static_cast<int64_t>(item) * p.R + x]) : INFINITY;
-        }
-        qlo[nb][e] = p.local > 0
-                         ? clamp32(static_cast<int64_t>(qp[nb][e]) - p.local) : INT_MIN;
-      }
-  };
-  load_limits(0);
+    for (int e = 0; e < 2; ++e) {
+      qp[nb][e] = kOne ? qmax32 : s_qp[8 * nb + 2 * q + e];
+      qlo[nb][e] = p.local > 0 ? clamp32(static_cast<int64_t>(qp[nb][e]) - p.local) : INT_MIN;
+    }
 
-  constexpr int kStage = at_stage_bytes<kMode>();
+  constexpr int kStage = kStageBytes;
   uint8_t* ring = at_smem + wp * (NS * kStage);
   const uint32_t ring_a = smem_u32(ring);
   // ldmatrix lane addresses within a stage, K rows as A (tokens x d) and V rows
@@ -451,8 +436,6 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
       } else {
         on = on && sees(ps, qmax32, lo_any, p.sinks);
       }
-      if (kMode == kWeights && !on && slot < N)
-        p.acc_out[base + slot] = p.acc_in ? p.acc_in[base + slot] : 0.f;
       const uint32_t mask = __ballot_sync(0xffffffffu, on);
       if (on) {
         const int at = (head + cnt + __popc(mask & ((1u << lane) - 1u))) & (kList - 1);
@@ -484,7 +467,7 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
           for (int c = 0; c < 4; ++c) {
             const uint32_t d = dst + 8 * h * kRowBytes + (((4 * c + q) ^ g) << 4);
             cp16(d, ks + 4 * c, on);
-            if (kMode != kWeights) cp16(d + kAtTok * kRowBytes, vs + 4 * c, on);
+            cp16(d + kAtTok * kRowBytes, vs + 4 * c, on);
           }
         }
         bool part = false;
@@ -529,283 +512,238 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
         const bool in = h ? in1 : in0;
         return kOne ? in : in && sees(ws.mpos[s][g + 8 * h], qp[nb][e], qlo[nb][e], p.sinks);
       };
-      float wsum0 = 0.f, wsum1 = 0.f;
-      for (int r0 = 0;;) {
-        // logits of 16 tokens x 8 NB query rows
-        float c[NB][4];
+      // logits of 16 tokens x 8 NB query rows
+      float c[NB][4];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[nb][e] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        uint32_t a[4];
+        ldsm4(a, (st_a + kofs) ^ (ks << 5));
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) mma16816(c[nb], a, bq[nb][ks][0], bq[nb][ks][1]);
+      }
+      if constexpr (kOne && kMode == kOwn) {
+        if (p.z && 2 * q < p.gp) {   // logits for the weights, before masks and scaling
+          float* z0 = p.z + (base + ws.mslot[s][g]) * p.gp + 2 * q;
+          float* z1 = p.z + (base + ws.mslot[s][g + 8]) * p.gp + 2 * q;
+          if (p.gp == 1) {
+            if (in0) *z0 = c[0][0];
+            if (in1) *z1 = c[0][2];
+          } else {
+            if (in0) __stcg(reinterpret_cast<float2*>(z0), make_float2(c[0][0], c[0][1]));
+            if (in1) __stcg(reinterpret_cast<float2*>(z1), make_float2(c[0][2], c[0][3]));
+          }
+        }
+      }
+      if (masked) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) c[nb][e] = 0.f;
+          for (int e = 0; e < 2; ++e) {
+            if (!seen(nb, e, 0)) c[nb][e] = -INFINITY;
+            if (!seen(nb, e, 1)) c[nb][2 + e] = -INFINITY;
+          }
+      }
+      uint32_t bh[NB][2], bl[NB][2];
+      float mref[NB][2];
+      bool grew = false;
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          uint32_t a[4];
-          ldsm4(a, (st_a + kofs) ^ (ks << 5));
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) mma16816(c[nb], a, bq[nb][ks][0], bq[nb][ks][1]);
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(c[nb][e], c[nb][2 + e]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          x *= p.scale_log2;
+          grew |= x > m[nb][e];
+          mref[nb][e] = fmaxf(x, m[nb][e]);
         }
-        if constexpr (kMode == kWeights) {
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // m = -inf (nothing seen yet): the factor is 0, and so are O and l
+            const float f = mref[nb][e] == m[nb][e] ? 1.f : ex2(m[nb][e] - mref[nb][e]);
+            m[nb][e] = mref[nb][e];
+            l[nb][e] *= f;
+#pragma unroll
+            for (int mb = 0; mb < 8; ++mb) {
+              O[mb][nb][e] *= f;
+              O[mb][nb][2 + e] *= f;
+            }
+          }
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float ref = m[nb][e] == -INFINITY ? 0.f : m[nb][e];
+          c[nb][e] = ex2(fmaf(c[nb][e], p.scale_log2, -ref));
+          c[nb][2 + e] = ex2(fmaf(c[nb][2 + e], p.scale_log2, -ref));
+          l[nb][e] += c[nb][e] + c[nb][2 + e];
+        }
+        // p as the sum of two bf16 (about 16 bits): one bf16 alone would cost the
+        // result as much again as its own rounding, and the steps are not the bound
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float x = c[nb][2 * h], y = c[nb][2 * h + 1];
+          const uint32_t hi = pack_bf16(x, y);
+          const uint32_t lo = pack_bf16(x - bf_lo(hi), y - bf_hi(hi));
+          bh[nb][h] = transpose8x8(hi);
+          bl[nb][h] = transpose8x8(lo);
+        }
+      }
+      if (careful) {
+        // tokens whose V row holds a value that is not finite
+        uint32_t bad = 0;
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          const int r = 2 * i + (lane >> 4);
+          const uint4 x = *reinterpret_cast<const uint4*>(
+              ring + s * kStage + kAtTok * kRowBytes + r * kRowBytes + (lane & 15) * 16);
+          auto two = [](uint32_t w) {
+            return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+          };
+          const uint32_t b =
+              __ballot_sync(0xffffffffu, two(x.x) || two(x.y) || two(x.z) || two(x.w));
+          bad |= ((b & 0xffffu) ? 1u : 0u) << (2 * i) | ((b >> 16) ? 1u : 0u) << (2 * i + 1);
+        }
+#pragma unroll 1
+        for (; bad; bad &= bad - 1u) {
+          const int t = __ffs(bad) - 1;
+          uint8_t* vr = ring + s * kStage + kAtTok * kRowBytes + t * kRowBytes;
+          float pv[NB][2];
+          bool on[NB][2];
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              if (!masked || seen(nb, e, 0)) wsum0 += ex2(fmaf(c[nb][e], p.scale_log2, -lse2[nb][e]));
-              if (!masked || seen(nb, e, 1))
-                wsum1 += ex2(fmaf(c[nb][2 + e], p.scale_log2, -lse2[nb][e]));
+              const float a = __shfl_sync(0xffffffffu, c[nb][e], (t & 7) * 4 + q);
+              const float b = __shfl_sync(0xffffffffu, c[nb][2 + e], (t & 7) * 4 + q);
+              pv[nb][e] = t < 8 ? a : b;
+              on[nb][e] = kOne || sees(ws.mpos[s][t], qp[nb][e], qlo[nb][e], p.sinks);
             }
-          r0 += 8 * NB;
-          if (8 * NB < p.R) {   // the next rows, or back to the first ones
-            load_queries(r0 < p.R ? r0 : 0);
-            load_limits(r0 < p.R ? r0 : 0);
-          }
-          if (r0 < p.R) continue;
-          break;
-        } else {
-          if constexpr (kOne && kMode == kOwn) {
-            if (p.z && 2 * q < p.gp) {   // logits for the weights, before masks and scaling
-              float* z0 = p.z + (base + ws.mslot[s][g]) * p.gp + 2 * q;
-              float* z1 = p.z + (base + ws.mslot[s][g + 8]) * p.gp + 2 * q;
-              if (p.gp == 1) {
-                if (in0) *z0 = c[0][0];
-                if (in1) *z1 = c[0][2];
-              } else {
-                if (in0) __stcg(reinterpret_cast<float2*>(z0), make_float2(c[0][0], c[0][1]));
-                if (in1) __stcg(reinterpret_cast<float2*>(z1), make_float2(c[0][2], c[0][3]));
-              }
-            }
-          }
-          if (masked) {
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                if (!seen(nb, e, 0)) c[nb][e] = -INFINITY;
-                if (!seen(nb, e, 1)) c[nb][2 + e] = -INFINITY;
-              }
-          }
-          uint32_t bh[NB][2], bl[NB][2];
-          float mref[NB][2];
-          bool grew = false;
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float x = fmaxf(c[nb][e], c[nb][2 + e]);
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-              x *= p.scale_log2;
-              grew |= x > m[nb][e];
-              mref[nb][e] = fmaxf(x, m[nb][e]);
-            }
-          if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                // m = -inf (nothing seen yet): the factor is 0, and so are O and l
-                const float f = mref[nb][e] == m[nb][e] ? 1.f : ex2(m[nb][e] - mref[nb][e]);
-                m[nb][e] = mref[nb][e];
-                l[nb][e] *= f;
-#pragma unroll
-                for (int mb = 0; mb < 8; ++mb) {
-                  O[mb][nb][e] *= f;
-                  O[mb][nb][2 + e] *= f;
-                }
-              }
-          }
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float ref = m[nb][e] == -INFINITY ? 0.f : m[nb][e];
-              c[nb][e] = ex2(fmaf(c[nb][e], p.scale_log2, -ref));
-              c[nb][2 + e] = ex2(fmaf(c[nb][2 + e], p.scale_log2, -ref));
-              l[nb][e] += c[nb][e] + c[nb][2 + e];
-            }
-            // p as the sum of two bf16 (about 16 bits): one bf16 alone would cost the
-            // result as much again as its own rounding, and the steps are not the bound
+          for (int mb = 0; mb < 8; ++mb)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float x = c[nb][2 * h], y = c[nb][2 * h + 1];
-              const uint32_t hi = pack_bf16(x, y);
-              const uint32_t lo = pack_bf16(x - bf_lo(hi), y - bf_hi(hi));
-              bh[nb][h] = transpose8x8(hi);
-              bl[nb][h] = transpose8x8(lo);
-            }
-          }
-          if (careful) {
-            // tokens whose V row holds a value that is not finite
-            uint32_t bad = 0;
-#pragma unroll 1
-            for (int i = 0; i < 8; ++i) {
-              const int r = 2 * i + (lane >> 4);
-              const uint4 x = *reinterpret_cast<const uint4*>(
-                  ring + s * kStage + kAtTok * kRowBytes + r * kRowBytes + (lane & 15) * 16);
-              auto two = [](uint32_t w) {
-                return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-              };
-              const uint32_t b =
-                  __ballot_sync(0xffffffffu, two(x.x) || two(x.y) || two(x.z) || two(x.w));
-              bad |= ((b & 0xffffu) ? 1u : 0u) << (2 * i) | ((b >> 16) ? 1u : 0u) << (2 * i + 1);
-            }
-#pragma unroll 1
-            for (; bad; bad &= bad - 1u) {
-              const int t = __ffs(bad) - 1;
-              uint8_t* vr = ring + s * kStage + kAtTok * kRowBytes + t * kRowBytes;
-              float pv[NB][2];
-              bool on[NB][2];
+              const int ch = (2 * mb + h) ^ (t & 7);
+              const float x = __bfloat162float(
+                  *reinterpret_cast<const __nv_bfloat16*>(vr + ch * 16 + g * 2));
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const float a = __shfl_sync(0xffffffffu, c[nb][e], (t & 7) * 4 + q);
-                  const float b = __shfl_sync(0xffffffffu, c[nb][2 + e], (t & 7) * 4 + q);
-                  pv[nb][e] = t < 8 ? a : b;
-                  on[nb][e] = kOne || sees(ws.mpos[s][t], qp[nb][e], qlo[nb][e], p.sinks);
-                }
-#pragma unroll
-              for (int mb = 0; mb < 8; ++mb)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const int ch = (2 * mb + h) ^ (t & 7);
-                  const float x = __bfloat162float(
-                      *reinterpret_cast<const __nv_bfloat16*>(vr + ch * 16 + g * 2));
-#pragma unroll
-                  for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                      if (on[nb][e]) O[mb][nb][2 * h + e] += pv[nb][e] * x;
-                }
-              __syncwarp();
-              if (lane < 16) *reinterpret_cast<uint4*>(vr + lane * 16) = make_uint4(0, 0, 0, 0);
-              __syncwarp();
+                for (int e = 0; e < 2; ++e)
+                  if (on[nb][e]) O[mb][nb][2 * h + e] += pv[nb][e] * x;
             }
-          }
-          // O^T (128 d x 8 NB) += V^T (128 d x 16) . p^T (16 x 8 NB)
-#pragma unroll
-          for (int mb = 0; mb < 8; ++mb) {
-            uint32_t a[4];
-            ldsm4_t(a, (st_a + vofs) ^ (mb << 5));
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              mma16816(O[mb][nb], a, bh[nb][0], bh[nb][1]);
-              mma16816(O[mb][nb], a, bl[nb][0], bl[nb][1]);
-            }
-          }
-          break;
+          __syncwarp();
+          if (lane < 16) *reinterpret_cast<uint4*>(vr + lane * 16) = make_uint4(0, 0, 0, 0);
+          __syncwarp();
         }
       }
-      if constexpr (kMode == kWeights) {
-        // a token's sum over its query rows: the four lanes of its group
-        wsum0 += __shfl_xor_sync(0xffffffffu, wsum0, 1);
-        wsum0 += __shfl_xor_sync(0xffffffffu, wsum0, 2);
-        wsum1 += __shfl_xor_sync(0xffffffffu, wsum1, 1);
-        wsum1 += __shfl_xor_sync(0xffffffffu, wsum1, 2);
-        if (q == 0) {
-          if (in0) {
-            const int64_t i = base + ws.mslot[s][g];
-            p.acc_out[i] = (p.acc_in ? p.acc_in[i] : 0.f) + wsum0;
-          }
-          if (in1) {
-            const int64_t i = base + ws.mslot[s][g + 8];
-            p.acc_out[i] = (p.acc_in ? p.acc_in[i] : 0.f) + wsum1;
-          }
+      // O^T (128 d x 8 NB) += V^T (128 d x 16) . p^T (16 x 8 NB)
+#pragma unroll
+      for (int mb = 0; mb < 8; ++mb) {
+        uint32_t a[4];
+        ldsm4_t(a, (st_a + vofs) ^ (mb << 5));
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          mma16816(O[mb][nb], a, bh[nb][0], bh[nb][1]);
+          mma16816(O[mb][nb], a, bl[nb][0], bl[nb][1]);
         }
       }
       __syncwarp();   // this stage's slot is written next
     }
     cp_wait<0>();
-    if constexpr (kMode == kWeights) {
-      return;
-    } else {
-      if (careful) break;
-      bool ok = true;
+    if (careful) break;
+    bool ok = true;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int mb = 0; mb < 8; ++mb)
+      for (int mb = 0; mb < 8; ++mb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) ok = ok && finite(O[mb][nb][e]);
-      if (!__any_sync(0xffffffffu, !ok)) break;
-      __syncwarp();
+        for (int e = 0; e < 4; ++e) ok = ok && finite(O[mb][nb][e]);
+    if (!__any_sync(0xffffffffu, !ok)) break;
+    __syncwarp();
+  }
+  // the warps' parts to shared memory (the rings are done with), then joined
+  __syncthreads();
+  float* sO = reinterpret_cast<float*>(at_smem);   // [warp][8 NB][kOStride]
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float x = l[nb][e];
+      x += __shfl_xor_sync(0xffffffffu, x, 4);
+      x += __shfl_xor_sync(0xffffffffu, x, 8);
+      x += __shfl_xor_sync(0xffffffffu, x, 16);
+      const int r = 8 * nb + 2 * q + e;
+      if (g == 0) {
+        s_ml[wp][0][r] = m[nb][e];
+        s_ml[wp][1][r] = x;
+      }
+      float* o = sO + (wp * 8 * NB + r) * kOStride;
+#pragma unroll
+      for (int mb = 0; mb < 8; ++mb) {
+        o[16 * mb + g] = O[mb][nb][e];
+        o[16 * mb + g + 8] = O[mb][nb][2 + e];
+      }
     }
   }
-  if constexpr (kMode != kWeights) {
-    // the warps' parts to shared memory (the rings are done with), then joined
-    __syncthreads();
-    float* sO = reinterpret_cast<float*>(at_smem);   // [warp][8 NB][kOStride]
+  __syncthreads();
+  // the prefix's parts: this launch may have started while they were computed
+  if (kMode == kOwn && p.pre_o) wait_for_previous_launch();
+  // one warp per query row, lane = four dimensions
+  for (int r = wp; r < min(nrow, 8 * NB); r += W) {
+    RowSum x = no_rows();
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = l[nb][e];
-        x += __shfl_xor_sync(0xffffffffu, x, 4);
-        x += __shfl_xor_sync(0xffffffffu, x, 8);
-        x += __shfl_xor_sync(0xffffffffu, x, 16);
-        const int r = 8 * nb + 2 * q + e;
-        if (g == 0) {
-          s_ml[wp][0][r] = m[nb][e];
-          s_ml[wp][1][r] = x;
-        }
-        float* o = sO + (wp * 8 * NB + r) * kOStride;
-#pragma unroll
-        for (int mb = 0; mb < 8; ++mb) {
-          o[16 * mb + g] = O[mb][nb][e];
-          o[16 * mb + g + 8] = O[mb][nb][2 + e];
-        }
-      }
+    for (int w = 0; w < W; ++w) {
+      const float4 o = *reinterpret_cast<const float4*>(sO + (w * 8 * NB + r) * kOStride + 4 * lane);
+      x = add_rows(x, {s_ml[w][0][r], s_ml[w][1][r], o});
     }
-    __syncthreads();
-    // the prefix's parts: this launch may have started while they were computed
-    if (kMode == kOwn && p.pre_o) wait_for_previous_launch();
-    // one warp per query row, lane = four dimensions
-    for (int r = wp; r < min(nrow, 8 * NB); r += W) {
-      RowSum x = no_rows();
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float4 o = *reinterpret_cast<const float4*>(sO + (w * 8 * NB + r) * kOStride + 4 * lane);
-        x = add_rows(x, {s_ml[w][0][r], s_ml[w][1][r], o});
-      }
-      const int64_t row = row_of(r);
-      if (p.part_o) {
-        const int64_t at =
-            kMode == kPrefix
-                ? static_cast<int64_t>(chunk) * p.rows + row
-                : (static_cast<int64_t>(item) * p.maxch + chunk) * p.R + row0 + r;
-        __stcg(reinterpret_cast<float4*>(p.part_o + at * 128 + 4 * lane), x.o);
-        if (lane == 0) __stcg(&p.part_ml[at], make_float2(x.M, x.L));
-      } else {
-        x = join_prefix(p, x, row, item);
-        attend_store(p, row, lane, x.M, x.L, x.o);
-        if (lane == 0) s_lse2[r] = x.L == 0.f ? INFINITY : x.M + log2f(x.L);
-      }
+    const int64_t row = row_of(r);
+    if (p.part_o) {
+      const int64_t at =
+          kMode == kPrefix
+              ? static_cast<int64_t>(chunk) * p.rows + row
+              : (static_cast<int64_t>(item) * p.maxch + chunk) * p.R + row0 + r;
+      __stcg(reinterpret_cast<float4*>(p.part_o + at * 128 + 4 * lane), x.o);
+      if (lane == 0) __stcg(&p.part_ml[at], make_float2(x.M, x.L));
+    } else {
+      x = join_prefix(p, x, row, item);
+      attend_store(p, row, lane, x.M, x.L, x.o);
+      if (lane == 0) s_lse2[r] = x.L == 0.f ? INFINITY : x.M + log2f(x.L);
     }
-    if constexpr (kMode == kOwn) {
-      if (p.part_o) {
-        // the CTA that finishes a unit's rows last joins its parts
-        __threadfence();
-        __syncthreads();
-        int* cnt = p.count + static_cast<int64_t>(item) * gridDim.y + blockIdx.y;
-        if (tid == 0) s_last = atomicAdd(cnt, 1) == p.maxch - 1;
-        __syncthreads();
-        if (!s_last) return;
-        __threadfence();
-        if (tid == 0) *cnt = 0;   // ready for the next call
-        const int64_t at0 = static_cast<int64_t>(item) * p.maxch * p.R + row0;
-        for (int r = wp; r < nrow; r += W) {
-          RowSum x = join_row(no_rows(), p.maxch, [&](int c, float2& ml, const float4*& src) {
-            const int64_t at = at0 + static_cast<int64_t>(c) * p.R + r;
-            ml = __ldcg(&p.part_ml[at]);
-            src = reinterpret_cast<const float4*>(p.part_o + at * 128);
-          });
-          x = join_prefix(p, x, row_of(r), item);
-          attend_store(p, row_of(r), lane, x.M, x.L, x.o);
-        }
-      } else if (kOne && p.z) {
-        __syncthreads();   // all logits of the unit are written
-        weights_any(p, base, first, qmax, s_lse2, 0, N);
+  }
+  if constexpr (kMode == kOwn) {
+    if (p.part_o) {
+      // the CTA that finishes a unit's rows last joins its parts
+      __threadfence();
+      __syncthreads();
+      int* cnt = p.count + static_cast<int64_t>(item) * gridDim.y + blockIdx.y;
+      if (tid == 0) s_last = atomicAdd(cnt, 1) == p.maxch - 1;
+      __syncthreads();
+      if (!s_last) return;
+      __threadfence();
+      if (tid == 0) *cnt = 0;   // ready for the next call
+      const int64_t at0 = static_cast<int64_t>(item) * p.maxch * p.R + row0;
+      for (int r = wp; r < nrow; r += W) {
+        RowSum x = join_row(no_rows(), p.maxch, [&](int c, float2& ml, const float4*& src) {
+          const int64_t at = at0 + static_cast<int64_t>(c) * p.R + r;
+          ml = __ldcg(&p.part_ml[at]);
+          src = reinterpret_cast<const float4*>(p.part_o + at * 128);
+        });
+        x = join_prefix(p, x, row_of(r), item);
+        attend_store(p, row_of(r), lane, x.M, x.L, x.o);
       }
+    } else if (kOne && p.z) {
+      __syncthreads();   // all logits of the unit are written
+      weights_any(p, base, first, qmax, s_lse2, 0, N);
     }
   }
 }
@@ -835,8 +773,8 @@ __global__ void __launch_bounds__(128) finish_kernel(const __grid_constant__ Att
 
 template <int NB, int kMode, int W>
 __host__ __device__ constexpr int at_smem_bytes() {
-  const int ring = W * AtCfg<NB>::kStages * at_stage_bytes<kMode>();
-  const int fin = kMode == kWeights ? 0 : W * 8 * NB * kOStride * 4;
+  const int ring = W * AtCfg<NB>::kStages * kStageBytes;
+  const int fin = W * 8 * NB * kOStride * 4;
   return ring > fin ? ring : fin;
 }
 
@@ -894,7 +832,6 @@ cudaError_t attend_configure() {
   if (e == cudaSuccess) e = configure_one<1, kOwn, true, 4>();
   if (e == cudaSuccess) e = configure_one<1, kOwn, true, 2>();
   if (e == cudaSuccess) e = configure_mode<kPrefix, 4>();
-  if (e == cudaSuccess) e = configure_mode<kWeights, 4>();
   return e;
 }
 
@@ -917,9 +854,7 @@ cudaError_t launch_attend_finish(const AttendParams& p, cudaStream_t st) {
 }
 
 cudaError_t launch_attend_weights(const AttendParams& p, int U, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(U) * p.maxch, 1);
-  if (p.z) return launch_early(weights_kernel, p, grid, 256, 0, true, st);
-  return launch_mode<kWeights, 4>(p, p.R, grid, false, st);
+  return launch_early(weights_kernel, p, dim3(static_cast<unsigned>(U) * p.maxch), 256, 0, true, st);
 }
 
 }  // namespace rkv

@@ -1,0 +1,268 @@
+// The weights of every cached row where the attention pass left no logits behind:
+// acc_out_i = acc_in_i + sum_r p_{r,i} over a unit's R query rows, from K and the rows'
+// log-sums, p = 2^(z - lse2).
+//
+// The logits are computed again with the TOKENS as the M side of tcgen05.mma: S^T (128
+// tokens x R) = K_tile Q^T, a token per tensor-memory lane, so one thread adds its
+// token's R weights without any exchange and writes one coalesced float.  K tiles come by
+// TMA; a CTA takes a run of a unit's tiles, with two S^T buffers, so the product of the
+// next tile and the loads of the ones after it run beside the sums.  Tiles that no query
+// sees are not read.
+//
+// Bound: HBM, 256 + 8 bytes per row (R = 32: a tile of 128 rows costs 256 cycles of 2^x
+// and 1400 of its share of HBM).  39 units of 2900 rows, R = 32: TIME us; on m16n8k16
+// steps, which spread a token's query rows over four lanes, 29.
+#include "attend_common.cuh"
+
+namespace rkv {
+namespace {
+
+constexpr int kTok = kWideTile;
+constexpr uint32_t kTileB = kTok * 256;     // a K tile: two halves of 64 columns
+constexpr uint64_t kDrainNs = 100000000ull;
+
+// kBig: up to 256 query rows and one CTA per SM, else up to 64 and two.
+template <bool kBig>
+struct WLayout {
+  static constexpr int kStages = kBig ? 4 : 2;
+  static constexpr int kRows = kBig ? 256 : 64;
+  static constexpr uint32_t ring = 0;
+  static constexpr uint32_t q = kStages * kTileB;
+  static constexpr uint32_t qp = q + kRows * 256;             // [kRows] positions
+  static constexpr uint32_t lse = qp + kRows * 4;             // [kRows]
+  static constexpr uint32_t bars = lse + kRows * 4;
+  static constexpr uint32_t misc = bars + (2 * kStages + 5) * 8;
+  static constexpr uint32_t total = misc + 24;
+  static constexpr uint32_t alloc = total + 1024;
+};
+
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t par) {
+  const uint32_t a = smem_u32(bar);
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(a, par))
+    if (globaltimer_ns() - t0 > kDrainNs) return;
+}
+
+template <bool kBig>
+__global__ void __launch_bounds__(192, kBig ? 1 : 2)
+    tile_weights_kernel(const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ AttendParams p) {
+  using Lay = WLayout<kBig>;
+  constexpr int NS = Lay::kStages;
+  extern __shared__ uint8_t w_raw[];
+  uint8_t* sm = w_raw + ((1024u - (smem_u32(w_raw) & 1023u)) & 1023u);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + Lay::bars);
+  uint64_t* empty = full + NS;
+  uint64_t* d_full = empty + NS;   // [2] S^T of a tile is in tensor memory
+  uint64_t* d_empty = d_full + 2;  // [2] it has been read
+  uint64_t* mdone = d_empty + 2;
+  int* s_qp = reinterpret_cast<int*>(sm + Lay::qp);
+  float* s_lse = reinterpret_cast<float*>(sm + Lay::lse);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Lay::misc);
+  volatile int* abort = reinterpret_cast<volatile int*>(sm + Lay::misc + 4);
+  int8_t* lastp = reinterpret_cast<int8_t*>(sm + Lay::misc + 8);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  const int item = blockIdx.x / p.maxch, chunk = blockIdx.x - item * p.maxch;
+  const int64_t base = __ldg(&p.tok_off[item]);
+  const int N = static_cast<int>(__ldg(&p.tok_off[item + 1]) - base);
+  const int first = prefix_len(p, item);
+  const int tiles = (N + kTok - 1) / kTok;
+  const int t_end = min(tiles, (chunk + 1) * p.gpc), t_begin = chunk * p.gpc;
+  if (t_begin >= t_end) return;
+  const int R = p.R, NQ = (R + 15) & ~15;   // query rows, and as the N side of the product
+  const int64_t qmax = p.q_pos ? static_cast<int64_t>(__ldg(&p.q_pos[item]))
+                               : static_cast<int64_t>(first) + N - 1;
+  const int64_t qmin = qmax - (p.nq - 1);
+  const int qmax32 = clamp32(qmax), qmin32 = clamp32(qmin);
+  const int lo_any = p.local > 0 ? clamp32(qmin - p.local) : INT_MIN;
+  const int lo_all = p.local > 0 ? clamp32(qmax - p.local) : INT_MIN;
+  // whether a query may see a row of tile t (rows in the order of their positions)
+  auto needed = [&](int t) {
+    if (p.pos) return true;
+    const int a = first + t * kTok, b = a + kTok - 1;
+    return a <= qmax32 && (b > lo_any || a < p.sinks);
+  };
+
+  if (tid == 0) {
+    prefetch_tmap(&kmap);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      lastp[s] = -1;
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&d_full[i], 1);
+      mbar_init(&d_empty[i], 4);   // warps
+    }
+    mbar_init(mdone, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  // tensor-memory columns: a power of two, two buffers of NQ
+  uint32_t cols = 32;
+  while (cols < 2u * NQ) cols *= 2;
+  if (warp == 1) {
+    tmem_alloc<1>(tmem_slot, cols);
+    tmem_relinquish<1>();
+  }
+  // Q in the layout that TMA writes for K, halves of NQ rows of 128 bytes
+  for (int i = tid; i < NQ * 16; i += 192) {
+    const int r = i >> 4, c = i & 15;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (r < R)
+      v = __ldg(reinterpret_cast<const uint4*>(p.Q) + (static_cast<int64_t>(item) * R + r) * 16 + c);
+    *reinterpret_cast<uint4*>(sm + Lay::q + (c >> 3) * NQ * 128 + r * 128 +
+                              (((c & 7) ^ (r & 7)) << 4)) = v;
+  }
+  for (int r = tid; r < NQ; r += 192) {
+    s_qp[r] = r < R ? clamp32(qmin + r % p.nq) : INT_MIN;
+    // a padded row weighs nothing
+    s_lse[r] = r < R ? __ldg(&p.lse2[static_cast<int64_t>(item) * R + r]) : INFINITY;
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_first();
+      int n = 0;
+      for (int t = t_begin; t < t_end; ++t) {
+        if (!needed(t)) continue;
+        const int s = n % NS;
+        const uint32_t ph = (n / NS) & 1;
+        if (!mbar_wait(&empty[s], ph ^ 1, abort, p.status)) break;
+        uint8_t* dst = sm + Lay::ring + s * kTileB;
+        const int y = static_cast<int>(base + static_cast<int64_t>(t) * kTok);
+        mbar_arrive_expect_tx(&full[s], kTileB);
+        tma_load_2d(dst, &kmap, &full[s], 0, y, pol);
+        tma_load_2d(dst + kTileB / 2, &kmap, &full[s], 64, y, pol);
+        lastp[s] = static_cast<int8_t>(ph);
+        ++n;
+      }
+      // teardown: every copy issued has landed before the CTA exits
+      for (int s = 0; s < NS; ++s)
+        if (lastp[s] >= 0) drain(&full[s], lastp[s]);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t leader = elect_leader();
+    const uint32_t idesc = idesc_bf16_f32(kTok, NQ);
+    const uint64_t kd = desc_kmajor_sw128(smem_u32(sm + Lay::ring));
+    const uint64_t qd = desc_kmajor_sw128(smem_u32(sm + Lay::q));
+    const uint32_t a_full = smem_u32(d_full), a_empty = smem_u32(empty);
+    int n = 0;
+    bool ok = true;
+    for (int t = t_begin; ok && t < t_end; ++t) {
+      if (!needed(t)) continue;
+      const int s = n % NS, b = n & 1;
+      ok = mbar_wait(&full[s], (n / NS) & 1, abort, p.status);
+      ok = ok && mbar_wait(&d_empty[b], ((n >> 1) & 1) ^ 1, abort, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t ko = ((k >> 2) * (kTileB / 2) + (k & 3) * 32) >> 4;
+        const uint32_t qo = ((k >> 2) * NQ * 128 + (k & 3) * 32) >> 4;
+        mma_bf16_by(leader, tmem + b * NQ, kd + s * (kTileB >> 4) + ko, qd + qo, idesc, k > 0);
+      }
+      mma_commit_by(leader, a_empty + 8 * s);
+      mma_commit_by(leader, a_full + 8 * b);
+      ++n;
+    }
+    // teardown: all MMAs (and their commits) are complete before TMEM is freed
+    mma_commit_by(leader, smem_u32(mdone));
+    drain(mdone, 0);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ a token per thread
+    const int w4 = warp & 3;   // the tensor-memory lanes that this warp may read
+    const uint32_t lanes = static_cast<uint32_t>(32 * w4) << 16;
+    int n = 0;
+    bool ok = true;
+    for (int t = t_begin; ok && t < t_end; ++t) {
+      const int i = t * kTok + 32 * w4 + lane;
+      const bool in = i < N;
+      const int64_t at = base + i;
+      float sum = in && p.acc_in ? p.acc_in[at] : 0.f;
+      if (needed(t)) {
+        int ps = first + i;
+        bool on = in;
+        if (in && p.keep) on = __ldg(&p.keep[at]) != 0;
+        if (in && p.pos) ps = __ldg(&p.pos[at]);
+        // seen by every query, by none, or by some
+        const bool all = on && sees(ps, qmin32, lo_all, p.sinks);
+        on = on && sees(ps, qmax32, lo_any, p.sinks);
+        const int b = n & 1;
+        ok = mbar_wait(&d_full[b], (n >> 1) & 1, abort, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const bool masked = __any_sync(0xffffffffu, on && !all);
+        float w = 0.f;
+        for (int c0 = 0; c0 < NQ; c0 += 16) {
+          uint32_t z[16];
+          tmem_ld16(tmem + lanes + b * NQ + c0, z);
+          tmem_wait_ld_dep(z);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float x = ex2(fmaf(__uint_as_float(z[c]), p.scale_log2, -s_lse[c0 + c]));
+            if (masked) {
+              const int qp = s_qp[c0 + c];
+              const int lo = p.local > 0 ? clamp32(static_cast<int64_t>(qp) - p.local) : INT_MIN;
+              if (sees(ps, qp, lo, p.sinks)) w += x;
+            } else {
+              w += x;
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&d_empty[b]);
+        if (on) sum += w;   // what lies in a dead row is dropped with its sum
+        ++n;
+      }
+      if (in) p.acc_out[at] = sum;
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<1>(tmem, cols);
+  }
+}
+
+}  // namespace
+
+cudaError_t tile_weights_configure() {
+  cudaError_t e = cudaFuncSetAttribute(tile_weights_kernel<false>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       WLayout<false>::alloc);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(tile_weights_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             WLayout<true>::alloc);
+  return e;
+}
+
+int tile_weights_ctas_per_sm(int R) { return R <= 64 ? 2 : 1; }
+
+cudaError_t launch_tile_weights(const CUtensorMap& kmap, const AttendParams& p, int U,
+                                cudaStream_t st) {
+  const unsigned grid = static_cast<unsigned>(U) * p.maxch;
+  if (p.R <= 64)
+    tile_weights_kernel<false><<<grid, 192, WLayout<false>::alloc, st>>>(kmap, p);
+  else
+    tile_weights_kernel<true><<<grid, 192, WLayout<true>::alloc, st>>>(kmap, p);
+  return cudaGetLastError();
+}
+
+}  // namespace rkv

@@ -57,14 +57,14 @@ int check_rows(const rkv_engine* e, const rkv_batch* b, Lengths* L) {
 
 constexpr int64_t kPartFloats = 130;   // a part: 128 values, maximum and sum
 
-// Query rows whose parts the scratch holds: eight waves of CTAs (two per SM) of at
-// most 32 rows; for shared calls also every query row's own and prefix part, and
-// two waves of CTAs of at most 256 rows of a split prefix.
+// Query rows whose parts the scratch holds: two waves of CTAs (three per SM) of at most
+// 32 rows; for shared calls also every query row's own and prefix part, and a wave of
+// CTAs of at most 256 rows of a split prefix.
 int64_t part_rows(const rkv_engine* e, bool shared) {
   const int64_t one = static_cast<int64_t>(e->cfg.group) * e->cfg.window;
   const int64_t all = one * e->cfg.max_units;
-  const int64_t split = 16ll * e->nsm * std::min<int64_t>(one, 32);
-  return split + (shared ? 2 * all + 2ll * e->nsm * std::min<int64_t>(all, 256) : 0);
+  const int64_t split = 6ll * e->nsm * std::min<int64_t>(one, 32);
+  return split + (shared ? 2 * all + static_cast<int64_t>(e->nsm) * std::min<int64_t>(all, 256) : 0);
 }
 // Counters of split units: one per unit and 32 query rows.
 int64_t part_counts(const rkv_engine* e) {
@@ -130,8 +130,8 @@ int pick_chunks(int64_t items, int64_t sum, int64_t nmax, int64_t slots, int64_t
 // weights 5 in a launch of their own or 0.3 per 32 rows and warp at the unit's end.  Measured: 128 units of 32768
 // rows 401 / 324 / 402 / 334 us in 1 / 2 / 4 / 6 chunks (modelled 389 / 340 / 395 / 344),
 // 509 windows of 1028 rows 50 us with two warps and 59 with four (50 / 62).
-void pick_shape(int64_t items, int64_t sum, int64_t nmax, int64_t resident, double step,
-                int64_t cap, bool weights, int* warps, int* chunks) {
+double pick_shape(int64_t items, int64_t sum, int64_t nmax, int64_t resident, double step,
+                  int64_t cap, bool weights, int* warps, int* chunks) {
   const double avg = std::max(1.0, static_cast<double>(sum) / static_cast<double>(items));
   const double share = resident * 8192.0 / 6.5e6;
   auto stage = [&](double part) { return std::max(step, share * part); };
@@ -160,6 +160,33 @@ void pick_shape(int64_t items, int64_t sum, int64_t nmax, int64_t resident, doub
         *chunks = static_cast<int>(c);
       }
     }
+  return least;
+}
+
+// The same for the wide kernel over own rows (tiles of 128, one CTA per SM): 7 us per
+// CTA, per tile 0.95 or its share of HBM, and 4 for the kernel that joins the parts.
+double pick_wide(int64_t items, int64_t sum, int64_t nmax, int64_t slots, int64_t cap,
+                 int* chunks) {
+  const double avg = std::max(1.0, static_cast<double>(sum) / static_cast<double>(items));
+  const double share = slots * 65536.0 / 6.5e6;
+  auto tile = [&](double part) { return std::max(0.95, share * part); };
+  double least = 1e300;
+  for (int64_t c = 1; c <= std::min(std::max<int64_t>(1, cap), nmax); c += c < 4 ? 1 : c / 4) {
+    const int64_t gpc = (nmax + c - 1) / c;
+    const double per = c == 1 ? 1.0
+                       : avg > 0.99 * nmax ? static_cast<double>(c)
+                                           : std::max(1.0, avg / gpc + 0.5);
+    const double waves = static_cast<double>(items) * per / slots;
+    const double full = std::floor(waves), rest = waves - full;
+    double cost = 4.0 + full * (avg / per * tile(1.0) + 7.0);
+    if (full == 0 || rest > 0.02) cost += gpc * tile(rest) + 7.0;
+    cost *= full == 0 ? 0.87 : 1.05;   // against the other model, as measured
+    if (cost < least) {
+      least = cost;
+      *chunks = static_cast<int>(c);
+    }
+  }
+  return least;
 }
 
 int check_prefix(const rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, int64_t* sum,
@@ -298,16 +325,20 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     gmax = std::max(gmax, g);
   }
   int own = 1, warps = 4;
-  pick_shape(rg * static_cast<int64_t>(U), rg * gsum, gmax,
-             static_cast<int64_t>(attend_warps_per_sm(R)) * e->nsm, R <= 16 ? 0.75 : 2.5,
-             cap / rows - (x ? 1 : 0), logits, &warps, &own);
+  const double narrow = pick_shape(rg * static_cast<int64_t>(U), rg * gsum, gmax,
+                                   static_cast<int64_t>(attend_warps_per_sm(R)) * e->nsm,
+                                   R <= 8 ? 0.75 : R <= 16 ? 1.0 : 2.5, cap / rows - (x ? 1 : 0),
+                                   logits, &warps, &own);
   const int64_t used = own > 1 ? static_cast<int64_t>(own) * rows : 0;   // parts of own chunks
   cudaError_t err;
   if (x) {
     const int64_t mrows = static_cast<int64_t>(members) * R;
-    // up to 32 query rows per prefix: HBM-bound, the same kernel as the own rows;
-    // more: 128- or 256-row tiles on tcgen05
-    const bool wide = mrows > 32;
+    // up to 4 query rows per prefix: the same kernel as the own rows; more: 128- or
+    // 256-row tiles on tcgen05 (32 prefixes of 4096 tokens, 4 rows: 16.4 and 18.0 us; 8
+    // prefixes, 8 rows: 18.0 and 14.3; 32 prefixes, 16 rows: 22.9 and 20.3, 24 rows: 36.1
+    // and 21.5).  Up to 16 rows over few tokens also go the first way, whose CTAs share the
+    // SMs with the own rows' (8 prefixes of 2048 tokens, 16 rows: 16.6 and 19.8).
+    const bool wide = mrows > 16 || (mrows > 4 && psum > 2ll * e->nsm * kWideTile);
     const int64_t tile = wide ? kWideTile : 32;
     const int64_t blocks = wide ? (mrows + 255) / 256 : 1;
     int64_t pg = 0, pmax = 1;
@@ -342,10 +373,11 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     if (err != cudaSuccess) return cuda_fail(err);
     ++e->launches;
   }
-  // many query rows over whole units: each unit goes through the wide kernel as a
-  // prefix of its own
-  const bool wide_own = !x && R > 16 && !a->keep && !a->pos && L.T >= 512ll * U;
-  if (wide_own) {
+  // many query rows over whole units: each unit may go through the wide kernel as a
+  // prefix of its own (64 units of 15-16K rows, 32 query rows: 212 us narrow, 90 wide; 512
+  // units of 300 rows, 16 query rows: 21 and 41)
+  bool wide_own = false;
+  if (!x && R > 8 && !a->keep && !a->pos && L.T > 0) {
     const int64_t blocks = (R + 255) / 256;
     int64_t tsum = 0, tmax = 1;
     for (int u = 0; u < U; ++u) {
@@ -354,12 +386,15 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
       tsum += t;
       tmax = std::max(tmax, t);
     }
-    p.PK = p.K;
-    p.PV = p.V;
-    p.pre_off = p.tok_off;
-    p.maxch = pick_chunks(U, tsum, tmax, std::max<int64_t>(1, e->nsm / blocks), cap / rows, 1, 3.0);
-    if (static_cast<int64_t>(p.maxch) * rows <= cap) {
-      p.gpc = static_cast<int>((tmax + p.maxch - 1) / p.maxch);
+    int c = 1;
+    const double cost = pick_wide(U * blocks, tsum * blocks, tmax, e->nsm, cap / rows, &c);
+    wide_own = cost < narrow && static_cast<int64_t>(c) * rows <= cap;
+    if (wide_own) {
+      p.PK = p.K;
+      p.PV = p.V;
+      p.pre_off = p.tok_off;
+      p.maxch = c;
+      p.gpc = static_cast<int>((tmax + c - 1) / c);
       p.part_o = part_o;
       p.part_ml = part_ml;
       p.status = e->status;
@@ -379,7 +414,7 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
       e->launches += 2;
     }
   }
-  if (!wide_own || !p.pre_o) {
+  if (!wide_own) {
     p.maxch = own;
     p.gpc = static_cast<int>((gmax + own - 1) / own);
     if (own > 1) {
@@ -393,14 +428,20 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     if (err != cudaSuccess) return cuda_fail(err);
     ++e->launches;
   }
-  if (a->acc_out && (own > 1 || !p.z)) {   // a unit of one chunk has done its weights
+  if (a->acc_out && L.T > 0 && (own > 1 || !p.z)) {   // a unit of one chunk has done its weights
     AttendParams pw = p;
-    const int64_t all = (static_cast<int64_t>(L.nmax) + 31) / 32;
-    pw.maxch = pick_chunks(U, (L.T + 31) / 32 + U, std::max<int64_t>(all, 1), 3 * e->nsm,
-                           std::max<int64_t>(1, (static_cast<int64_t>(1) << 30) / U), 4, 4.0);
-    pw.gpc = static_cast<int>((std::max<int64_t>(all, 1) + pw.maxch - 1) / pw.maxch);
+    pw.status = e->status;
+    const int64_t tile = p.z ? 32 : kWideTile;   // rows of a group
+    const int64_t all = (static_cast<int64_t>(L.nmax) + tile - 1) / tile;
+    const int64_t wslots = (p.z ? 8 : tile_weights_ctas_per_sm(R)) * static_cast<int64_t>(e->nsm);
+    pw.maxch = pick_chunks(U, L.T / tile + U, all, wslots, (static_cast<int64_t>(1) << 30) / U,
+                           p.z ? 8 : 1, p.z ? 16.0 : 6.0);
+    pw.gpc = static_cast<int>((all + pw.maxch - 1) / pw.maxch);
+    CUtensorMap kmap;
+    if (!p.z && make_map(e, &kmap, b->K, static_cast<uint64_t>(L.T), kWideTile) != RKV_OK)
+      return RKV_ERR_CUDA;
     t_begin(e, RKV_KERNEL_WEIGHT, st);
-    err = launch_attend_weights(pw, U, st);
+    err = p.z ? launch_attend_weights(pw, U, st) : launch_tile_weights(kmap, pw, U, st);
     t_end(e, st);
     if (err != cudaSuccess) return cuda_fail(err);
     ++e->launches;

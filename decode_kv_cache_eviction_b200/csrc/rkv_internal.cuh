@@ -346,6 +346,11 @@ cudaError_t launch_attend_wide(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                const AttendParams& p, int P, int max_rows, cudaStream_t st);
 cudaError_t launch_attend_finish(const AttendParams& p, cudaStream_t st);
 cudaError_t launch_attend_weights(const AttendParams& p, int U, cudaStream_t st);
+// Weights from K: p.gpc tiles of kWideTile rows per chunk.
+cudaError_t tile_weights_configure();
+int tile_weights_ctas_per_sm(int R);
+cudaError_t launch_tile_weights(const CUtensorMap& kmap, const AttendParams& p, int U,
+                                cudaStream_t st);
 
 // ---------------------------------------------------------------- eviction by weight
 struct DropParams {
