@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kAtTok = 16;                     // rows per stage
 constexpr int kList = 64;                      // visible-row list (ring) of a warp
+constexpr int kAhead = 4;                      // groups whose masks are loaded ahead
 constexpr int kRowBytes = 256;
 constexpr int kOStride = 132;                  // floats per output row in shared memory
 
@@ -213,8 +214,9 @@ __device__ __forceinline__ RowSum join_prefix(const AttendParams& p, RowSum s, i
 
 // acc_out = acc_in + sum_r 2^(z_r - lse2_r) for rows i0 .. i1 of a unit, from the
 // logits that the attention pass left in p.z (one query per head, so a row is
-// seen by all heads or by none).  GP: floats per row of p.z.
-template <int GP>
+// seen by all heads or by none).  GP: floats per row of p.z; kRowsAhead: rows of a thread
+// in flight.
+template <int GP, int kRowsAhead>
 __device__ __forceinline__ void weights_from_logits(const AttendParams& p, int64_t base, int first,
                                                     int64_t qpos, const float* lse2, int i0,
                                                     int i1) {
@@ -222,48 +224,65 @@ __device__ __forceinline__ void weights_from_logits(const AttendParams& p, int64
   float ls[GP];
 #pragma unroll
   for (int r = 0; r < GP; ++r) ls[r] = r < p.R ? lse2[r] : INFINITY;
-#pragma unroll 4
-  for (int i = i0 + threadIdx.x; i < i1; i += blockDim.x) {
-    const int64_t at = base + i;
-    float a = p.acc_in ? p.acc_in[at] : 0.f;
-    bool on = !p.keep || p.keep[at] != 0;
-    const int ps = p.pos ? p.pos[at] : first + i;
-    on = on && sees(ps, qp, lo, p.sinks);
-    if (on) {
-      float z[GP];
-      const float* src = p.z + at * GP;
+  for (int i = i0 + threadIdx.x; i < i1; i += kRowsAhead * blockDim.x) {
+    float a[kRowsAhead], z[kRowsAhead][GP];
+    bool on[kRowsAhead];
+#pragma unroll
+    for (int k = 0; k < kRowsAhead; ++k) {
+      const int r = i + k * blockDim.x;
+      const int64_t at = base + r;
+      on[k] = r < i1;
+      a[k] = on[k] && p.acc_in ? p.acc_in[at] : 0.f;
+      int ps = first + r;
+      if (on[k] && p.pos) ps = p.pos[at];
+      if (on[k] && p.keep) on[k] = p.keep[at] != 0;
+      on[k] = on[k] && sees(ps, qp, lo, p.sinks);
+    }
+#pragma unroll
+    for (int k = 0; k < kRowsAhead; ++k) {
+      const float* src = p.z + (base + i + k * blockDim.x) * GP;
+#pragma unroll
+      for (int r = 0; r < GP; ++r) z[k][r] = -INFINITY;
+      if (!on[k]) continue;
       if constexpr (GP == 1) {
-        z[0] = __ldcg(src);
+        z[k][0] = __ldcg(src);
       } else if constexpr (GP == 2) {
         const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
-        z[0] = x.x;
-        z[1] = x.y;
+        z[k][0] = x.x;
+        z[k][1] = x.y;
       } else {
 #pragma unroll
-        for (int k = 0; k < GP / 4; ++k) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(src) + k);
-          z[4 * k] = x.x;
-          z[4 * k + 1] = x.y;
-          z[4 * k + 2] = x.z;
-          z[4 * k + 3] = x.w;
+        for (int c = 0; c < GP / 4; ++c) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(src) + c);
+          z[k][4 * c] = x.x;
+          z[k][4 * c + 1] = x.y;
+          z[k][4 * c + 2] = x.z;
+          z[k][4 * c + 3] = x.w;
         }
       }
-      float w = 0.f;
-#pragma unroll
-      for (int r = 0; r < GP; ++r)
-        if (r < p.R) w += ex2(fmaf(z[r], p.scale_log2, -ls[r]));
-      a += w;
     }
-    p.acc_out[at] = a;
+#pragma unroll
+    for (int k = 0; k < kRowsAhead; ++k) {
+      const int r = i + k * blockDim.x;
+      if (r >= i1) break;
+      float w = 0.f;
+      if (on[k]) {
+#pragma unroll
+        for (int q = 0; q < GP; ++q)
+          if (q < p.R) w += ex2(fmaf(z[k][q], p.scale_log2, -ls[q]));
+      }
+      p.acc_out[base + r] = a[k] + w;
+    }
   }
 }
+template <int kRowsAhead>
 __device__ __forceinline__ void weights_any(const AttendParams& p, int64_t base, int first,
                                             int64_t qpos, const float* lse2, int i0, int i1) {
   switch (p.gp) {
-    case 1: weights_from_logits<1>(p, base, first, qpos, lse2, i0, i1); break;
-    case 2: weights_from_logits<2>(p, base, first, qpos, lse2, i0, i1); break;
-    case 4: weights_from_logits<4>(p, base, first, qpos, lse2, i0, i1); break;
-    default: weights_from_logits<8>(p, base, first, qpos, lse2, i0, i1); break;
+    case 1: weights_from_logits<1, kRowsAhead>(p, base, first, qpos, lse2, i0, i1); break;
+    case 2: weights_from_logits<2, kRowsAhead>(p, base, first, qpos, lse2, i0, i1); break;
+    case 4: weights_from_logits<4, kRowsAhead>(p, base, first, qpos, lse2, i0, i1); break;
+    default: weights_from_logits<8, kRowsAhead / 2>(p, base, first, qpos, lse2, i0, i1); break;
   }
 }
 
@@ -406,26 +425,29 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
     }
     int v = chunk * p.gpc + wp;   // next group of this warp
     int head = 0, cnt = 0;        // list: first entry, entries
-    // a group's live bytes and positions, loaded two groups ahead
-    auto fetch = [&](int vv, int& live, int& ps) {
+    // a group's live bytes and positions, loaded kAhead groups ahead
+    auto fetch = [&](int vv, int& alive, int& ps) {
       const int slot = 32 * sp.group(vv) + lane;
       const bool in = vv < v_end && slot < N;
-      live = in ? 1 : 0;
+      alive = in ? 1 : 0;
       ps = first + slot;
-      if (keep && in) live = __ldg(&keep[base + slot]);
+      if (keep && in) alive = __ldg(&keep[base + slot]);
       if (pos && in) ps = __ldg(&pos[base + slot]);
     };
-    int live0, pos0, live1, pos1;
-    fetch(v, live0, pos0);
-    fetch(v + W, live1, pos1);
+    int live[kAhead], at[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) fetch(v + k * W, live[k], at[k]);
     // rows of group v (virtual order: sinks' groups, then the window's)
     auto scan = [&]() {
       const int slot = 32 * sp.group(v) + lane;
-      const int ps = pos0;
-      bool on = live0 != 0;
-      live0 = live1;
-      pos0 = pos1;
-      fetch(v + 2 * W, live1, pos1);
+      const int ps = at[0];
+      bool on = live[0] != 0;
+#pragma unroll
+      for (int k = 0; k < kAhead - 1; ++k) {
+        live[k] = live[k + 1];
+        at[k] = at[k + 1];
+      }
+      fetch(v + kAhead * W, live[kAhead - 1], at[kAhead - 1]);
       if (kMode == kPrefix && p.local > 0) {
         bool any = false;
         for (int r = 0; r < nrow; ++r) {
@@ -438,9 +460,9 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
       }
       const uint32_t mask = __ballot_sync(0xffffffffu, on);
       if (on) {
-        const int at = (head + cnt + __popc(mask & ((1u << lane) - 1u))) & (kList - 1);
-        ws.slot[at] = slot;
-        ws.pos[at] = ps;
+        const int to = (head + cnt + __popc(mask & ((1u << lane) - 1u))) & (kList - 1);
+        ws.slot[to] = slot;
+        ws.pos[to] = ps;
       }
       cnt += __popc(mask);
       v += W;
@@ -587,15 +609,15 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
           c[nb][2 + e] = ex2(fmaf(c[nb][2 + e], p.scale_log2, -ref));
           l[nb][e] += c[nb][e] + c[nb][2 + e];
         }
-        // p as the sum of two bf16 (about 16 bits): one bf16 alone would cost the
-        // result as much again as its own rounding, and the steps are not the bound
+        // p as the sum of two bf16 (about 16 bits) while the steps are not the bound; with
+        // more than 8 query rows as one (2^-8 of each weight at most, of random sign): the
+        // second part would be a third of the mma.sync steps, which then are
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float x = c[nb][2 * h], y = c[nb][2 * h + 1];
           const uint32_t hi = pack_bf16(x, y);
-          const uint32_t lo = pack_bf16(x - bf_lo(hi), y - bf_hi(hi));
           bh[nb][h] = transpose8x8(hi);
-          bl[nb][h] = transpose8x8(lo);
+          if (NB == 1) bl[nb][h] = transpose8x8(pack_bf16(x - bf_lo(hi), y - bf_hi(hi)));
         }
       }
       if (careful) {
@@ -654,7 +676,7 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           mma16816(O[mb][nb], a, bh[nb][0], bh[nb][1]);
-          mma16816(O[mb][nb], a, bl[nb][0], bl[nb][1]);
+          if (NB == 1) mma16816(O[mb][nb], a, bl[nb][0], bl[nb][1]);
         }
       }
       __syncwarp();   // this stage's slot is written next
@@ -721,7 +743,7 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
     }
   }
   if constexpr (kMode == kOwn) {
-    if (p.part_o) {
+    if (p.count) {
       // the CTA that finishes a unit's rows last joins its parts
       __threadfence();
       __syncthreads();
@@ -741,9 +763,9 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
         x = join_prefix(p, x, row_of(r), item);
         attend_store(p, row_of(r), lane, x.M, x.L, x.o);
       }
-    } else if (kOne && p.z) {
+    } else if (kOne && p.z && !p.part_o) {
       __syncthreads();   // all logits of the unit are written
-      weights_any(p, base, first, qmax, s_lse2, 0, N);
+      weights_any<8>(p, base, first, qmax, s_lse2, 0, N);
     }
   }
 }
@@ -756,18 +778,28 @@ __global__ void __launch_bounds__(256) weights_kernel(const __grid_constant__ At
   const int64_t i0 = static_cast<int64_t>(chunk) * p.gpc * 32;
   wait_for_previous_launch();
   if (i0 >= N) return;
-  weights_any(p, base, prefix_len(p, item), newest_query(p, item),
+  weights_any<4>(p, base, prefix_len(p, item), newest_query(p, item),
               p.lse2 + static_cast<int64_t>(item) * p.R, static_cast<int>(i0),
               static_cast<int>(min(static_cast<int64_t>(N), i0 + static_cast<int64_t>(p.gpc) * 32)));
 }
 
-// Query rows whose parts are all in p.pre_o: own rows that went through the wide
-// kernel, each unit as a prefix of its own.  One warp per query row.
+// Joins the parts of every query row, one warp each: those that the wide kernel left in
+// p.pre_o (a prefix's, or own rows that went through it as a prefix of their own), and
+// those of the unit's chunks in p.part_o.
 __global__ void __launch_bounds__(128) finish_kernel(const __grid_constant__ AttendParams p) {
+  allow_next_launch();
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   wait_for_previous_launch();
   if (row >= p.rows) return;
-  const RowSum x = join_prefix(p, no_rows(), row, static_cast<int>(row / p.R));
+  const int u = static_cast<int>(row / p.R), r = static_cast<int>(row - static_cast<int64_t>(u) * p.R);
+  RowSum x = no_rows();
+  if (p.part_o)
+    x = join_row(x, p.maxch, [&](int c, float2& ml, const float4*& src) {
+      const int64_t at = (static_cast<int64_t>(u) * p.maxch + c) * p.R + r;
+      ml = p.part_ml[at];
+      src = reinterpret_cast<const float4*>(p.part_o + at * 128);
+    });
+  x = join_prefix(p, x, row, u);
   attend_store(p, row, threadIdx.x & 31, x.M, x.L, x.o);
 }
 

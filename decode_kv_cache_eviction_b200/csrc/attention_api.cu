@@ -123,6 +123,18 @@ int pick_chunks(int64_t items, int64_t sum, int64_t nmax, int64_t slots, int64_t
   return static_cast<int>(best);
 }
 
+// Group counts of up to 32 units, evenly spaced over the batch, and what they say of all.
+struct Sample {
+  int n = 0;
+  int groups[32];
+  // chunks of gpc groups that a unit takes on average, and groups of a chunk
+  double per(int64_t gpc) const {
+    int64_t s = 0;
+    for (int i = 0; i < n; ++i) s += std::max<int64_t>(1, (groups[i] + gpc - 1) / gpc);
+    return static_cast<double>(s) / std::max(n, 1);
+  }
+};
+
 // Warps per CTA and chunks per unit of the attention over own rows, by waves of CTAs on
 // the `resident` warps that the GPU holds at once.  In us: a CTA costs 5 for its start
 // and end, and per 16-row stage of a warp `step` when few run beside it and the stage's
@@ -130,8 +142,9 @@ int pick_chunks(int64_t items, int64_t sum, int64_t nmax, int64_t slots, int64_t
 // weights 5 in a launch of their own or 0.3 per 32 rows and warp at the unit's end.  Measured: 128 units of 32768
 // rows 401 / 324 / 402 / 334 us in 1 / 2 / 4 / 6 chunks (modelled 389 / 340 / 395 / 344),
 // 509 windows of 1028 rows 50 us with two warps and 59 with four (50 / 62).
-double pick_shape(int64_t items, int64_t sum, int64_t nmax, int64_t resident, double step,
-                  int64_t cap, bool weights, int* warps, int* chunks) {
+double pick_shape(const Sample& sample, int64_t items, int64_t sum, int64_t nmax,
+                  int64_t resident, double step, int64_t cap, bool weights, int* warps,
+                  int* chunks) {
   const double avg = std::max(1.0, static_cast<double>(sum) / static_cast<double>(items));
   const double share = resident * 8192.0 / 6.5e6;
   auto stage = [&](double part) { return std::max(step, share * part); };
@@ -141,10 +154,7 @@ double pick_shape(int64_t items, int64_t sum, int64_t nmax, int64_t resident, do
                                                std::max<int64_t>(1, nmax / w));
          c += c < 4 ? 1 : c / 4) {
       const int64_t gpc = (nmax + c - 1) / c;
-      // CTAs of an average unit: exact for equal lengths, else a half one more
-      const double per = c == 1 ? 1.0
-                         : avg > 0.99 * nmax ? static_cast<double>(c)
-                                             : std::max(1.0, avg / gpc + 0.5);
+      const double per = c == 1 ? 1.0 : sample.per(gpc);
       const double waves = static_cast<double>(items) * per * w / resident;
       const double full = std::floor(waves), rest = waves - full;
       const double mean = 2.0 * avg / per / w + 0.5;
@@ -165,17 +175,15 @@ double pick_shape(int64_t items, int64_t sum, int64_t nmax, int64_t resident, do
 
 // The same for the wide kernel over own rows (tiles of 128, one CTA per SM): 7 us per
 // CTA, per tile 0.95 or its share of HBM, and 4 for the kernel that joins the parts.
-double pick_wide(int64_t items, int64_t sum, int64_t nmax, int64_t slots, int64_t cap,
-                 int* chunks) {
+double pick_wide(const Sample& sample, int64_t items, int64_t sum, int64_t nmax, int64_t slots,
+                 int64_t cap, int* chunks) {
   const double avg = std::max(1.0, static_cast<double>(sum) / static_cast<double>(items));
   const double share = slots * 65536.0 / 6.5e6;
   auto tile = [&](double part) { return std::max(0.95, share * part); };
   double least = 1e300;
   for (int64_t c = 1; c <= std::min(std::max<int64_t>(1, cap), nmax); c += c < 4 ? 1 : c / 4) {
     const int64_t gpc = (nmax + c - 1) / c;
-    const double per = c == 1 ? 1.0
-                       : avg > 0.99 * nmax ? static_cast<double>(c)
-                                           : std::max(1.0, avg / gpc + 0.5);
+    const double per = c == 1 ? 1.0 : sample.per(gpc);
     const double waves = static_cast<double>(items) * per / slots;
     const double full = std::floor(waves), rest = waves - full;
     double cost = 4.0 + full * (avg / per * tile(1.0) + 7.0);
@@ -318,14 +326,17 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
 
   // the units' own rows
   int64_t gsum = 0, gmax = 1;
+  Sample sample;
+  const int step = (U + 31) / 32;
   for (int u = 0; u < U; ++u) {
     const int64_t n = b->tok_off_host[u + 1] - b->tok_off_host[u];
     const int64_t g = a->pos ? (n + 31) / 32 : reach(n, a->local, a->sinks, p.nq);
     gsum += g;
     gmax = std::max(gmax, g);
+    if (u % step == 0) sample.groups[sample.n++] = static_cast<int>(g);
   }
   int own = 1, warps = 4;
-  const double narrow = pick_shape(rg * static_cast<int64_t>(U), rg * gsum, gmax,
+  const double narrow = pick_shape(sample, rg * static_cast<int64_t>(U), rg * gsum, gmax,
                                    static_cast<int64_t>(attend_warps_per_sm(R)) * e->nsm,
                                    R <= 8 ? 0.75 : R <= 16 ? 1.0 : 2.5, cap / rows - (x ? 1 : 0),
                                    logits, &warps, &own);
@@ -380,14 +391,16 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
   if (!x && R > 8 && !a->keep && !a->pos && L.T > 0) {
     const int64_t blocks = (R + 255) / 256;
     int64_t tsum = 0, tmax = 1;
+    Sample tiles;
     for (int u = 0; u < U; ++u) {
       const int64_t n = b->tok_off_host[u + 1] - b->tok_off_host[u];
       const int64_t t = reach(n, a->local, a->sinks, p.nq, kWideTile);
       tsum += t;
       tmax = std::max(tmax, t);
+      if (u % step == 0) tiles.groups[tiles.n++] = static_cast<int>(t);
     }
     int c = 1;
-    const double cost = pick_wide(U * blocks, tsum * blocks, tmax, e->nsm, cap / rows, &c);
+    const double cost = pick_wide(tiles, U * blocks, tsum * blocks, tmax, e->nsm, cap / rows, &c);
     wide_own = cost < narrow && static_cast<int64_t>(c) * rows <= cap;
     if (wide_own) {
       p.PK = p.K;
@@ -420,10 +433,15 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     if (own > 1) {
       p.part_o = part_o;
       p.part_ml = part_ml;
-      p.count = count;
+      // up to 8 query rows are joined by the unit's last CTA, two per warp; 32 took it 16 us
+      if (R <= 8) p.count = count;
     }
     t_begin(e, RKV_KERNEL_ATTEND, st);
     err = launch_attend(p, U, warps, x != nullptr, st);
+    if (err == cudaSuccess && own > 1 && R > 8) {
+      err = launch_attend_finish(p, st);
+      ++e->launches;
+    }
     t_end(e, st);
     if (err != cudaSuccess) return cuda_fail(err);
     ++e->launches;

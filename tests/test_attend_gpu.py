@@ -10,9 +10,8 @@ Tolerances, elementwise, from the arithmetic:
 * out adds the accumulation of the p v (N terms in fp32: at most N 2^-23 of
   sum p |v|, in practice far less; a warp adds 16 per step) and one rounding to
   bf16, 2^-8 of the value at most;
-* where a prefix has more than 4 query rows, or a unit without mask and positions
-  more than 8, the tensor-memory kernel may run (by size): its p is one bf16, half a
-  step, 2^-8 of each p at most, on its share of sum p |v|, and its 2^x may come from a
+* where a prefix has more than 4 query rows, or a unit more than 8, p is one bf16, half
+  a step, 2^-8 of each p at most, on its share of sum p |v|, and 2^x may come from a
   polynomial that is off by 2.6e-6 < 2^-18 at most (numerator and denominator: 2^-17);
 * lse: dz + 2^-20 + 2^-22 |lse|;  acc: |p| times the factor above, and 2^-23 of
   the sum.
@@ -92,8 +91,7 @@ class Case:
         return self
 
     def wide(self):
-        return (self.prefixes is None and self.G * self.nq > 8 and self.keep is None
-                and self.pos is None)
+        return self.G * self.nq > 8
 
     def unit(self, u):
         """Oracle arguments of unit u (prefix rows first) and its prefix length."""
