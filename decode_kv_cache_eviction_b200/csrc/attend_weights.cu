@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(192, kBig ? 1 : 2)
               const int qp = s_qp[c0 + c];
               const int lo = p.local > 0 ? clamp32(static_cast<int64_t>(qp) - p.local) : INT_MIN;
               if (sees(ps, qp, lo, p.sinks)) w += x;
-            } else {
+            } else if (c0 + c < R) {   // a padded row's 0 x inf is not a weight
               w += x;
             }
           }

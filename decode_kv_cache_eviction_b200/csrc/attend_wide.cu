@@ -70,7 +70,9 @@ struct WideLayout {
 // the nearest whole number, added as 1.5 2^23 + n so that its low bits are n; a
 // polynomial of degree 4 for 2^f, |f| <= 1/2, fitted for the smallest largest
 // relative error, 2.6e-6 (2^-18.5: far below the rounding to bf16 that follows); n is
-// added to the exponent.  Smaller x give 2^-126; NaN is caught by the row's maximum.
+// added to the exponent.  x <= -126 (an unseen token) gives 2^-126, which is taken off
+// everywhere: the largest finite V times what is left is below 1e-5.  NaN is caught by
+// the row's maximum.
 __device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
   float x0, x1;
   unpair(x, x0, x1);
@@ -86,8 +88,9 @@ __device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
   float t0, t1, y0, y1;
   unpair(t, t0, t1);
   unpair(y, y0, y1);
-  return pair(__uint_as_float(__float_as_uint(y0) + (__float_as_uint(t0) << 23)),
-              __uint_as_float(__float_as_uint(y1) + (__float_as_uint(t1) << 23)));
+  return add_pair(pair(__uint_as_float(__float_as_uint(y0) + (__float_as_uint(t0) << 23)),
+                       __uint_as_float(__float_as_uint(y1) + (__float_as_uint(t1) << 23))),
+                  pair(-0x1p-126f, -0x1p-126f));
 }
 
 // Teardown: wait (bounded, regardless of an abort) for a phase that is under way.
@@ -478,7 +481,7 @@ __global__ void __launch_bounds__(64 + 256 * QT, 1)
       l[h] += a;
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      if (m[h] == -INFINITY) l[h] = 0.f;   // saw nothing (each unseen 2^x may be 2^-126)
+      if (m[h] == -INFINITY) l[h] = 0.f;   // saw nothing (an unseen 2^x may be off by 2^-145)
     }
     if (ok)   // the last step
       ok = mbar_wait(&o_done[QT == 2 ? t : ((nt - 1) & 1)], ((nt - 1) / kBuf) & 1, abort, p.status);

@@ -273,7 +273,7 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
   if (x) {
     rc = check_prefix(e, b, x, &psum, &plong, &members);
     if (rc != RKV_OK) return rc;
-    if (members == 0) x = nullptr;   // no unit has a prefix
+    if (members == 0 || psum == 0) x = nullptr;   // no unit has a prefix, or no rows in it
   }
   DeviceGuard dev(e->device);
   if (!dev.ok) return cuda_fail(cudaErrorUnknown);

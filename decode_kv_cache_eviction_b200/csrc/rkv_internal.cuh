@@ -281,9 +281,9 @@ cudaError_t launch_evict_in_place(const int64_t* tok_off, int U, int nmax, int W
                                   const int32_t* idx, const int32_t* n_kept, uint8_t* keep,
                                   int32_t* free_slots, int32_t* n_free, int* status, int nsm,
                                   cudaStream_t st);
-// What rkv_fill_slots_ex adds to rkv_fill_slots (all null without it): the
-// positions and zero weights of the filled slots, and other buffers for the
-// list that is left (null: in place).
+// What rkv_fill_slots_ex adds to rkv_fill_slots: the positions and zero weights of
+// the filled slots (null without it), and where the list that is left goes (the
+// input list itself: in place).
 struct FillExtra {
   const int32_t* pos_new;
   int32_t* pos;

@@ -303,3 +303,58 @@ def test_decode_loop():
             assert nf[u] == len(s["free"])
     eng.check_status()
     assert evictions >= 5
+
+
+def test_captured_decode_step():
+    """Fill, attend and evict captured together: replays give the bits of eager steps."""
+    G, w, cap, budget, U = 4, 4, 200, 90, 5
+    off, T = offsets([cap] * U), 5 * cap
+    one = Offsets(np.arange(U + 1), DEV)
+    ends = []
+    for captured in (False, True):
+        torch.manual_seed(3)
+        eng = Engine(G, w, U, T, redundancy="closed")
+        K, V = (torch.randn((T, 128), device=DEV).to(torch.bfloat16) for _ in range(2))
+        b = Batch(K, V, None, off)
+        keep = torch.ones(T, dtype=torch.uint8, device=DEV)
+        pos = torch.arange(cap, dtype=torch.int32, device=DEV).repeat(U)
+        acc, acc2 = torch.rand(T, device=DEV), torch.zeros(T, device=DEV)
+        free, nf = torch.full((T,), -1, dtype=torch.int32, device=DEV), torch.zeros(U, dtype=torch.int32, device=DEV)
+        free2, nf2 = torch.zeros_like(free), torch.zeros_like(nf)
+        kn, vn = (torch.zeros((U, 128), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        q = torch.zeros((U, G, 1, 128), dtype=torch.bfloat16, device=DEV)
+        at = torch.full((U,), cap, dtype=torch.int32, device=DEV)
+        out = torch.empty_like(q)
+
+        def step():
+            eng.evict_accumulated(b, acc, budget, keep, free, nf, live=keep, pos=pos, sinks=3, acc_out=acc2)
+            eng.fill_slots_ex(b, one, kn, vn, keep, free, nf, pos=pos, pos_new=at, acc=acc2,
+                              free_out=free2, n_free_out=nf2)
+            eng.attend(b, q, out, keep=keep, pos=pos, q_pos=at, acc=acc2, acc_out=acc)
+            at.add_(1)
+
+        step()                     # scratch is allocated outside the capture
+        if captured:
+            g = torch.cuda.CUDAGraph()
+            state = [t.clone() for t in (keep, pos, acc, acc2, free, nf, free2, nf2, at, K, V)]
+            with torch.cuda.graph(g):
+                step()
+            for t, x in zip((keep, pos, acc, acc2, free, nf, free2, nf2, at, K, V), state):
+                t.copy_(x)
+        log = []
+        for i in range(20):
+            torch.manual_seed(100 + i)
+            kn.copy_(torch.randn(U, 128, device=DEV))
+            vn.copy_(torch.randn(U, 128, device=DEV))
+            q.copy_(torch.randn(U, G, 1, 128, device=DEV))
+            if captured:
+                g.replay()
+            else:
+                step()
+            log.append([t.clone() for t in (out, keep, pos, acc, acc2, free, nf, free2, nf2)])
+        eng.check_status()
+        ends.append(log)
+    for x, y in zip(*ends):
+        for s, t in zip(x, y):
+            assert torch.equal(s, t)
+    assert int(ends[0][-1][6].sum()) > 0

@@ -218,6 +218,38 @@ def test_many_query_rows_and_values_that_are_not_finite():
     assert bool(c.out[1, :, 7].isnan().any()) and not bool(c.out[1, :, :7].isnan().any())
 
 
+def test_largest_finite_values_in_unseen_rows():
+    """An unseen row's weight is 0 for every V, the type's largest and lowest too: through
+    windows and causal masks of many query rows, and behind a prefix's end."""
+    big = float(torch.finfo(torch.bfloat16).max)
+    c = Case([1500, 1000], 4, 8, seed=63, local=200, sinks=2).run()
+    want = c.out.clone()
+    c.V[100:1000] = big                           # before every window of unit 0
+    c.V[1500 + 2:1500 + 790] = -big               # unit 1: between the sinks and the windows
+    c.run(c.eng)
+    assert torch.allclose(c.out.float(), want.float(), atol=1e-2)
+    c.check()
+    c = Case([10] * 20 + [300] * 20, 2, 1, seed=64, prefixes=[500, 300], unit_prefix=[0] * 40,
+             local=250).run()
+    want = c.out.clone()
+    c.PV[500:], c.PV[:200] = big, -big            # the next prefix, and rows nobody sees
+    c.PV[400] = big                               # seen by the short units alone
+    c.run(c.eng)
+    assert torch.allclose(c.out[20:].float(), want[20:].float(), atol=1e-2)
+
+
+@pytest.mark.parametrize("G,nq", [(4, 1), (2, 3), (4, 3)])
+def test_logits_of_minus_infinity_weigh_nothing(G, nq):
+    """A seen row whose logits are all -inf: its p is 0, in the sums and in the weights."""
+    c = Case([300, 40], G, nq, seed=65, weights=True)
+    c.Q.copy_(c.Q.abs().clamp_min(0.01))
+    c.K[20] = float("-inf")
+    c.run()
+    assert not bool(c.out.isnan().any()) and not bool(c.acc_out.isnan().any())
+    assert float(c.acc_out[20]) == float(c.acc[20])
+    c.check([1])
+
+
 def test_queries_that_stand_elsewhere():
     """q_pos without pos: queries behind the cache, inside it, and before it."""
     c = Case([300, 300, 300, 300], 4, 2, seed=8, local=50, sinks=3, weights=True)
@@ -304,6 +336,59 @@ def test_captured_call_replays_on_new_inputs():
     g.replay()
     torch.cuda.synchronize()
     c.check()
+
+
+@pytest.mark.parametrize("G,nq,shared", [(4, 3, False), (4, 8, False), (4, 1, True), (4, 4, True)])
+def test_captured_calls_of_one_engine(G, nq, shared):
+    """Two captures that share the engine's scratch, replayed in turn on new inputs; their
+    launches start early only where the one before is of the same call."""
+    kw = dict(weights=True, live=0.7)
+    if shared:
+        kw.update(prefixes=[700, 90], unit_prefix=[0, 1, 0, -1])
+    c = Case([2000, 300, 5, 64], G, nq, seed=66, **kw).run()
+    d = Case([70, 1000, 0, 900], G, nq, seed=67, **kw)
+    eng = Engine(G, nq, 4, 4000, redundancy="closed")
+    c.run(eng)
+    d.run(eng)
+    graphs = []
+    for x in (c, d):
+        b = Batch(x.K, x.V, None, x.off)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            a = dict(keep=x.keep, acc=x.acc, acc_out=x.acc_out)
+            if shared:
+                eng.attend_shared(b, x.prefix, x.Q, x.out, x.lse, **a)
+            else:
+                eng.attend(b, x.Q, x.out, x.lse, **a)
+        graphs.append((b, g))
+    for x in (c, d):
+        x.Q.copy_(torch.randn_like(x.Q))
+        x.acc.copy_(torch.rand_like(x.acc))
+    for _ in range(3):
+        for _, g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    c.check()
+    d.check()
+
+
+def test_two_engines_on_two_streams():
+    cases = [Case([3000, 100], 4, 2, seed=68, weights=True), Case([900, 4000], 4, 8, seed=69, weights=True)]
+    want = []
+    for c in cases:
+        c.run()
+        want.append((c.out.clone(), c.lse.clone(), c.acc_out.clone()))
+    streams = [torch.cuda.Stream() for _ in cases]
+    batches = [Batch(c.K, c.V, None, c.off) for c in cases]
+    for c in cases:
+        c.out.fill_(float("nan"))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, b, s in zip(cases, batches, streams):
+            c.eng.attend(b, c.Q, c.out, c.lse, acc=c.acc, acc_out=c.acc_out, stream=s)
+    torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        assert torch.equal(c.out, w[0]) and torch.equal(c.lse, w[1]) and torch.equal(c.acc_out, w[2])
 
 
 def test_first_call_inside_a_capture_is_refused():
@@ -424,6 +509,14 @@ def test_shared_call_without_any_prefix():
     c.check()
     d = Case([100, 33], 4, 1, seed=44, prefixes=[], unit_prefix=[-1, -1], weights=True).run()
     assert torch.equal(c.out, d.out)
+
+
+@pytest.mark.parametrize("units", [2, 40])
+def test_prefixes_without_rows(units):
+    up = [i % 2 for i in range(units)]
+    c = Case([100] * units, 4, 1, seed=47, prefixes=[0, 0], unit_prefix=up, weights=True).run()
+    c.check()
+    Case([30] * units, 4, 1, seed=48, prefixes=[0, 200], unit_prefix=up, weights=True).run().check()
 
 
 # ---------------------------------------------------------------- refusals
