@@ -10,8 +10,11 @@
 // sees are not read.
 //
 // Bound: HBM, 256 + 8 bytes per row (R = 32: a tile of 128 rows costs 256 cycles of 2^x
-// and 1400 of its share of HBM).  39 units of 2900 rows, R = 32: TIME us; on m16n8k16
-// steps, which spread a token's query rows over four lanes, 29.
+// and 1400 of its share of HBM); with few units the latency of a tile's chain (product,
+// tensor-memory load, 2^x, sums; hence four partial sums and no branch per row).  256
+// units of 2900 rows, R = 32: 33 us beyond the attention's time (30 at HBM's rate); 39 units:
+// 5 us, and 29 on m16n8k16 steps, which spread a token's query rows over four lanes.
+// 256 query rows over 16 units of 8000 rows: 26 us.
 #include "attend_common.cuh"
 
 namespace rkv {
@@ -69,7 +72,10 @@ __global__ void __launch_bounds__(192, kBig ? 1 : 2)
   const int first = prefix_len(p, item);
   const int tiles = (N + kTok - 1) / kTok;
   const int t_end = min(tiles, (chunk + 1) * p.gpc), t_begin = chunk * p.gpc;
-  if (t_begin >= t_end) return;
+  if (t_begin >= t_end) {
+    wait_for_previous_launch();
+    return;
+  }
   const int R = p.R, NQ = (R + 15) & ~15;   // query rows, and as the N side of the product
   const int64_t qmax = p.q_pos ? static_cast<int64_t>(__ldg(&p.q_pos[item]))
                                : static_cast<int64_t>(first) + N - 1;
@@ -115,11 +121,7 @@ __global__ void __launch_bounds__(192, kBig ? 1 : 2)
     *reinterpret_cast<uint4*>(sm + Lay::q + (c >> 3) * NQ * 128 + r * 128 +
                               (((c & 7) ^ (r & 7)) << 4)) = v;
   }
-  for (int r = tid; r < NQ; r += 192) {
-    s_qp[r] = r < R ? clamp32(qmin + r % p.nq) : INT_MIN;
-    // a padded row weighs nothing
-    s_lse[r] = r < R ? __ldg(&p.lse2[static_cast<int64_t>(item) * R + r]) : INFINITY;
-  }
+  for (int r = tid; r < NQ; r += 192) s_qp[r] = r < R ? clamp32(qmin + r % p.nq) : INT_MIN;
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
@@ -186,6 +188,12 @@ __global__ void __launch_bounds__(192, kBig ? 1 : 2)
     const uint32_t lanes = static_cast<uint32_t>(32 * w4) << 16;
     int n = 0;
     bool ok = true;
+    // the log-sums: this launch may have started while they were computed
+    wait_for_previous_launch();
+    for (int r = tid - 64; r < NQ; r += 128)
+      s_lse[r] = r < R ? __ldcg(&p.lse2[static_cast<int64_t>(item) * R + r]) : INFINITY;
+    __syncwarp();
+    named_bar_sync(1, 128);
     for (int t = t_begin; ok && t < t_end; ++t) {
       const int i = t * kTok + 32 * w4 + lane;
       const bool in = i < N;
@@ -193,39 +201,51 @@ __global__ void __launch_bounds__(192, kBig ? 1 : 2)
       float sum = in && p.acc_in ? p.acc_in[at] : 0.f;
       if (needed(t)) {
         int ps = first + i;
-        bool on = in;
-        if (in && p.keep) on = __ldg(&p.keep[at]) != 0;
+        uint32_t live = 1u;
+        if (in && p.keep) live = __ldg(&p.keep[at]);
         if (in && p.pos) ps = __ldg(&p.pos[at]);
-        // seen by every query, by none, or by some
-        const bool all = on && sees(ps, qmin32, lo_all, p.sinks);
-        on = on && sees(ps, qmax32, lo_any, p.sinks);
         const int b = n & 1;
         ok = mbar_wait(&d_full[b], (n >> 1) & 1, abort, p.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const bool masked = __any_sync(0xffffffffu, on && !all);
-        float w = 0.f;
-        for (int c0 = 0; c0 < NQ; c0 += 16) {
-          uint32_t z[16];
-          tmem_ld16(tmem + lanes + b * NQ + c0, z);
-          tmem_wait_ld_dep(z);
+        // seen by every query, by none, or by some
+        const bool on = in && live != 0u && sees(ps, qmax32, lo_any, p.sinks);
+        const bool masked = __any_sync(0xffffffffu, on && !sees(ps, qmin32, lo_all, p.sinks));
+        const uint32_t from = tmem + lanes + b * NQ;
+        float w[4] = {0.f, 0.f, 0.f, 0.f};
+        // adds 16 query rows' weights; some: not every one sees the token
+        auto add = [&](const uint32_t (&z)[16], int c0, bool some) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const float x = ex2(fmaf(__uint_as_float(z[c]), p.scale_log2, -s_lse[c0 + c]));
-            if (masked) {
-              const int qp = s_qp[c0 + c];
-              const int lo = p.local > 0 ? clamp32(static_cast<int64_t>(qp) - p.local) : INT_MIN;
-              if (sees(ps, qp, lo, p.sinks)) w += x;
-            } else if (c0 + c < R) {   // a padded row's 0 x inf is not a weight
-              w += x;
+          for (int c = 0; c < 16; c += 4) {
+            const float4 ls = *reinterpret_cast<const float4*>(s_lse + c0 + c);
+            const float l[4] = {ls.x, ls.y, ls.z, ls.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float x = ex2(fmaf(__uint_as_float(z[c + k]), p.scale_log2, -l[k]));
+              if (some) {   // not seen, or a padded row (0 x inf is not a weight)
+                const int qp = s_qp[c0 + c + k];
+                const int lo = p.local > 0 ? clamp32(static_cast<int64_t>(qp) - p.local) : INT_MIN;
+                if (!(c0 + c + k < R && sees(ps, qp, lo, p.sinks))) x = 0.f;
+              }
+              w[k] += x;
             }
           }
+        };
+        uint32_t z[16];
+        // blocks whose 16 rows all see the warp's tokens, then the others
+        const int whole = masked ? 0 : R & ~15;
+        for (int c0 = 0; c0 < NQ; c0 += 16) {
+          tmem_ld16(from + c0, z);
+          tmem_wait_ld_dep(z);
+          if (c0 < whole) add(z, c0, false);
+          else add(z, c0, true);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&d_empty[b]);
-        if (on) sum += w;   // what lies in a dead row is dropped with its sum
+        // what lies in a dead row is dropped with its sum
+        if (on) sum += (w[0] + w[1]) + (w[2] + w[3]);
         ++n;
       }
       if (in) p.acc_out[at] = sum;
@@ -257,12 +277,19 @@ int tile_weights_ctas_per_sm(int R) { return R <= 64 ? 2 : 1; }
 
 cudaError_t launch_tile_weights(const CUtensorMap& kmap, const AttendParams& p, int U,
                                 cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>(U) * p.maxch;
-  if (p.R <= 64)
-    tile_weights_kernel<false><<<grid, 192, WLayout<false>::alloc, st>>>(kmap, p);
-  else
-    tile_weights_kernel<true><<<grid, 192, WLayout<true>::alloc, st>>>(kmap, p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(U) * p.maxch);
+  cfg.blockDim = dim3(192);
+  cfg.dynamicSmemBytes = p.R <= 64 ? WLayout<false>::alloc : WLayout<true>::alloc;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];   // starts while the sums are still being joined
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = p.R <= 64 ? cudaLaunchKernelEx(&cfg, tile_weights_kernel<false>, kmap, p)
+                                  : cudaLaunchKernelEx(&cfg, tile_weights_kernel<true>, kmap, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace rkv
