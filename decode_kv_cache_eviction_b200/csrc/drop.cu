@@ -357,94 +357,80 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
     }
   }
 
-  // bits of a vector's rows: kept, or equal to the threshold
-  auto kept4 = [&](int v) -> uint32_t {
-    const uint4 k = keys[v];
-    auto one = [&](uint32_t x, int c) {
-      return (x > thr || (x == thr && 4 * v + c <= cut) ? 1u : 0u) << c;
-    };
-    return one(k.x, 0) | one(k.y, 1) | one(k.z, 2) | one(k.w, 3);
-  };
-  auto tied4 = [&](int v) -> uint32_t {
-    const uint4 k = keys[v];
-    return (k.x == thr ? 1u : 0u) | (k.y == thr ? 2u : 0u) | (k.z == thr ? 4u : 0u) |
-           (k.w == thr ? 8u : 0u);
-  };
-  // Of one bit per row: the number set in lower lanes' elements of a round, and in
-  // cnt[round kWarps + warp] (after scan) the number set in warps before.
-  auto lower = [&](uint32_t b) {
-    int k = 0;
+  // Bits of every vector's rows that stay (g), and of those equal to a threshold that not
+  // all of them pass (e), with the numbers set in lower lanes' vectors of the round, over
+  // its keys: g | e << 4 | lower g << 8 | lower e << 16.  cnt[round kWarps + warp] gets the
+  // numbers set in this CTA before that warp and round, g | e << 16.
+  __syncthreads();
+  for (int r = 0; r < nr; ++r) {
+    const int v = r * T + tid;
+    uint32_t g = 0u, e = 0u, lg = 0u, le = 0u;
+    if (v < nv) {
+      const uint4 k = keys[v];
+      auto one = [&](uint32_t x, int c) {
+        if (x > thr || (x == thr && 4 * v + c <= cut)) g |= 1u << c;
+        else if (some_ties && x == thr) e |= 1u << c;
+      };
+      one(k.x, 0);
+      one(k.y, 1);
+      one(k.z, 2);
+      one(k.w, 3);
+    }
 #pragma unroll
-    for (int c = 0; c < 4; ++c) k += __popc(__ballot_sync(0xffffffffu, (b >> c) & 1u) & below);
-    return k;
-  };
-  auto scan = [&](auto bits, uint32_t& total) {
-    __syncthreads();
-    for (int r = 0; r < nr; ++r) {
-      const int v = r * T + tid;
-      const uint32_t k =
-          __reduce_add_sync(0xffffffffu, v < nv ? static_cast<uint32_t>(__popc(bits(v))) : 0u);
-      if (lane == 0) cnt[r * kWarps + wp] = k;
-    }
-    __syncthreads();
-    const int used = nr * kWarps;
-    if (wp == 0) {
-      uint32_t carry = 0;
-      for (int k0 = 0; k0 < used; k0 += 32) {
-        const uint32_t x = k0 + lane < used ? cnt[k0 + lane] : 0u;
-        uint32_t y = x;
+    for (int c = 0; c < 4; ++c) lg += __popc(__ballot_sync(0xffffffffu, (g >> c) & 1u) & below);
+    if (some_ties) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t z = __shfl_up_sync(0xffffffffu, y, o);
-          if (lane >= o) y += z;
-        }
-        if (k0 + lane < used) cnt[k0 + lane] = carry + y - x;
-        carry += __shfl_sync(0xffffffffu, y, 31);
-      }
-      if (lane == 0) cnt[used] = carry;
+      for (int c = 0; c < 4; ++c) le += __popc(__ballot_sync(0xffffffffu, (e >> c) & 1u) & below);
     }
-    __syncthreads();
-    total = cnt[used];
-  };
-  // the CTAs' totals: over the cluster, and of the CTAs before this one
-  auto across = [&](uint32_t mine, uint32_t& total, uint32_t& before) {
-    total = mine;
-    before = 0;
-    if (cs > 1) {
-      uint32_t a[1] = {wp == 0 ? mine : 0u}, b[1];
-      ex.all(a, b, [](int, uint32_t x, uint32_t y) { return x + y; });
-      total = a[0];
-      before = b[0];
-    }
-  };
-  uint32_t total, all, before;
-  if (some_ties) {
-    // the first `ties` of the equal rows become unranked ones that stay
-    scan(tied4, total);
-    across(total, all, before);
-    for (int r = 0; r < nr; ++r) {
-      const int v = r * T + tid;
-      const uint32_t b = v < nv ? tied4(v) : 0u;
-      uint32_t at = before + cnt[r * kWarps + wp] + lower(b);
-      uint32_t* k = reinterpret_cast<uint32_t*>(keys + v);
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if ((b >> c) & 1u) {
-          if (at < ties) k[c] = kSafe;
-          ++at;
-        }
-    }
+    if (v < nv) keys[v].x = g | e << 4 | lg << 8 | le << 16;
+    if (lane == 31) cnt[r * kWarps + wp] = (lg + __popc(g)) | (le + __popc(e)) << 16;
   }
-  scan(kept4, total);
-  across(total, all, before);
+  __syncthreads();
+  const int used = nr * kWarps;
+  if (wp == 0) {
+    uint32_t carry = 0;
+    for (int k0 = 0; k0 < used; k0 += 32) {
+      const uint32_t x = k0 + lane < used ? cnt[k0 + lane] : 0u;
+      uint32_t y = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
+      }
+      if (k0 + lane < used) cnt[k0 + lane] = carry + y - x;
+      carry += __shfl_sync(0xffffffffu, y, 31);
+    }
+    if (lane == 0) cnt[used] = carry;
+  }
+  __syncthreads();
+  // the numbers of both in the unit, and in the CTAs before this one
+  uint32_t all[2] = {cnt[used] & 0xffffu, cnt[used] >> 16}, before[2] = {0u, 0u};
+  if (cs > 1) {
+    if (wp > 0) all[0] = all[1] = 0u;
+    ex.all(all, before, [](int, uint32_t x, uint32_t y) { return x + y; });
+  }
+  const int nk = static_cast<int>(all[0] + min(all[1], ties));   // rows that stay
   int32_t* idx = p.idx ? p.idx + static_cast<int64_t>(u) * p.W : nullptr;
   int32_t* fs = p.free_slots + base;
 #pragma unroll 2
   for (int r = 0; r < nr; ++r) {
     const int v = r * T + tid;
-    const uint32_t k = v < nv ? kept4(v) : 0u;
-    int at = static_cast<int>(before + cnt[r * kWarps + wp]) + lower(k);
     if (v >= nv) continue;
+    // a row's place among those that stay: the ones before it in g, and of those in e the
+    // unit's first `ties`
+    const uint32_t x = keys[v].x, first = cnt[r * kWarps + wp];
+    uint32_t k = x & 15u;
+    int at = static_cast<int>(before[0] + (first & 0xffffu) + ((x >> 8) & 255u));
+    if (some_ties) {
+      uint32_t ae = before[1] + (first >> 16) + (x >> 16);
+      at += min(ae, ties);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if ((x >> (4 + c)) & 1u) {
+          if (ae < ties) k |= 1u << c;
+          ++ae;
+        }
+    }
     const int64_t g = at0 + 4 * v;
     const bool full = whole(v);
     const int row0 = lo - skew + 4 * v;
@@ -476,7 +462,6 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
       }
   }
   // what is left of the list and of idx
-  const int nk = static_cast<int>(all);
   for (int i = N - nk + rank * T + tid; i < N; i += cs * T) fs[i] = -1;
   if (idx)
     for (int i = nk + rank * T + tid; i < p.W; i += cs * T) idx[i] = -1;
