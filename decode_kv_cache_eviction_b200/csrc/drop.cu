@@ -26,10 +26,12 @@ namespace {
 
 // Order-preserving key of a weight, at least 1: -0 and +0 alike, NaN below
 // every number.  0 marks a row that is not ranked.
-__device__ __forceinline__ uint32_t weight_key(float s) {
+__device__ __forceinline__ uint32_t number_key(float s) {
   const uint32_t b = __float_as_uint(__fadd_rn(s, 0.f));
-  const uint32_t k = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-  return s == s ? k : 1u;   // -inf has key 0x007fffff
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ uint32_t weight_key(float s) {
+  return s == s ? number_key(s) : 1u;   // -inf has key 0x007fffff
 }
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -59,9 +61,8 @@ struct DropShared {
   uint32_t total[2][4];          // this CTA's
   uint32_t wsum[T / 32];
   uint32_t found[3];             // bin, its rows, rows wanted of it
-  uint2 list[kList];             // keys and rows of a small bin
+  uint32_t list[kList];          // keys of a small bin
   uint32_t listed;
-  uint2 last;                    // the last of them that stays
 };
 
 // Exchanges of up to 4 values over the CTA and the cluster.
@@ -116,7 +117,6 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
   extern __shared__ uint4 keys[];           // [nv] vectors of four rows, then the places
   __shared__ DropShared<T> sh;
   const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
-  const unsigned below = (1u << lane) - 1u;
   const int rank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int u = blockIdx.x / cs;
   const int64_t base = p.tok_off[u];
@@ -185,35 +185,45 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
     newest = static_cast<int>(m[0] ^ 0x80000000u);
   }
   const int recent = newest < INT_MIN + p.w ? INT_MIN : newest - p.w;   // positions above stay
-  uint32_t kmax = 0u, kinv = 0u, count = 0u;   // kinv: complement of the smallest key
+  uint32_t kmax = 0u, kmin = 0xffffffffu, count = 0u;
 #pragma unroll 4
   for (int v = tid; v < nv; v += T) {
     const float4 a = acc4(v);
     const uint32_t l = live4(v);
     const int4 y = pos4(v);
-    auto one = [&](float w, int x, int c) -> uint32_t {
-      if (!((l >> (8 * c)) & 0xffu)) return 0u;
-      if (x < p.sinks || x > recent) return kSafe;
-      const uint32_t k = weight_key(w);
-      kmax = max(kmax, k);
-      kinv = max(kinv, ~k);
-      ++count;
-      return k;
-    };
-    keys[v] = make_uint4(one(a.x, y.x, 0), one(a.y, y.y, 1), one(a.z, y.z, 2), one(a.w, y.w, 3));
+    const float sum = (a.x + a.y) + (a.z + a.w);
+    uint4 k;
+    if (l == 0x01010101u && sum == sum && min(min(y.x, y.y), min(y.z, y.w)) >= p.sinks &&
+        max(max(y.x, y.y), max(y.z, y.w)) <= recent) {
+      // four ranked rows, and no NaN among them
+      k = make_uint4(number_key(a.x), number_key(a.y), number_key(a.z), number_key(a.w));
+      kmax = max(kmax, max(max(k.x, k.y), max(k.z, k.w)));
+      kmin = min(kmin, min(min(k.x, k.y), min(k.z, k.w)));
+      count += 4u;
+    } else {
+      auto one = [&](float w, int x, int c) -> uint32_t {
+        if (!((l >> (8 * c)) & 0xffu)) return 0u;
+        if (x < p.sinks || x > recent) return kSafe;
+        const uint32_t q = weight_key(w);
+        kmax = max(kmax, q);
+        kmin = min(kmin, q);
+        ++count;
+        return q;
+      };
+      k = make_uint4(one(a.x, y.x, 0), one(a.y, y.y, 1), one(a.z, y.z, 2), one(a.w, y.w, 3));
+    }
+    keys[v] = k;
   }
-  uint32_t m[3] = {__reduce_max_sync(0xffffffffu, kmax), __reduce_max_sync(0xffffffffu, kinv),
-                   __reduce_add_sync(0xffffffffu, count)};
+  uint32_t m[3] = {__reduce_max_sync(0xffffffffu, kmax), ~__reduce_min_sync(0xffffffffu, kmin),
+                   __reduce_add_sync(0xffffffffu, count)};   // the smallest key's complement
   uint32_t bm[3];
   ex.all(m, bm, [](int k, uint32_t a, uint32_t x) { return k == 2 ? a + x : a > x ? a : x; });
   const uint32_t ranked = m[2];
   int budget = p.budget;
   if (p.budgets) budget = min(max(p.budgets[u], 0), p.budget);
 
-  // rows with key > thr stay, and of those with key = thr the rows of the run up to
-  // `cut`, or (some_ties) the unit's first `ties`
+  // rows with key > thr stay, and (some_ties) of those with key = thr the unit's first `ties`
   uint32_t thr = 0u, ties = 0u;
-  int cut = INT_MIN;
   bool some_ties = false;
   if (budget == 0) {
     thr = kSafe - 1u;
@@ -303,29 +313,34 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
         // few rows left: each one's rank by comparing it with the others
         for (int v = tid; v < nv; v += T) {
           const uint4 k = keys[v];
-          auto put = [&](uint32_t x, int c) {
-            if (x - low <= span)
-              sh.list[atomicAdd(&sh.listed, 1u)] = make_uint2(x, static_cast<uint32_t>(4 * v + c));
+          auto put = [&](uint32_t x) {
+            if (x - low <= span) sh.list[atomicAdd(&sh.listed, 1u)] = x;
           };
-          put(k.x, 0);
-          put(k.y, 1);
-          put(k.z, 2);
-          put(k.w, 3);
+          put(k.x);
+          put(k.y);
+          put(k.z);
+          put(k.w);
         }
         __syncthreads();
         if (tid < static_cast<int>(in_bin)) {
-          const uint2 own = sh.list[tid];
-          uint32_t above_own = 0;
+          const uint32_t own = sh.list[tid];
+          uint32_t above_own = 0, same = 0;
           for (uint32_t k = 0; k < in_bin; ++k) {
-            const uint2 x = sh.list[k];
-            above_own += x.x > own.x || (x.x == own.x && x.y < own.y) ? 1u : 0u;
+            const uint32_t x = sh.list[k];
+            above_own += x > own ? 1u : 0u;
+            same += x == own ? 1u : 0u;
           }
-          if (above_own == want - 1u) sh.last = own;
+          if (above_own < want && want <= above_own + same) {   // rows of one key
+            sh.found[0] = own;
+            sh.found[1] = same;
+            sh.found[2] = want - above_own;
+          }
         }
         __syncthreads();
-        thr = sh.last.x;
-        cut = static_cast<int>(sh.last.y);
-        some_ties = false;
+        thr = low = sh.found[0];
+        want = sh.found[2];
+        some_ties = want != sh.found[1];
+        if (!some_ties) --thr;
         break;
       }
       if (in_bin * 16u > ranked) {
@@ -359,31 +374,29 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
 
   // Bits of every vector's rows that stay (g), and of those equal to a threshold that not
   // all of them pass (e), with the numbers set in lower lanes' vectors of the round, over
-  // its keys: g | e << 4 | lower g << 8 | lower e << 16.  cnt[round kWarps + warp] gets the
+  // its keys: g | e << 4 | lower g << 8 | lower e << 24.  cnt[round kWarps + warp] gets the
   // numbers set in this CTA before that warp and round, g | e << 16.
   __syncthreads();
   for (int r = 0; r < nr; ++r) {
     const int v = r * T + tid;
-    uint32_t g = 0u, e = 0u, lg = 0u, le = 0u;
+    uint32_t g = 0u, e = 0u;
     if (v < nv) {
       const uint4 k = keys[v];
-      auto one = [&](uint32_t x, int c) {
-        if (x > thr || (x == thr && 4 * v + c <= cut)) g |= 1u << c;
-        else if (some_ties && x == thr) e |= 1u << c;
-      };
-      one(k.x, 0);
-      one(k.y, 1);
-      one(k.z, 2);
-      one(k.w, 3);
+      g = (k.x > thr ? 1u : 0u) | (k.y > thr ? 2u : 0u) | (k.z > thr ? 4u : 0u) |
+          (k.w > thr ? 8u : 0u);
+      if (some_ties)
+        e = (k.x == thr ? 1u : 0u) | (k.y == thr ? 2u : 0u) | (k.z == thr ? 4u : 0u) |
+            (k.w == thr ? 8u : 0u);
     }
+    const uint32_t own = __popc(g) | __popc(e) << 16;
+    uint32_t incl = own;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) lg += __popc(__ballot_sync(0xffffffffu, (g >> c) & 1u) & below);
-    if (some_ties) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) le += __popc(__ballot_sync(0xffffffffu, (e >> c) & 1u) & below);
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
     }
-    if (v < nv) keys[v].x = g | e << 4 | lg << 8 | le << 16;
-    if (lane == 31) cnt[r * kWarps + wp] = (lg + __popc(g)) | (le + __popc(e)) << 16;
+    if (v < nv) keys[v].x = g | e << 4 | (incl - own) << 8;
+    if (lane == 31) cnt[r * kWarps + wp] = incl;
   }
   __syncthreads();
   const int used = nr * kWarps;
@@ -422,7 +435,7 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
     uint32_t k = x & 15u;
     int at = static_cast<int>(before[0] + (first & 0xffffu) + ((x >> 8) & 255u));
     if (some_ties) {
-      uint32_t ae = before[1] + (first >> 16) + (x >> 16);
+      uint32_t ae = before[1] + (first >> 16) + (x >> 24);
       at += min(ae, ties);
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -439,9 +452,7 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
     const float4 o = make_float4(k & 1u ? a.x : 0.f, k & 2u ? a.y : 0.f, k & 4u ? a.z : 0.f,
                                  k & 8u ? a.w : 0.f);
     if (full) {
-      // bits 0..3 to bytes
-      *reinterpret_cast<uint32_t*>(p.keep + g) =
-          (k & 1u) | (k & 2u) << 7 | (k & 4u) << 14 | (k & 8u) << 21;
+      *reinterpret_cast<uint32_t*>(p.keep + g) = (k * 0x00204081u) & 0x01010101u;   // bits to bytes
       if (p.acc_out) *reinterpret_cast<float4*>(p.acc_out + g) = o;
     } else {
       const float w[4] = {o.x, o.y, o.z, o.w};
@@ -452,14 +463,26 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
           if (p.acc_out) p.acc_out[g + c] = w[c];
         }
     }
+    uint32_t gone = ~k & 15u;
+    if (!full)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (!inside(v, c)) gone &= ~(1u << c);
+    // a free row's place is its row less the rows before it that stay; outside rows (of the
+    // first vector) lie before them
+    const int out = !full && skew > 4 * v ? skew - 4 * v : 0;
+    int32_t* f = fs + (row0 + out - at);
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-      if (full || inside(v, c)) {
-        const bool stays = (k >> c) & 1u;
-        if (!stays) fs[row0 + c - at] = row0 + c;
-        else if (idx && at < p.W) idx[at] = row0 + c;
-        at += stays ? 1 : 0;
-      }
+      if ((gone >> c) & 1u) *f++ = row0 + c;
+    if (idx) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if ((k >> c) & 1u) {
+          if (at < p.W) idx[at] = row0 + c;
+          ++at;
+        }
+    }
   }
   // what is left of the list and of idx
   for (int i = N - nk + rank * T + tid; i < N; i += cs * T) fs[i] = -1;
