@@ -167,56 +167,71 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
     return make_float4(x[0], x[1], x[2], x[3]);
   };
 
-  // the newest live position
-  int newest = N - 1;
-  if (kPos || p.live) {
-    int x = INT_MIN;
+  // Keys of this thread's rows and what they say: the largest, the smallest, the smallest
+  // above that of 0 (less it), their number, and the newest live position.
+  constexpr uint32_t kZero = 0x80000000u;   // the key of 0
+  uint32_t kmax, kmin, kpos, count;
+  int newest;
+  auto rank_rows = [&](int recent) {
+    kmax = count = 0u;
+    kmin = kpos = 0xffffffffu;
+    newest = INT_MIN;
+    auto see = [&](uint32_t q) {
+      kmax = max(kmax, q);
+      kmin = min(kmin, q);
+      kpos = min(kpos, q - (kZero + 1u));   // large below it, too
+    };
 #pragma unroll 4
     for (int v = tid; v < nv; v += T) {
+      const float4 a = acc4(v);
       const uint32_t l = live4(v);
       const int4 y = pos4(v);
-      if (l & 0xffu) x = max(x, y.x);
-      if (l & 0xff00u) x = max(x, y.y);
-      if (l & 0xff0000u) x = max(x, y.z);
-      if (l & 0xff000000u) x = max(x, y.w);
+      const float sum = (a.x + a.y) + (a.z + a.w);
+      const int high = max(max(y.x, y.y), max(y.z, y.w));
+      uint4 k;
+      if (l == 0x01010101u && sum == sum && min(min(y.x, y.y), min(y.z, y.w)) >= p.sinks &&
+          high <= recent) {
+        // four ranked rows, and no NaN among them
+        k = make_uint4(number_key(a.x), number_key(a.y), number_key(a.z), number_key(a.w));
+        see(k.x);
+        see(k.y);
+        see(k.z);
+        see(k.w);
+        count += 4u;
+        newest = max(newest, high);
+      } else {
+        auto one = [&](float w, int x, int c) -> uint32_t {
+          if (!((l >> (8 * c)) & 0xffu)) return 0u;
+          newest = max(newest, x);
+          if (x < p.sinks || x > recent) return kSafe;
+          const uint32_t q = weight_key(w);
+          see(q);
+          ++count;
+          return q;
+        };
+        k = make_uint4(one(a.x, y.x, 0), one(a.y, y.y, 1), one(a.z, y.z, 2), one(a.w, y.w, 3));
+      }
+      keys[v] = k;
     }
-    uint32_t m[1] = {static_cast<uint32_t>(__reduce_max_sync(0xffffffffu, x)) ^ 0x80000000u}, b[1];
+  };
+  auto window = [&](int x) { return x < INT_MIN + p.w ? INT_MIN : x - p.w; };   // above: stay
+  if (kPos || p.live) {
+    // the newest live position comes out of the same pass; threads that have rows of the
+    // window then go over theirs again
+    rank_rows(INT_MAX);
+    uint32_t m[1] = {static_cast<uint32_t>(__reduce_max_sync(0xffffffffu, newest)) ^ 0x80000000u};
+    uint32_t b[1];
     ex.all(m, b, [](int, uint32_t a, uint32_t x) { return a > x ? a : x; });
-    newest = static_cast<int>(m[0] ^ 0x80000000u);
+    const int recent = window(static_cast<int>(m[0] ^ 0x80000000u));
+    if (newest > recent) rank_rows(recent);
+    __syncwarp();
+  } else {
+    rank_rows(window(N - 1));
   }
-  const int recent = newest < INT_MIN + p.w ? INT_MIN : newest - p.w;   // positions above stay
-  uint32_t kmax = 0u, kmin = 0xffffffffu, count = 0u;
-#pragma unroll 4
-  for (int v = tid; v < nv; v += T) {
-    const float4 a = acc4(v);
-    const uint32_t l = live4(v);
-    const int4 y = pos4(v);
-    const float sum = (a.x + a.y) + (a.z + a.w);
-    uint4 k;
-    if (l == 0x01010101u && sum == sum && min(min(y.x, y.y), min(y.z, y.w)) >= p.sinks &&
-        max(max(y.x, y.y), max(y.z, y.w)) <= recent) {
-      // four ranked rows, and no NaN among them
-      k = make_uint4(number_key(a.x), number_key(a.y), number_key(a.z), number_key(a.w));
-      kmax = max(kmax, max(max(k.x, k.y), max(k.z, k.w)));
-      kmin = min(kmin, min(min(k.x, k.y), min(k.z, k.w)));
-      count += 4u;
-    } else {
-      auto one = [&](float w, int x, int c) -> uint32_t {
-        if (!((l >> (8 * c)) & 0xffu)) return 0u;
-        if (x < p.sinks || x > recent) return kSafe;
-        const uint32_t q = weight_key(w);
-        kmax = max(kmax, q);
-        kmin = min(kmin, q);
-        ++count;
-        return q;
-      };
-      k = make_uint4(one(a.x, y.x, 0), one(a.y, y.y, 1), one(a.z, y.z, 2), one(a.w, y.w, 3));
-    }
-    keys[v] = k;
-  }
-  uint32_t m[3] = {__reduce_max_sync(0xffffffffu, kmax), ~__reduce_min_sync(0xffffffffu, kmin),
-                   __reduce_add_sync(0xffffffffu, count)};   // the smallest key's complement
-  uint32_t bm[3];
+  // smallest keys as their complements
+  uint32_t m[4] = {__reduce_max_sync(0xffffffffu, kmax), ~__reduce_min_sync(0xffffffffu, kmin),
+                   __reduce_add_sync(0xffffffffu, count), ~__reduce_min_sync(0xffffffffu, kpos)};
+  uint32_t bm[4];
   ex.all(m, bm, [](int k, uint32_t a, uint32_t x) { return k == 2 ? a + x : a > x ? a : x; });
   const uint32_t ranked = m[2];
   int budget = p.budget;
@@ -229,8 +244,13 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
     thr = kSafe - 1u;
   } else if (ranked > static_cast<uint32_t>(budget)) {
     uint32_t want = budget;
-    const uint32_t high = m[0];
+    uint32_t high = m[0];
     uint32_t low = ~m[1];              // the keys that are left: low .. low + span
+    // Rows of weight 0 (new tokens) would stretch the range over all exponents and crowd
+    // the others into few bins: first the keys above that of 0.
+    const uint32_t above_zero = ~m[3] + kZero + 1u;
+    bool rest = low <= kZero && above_zero > kZero && above_zero < high;
+    if (rest) low = above_zero;
     uint32_t span = high - low;
     some_ties = true;
     for (int round = 0; span > 0u; ++round) {
@@ -286,6 +306,17 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
 #pragma unroll
       for (int w = 0; w < 3; ++w)
         if (w < wp) incl += sh.wsum[w];   // bins lie in the first four warps
+      if (rest) {
+        rest = false;
+        const uint32_t total = sh.wsum[0] + sh.wsum[1] + sh.wsum[2] + sh.wsum[3];
+        if (total < want) {   // the last to stay is not among them
+          want -= total;
+          low = ~m[1];
+          high = kZero;
+          span = high - low;
+          continue;
+        }
+      }
       uint32_t above = incl - mine;
       if (wp < 4 && above < want && want <= incl) {   // one thread
 #pragma unroll
