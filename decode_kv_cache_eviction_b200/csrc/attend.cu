@@ -344,8 +344,8 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
   int64_t qmin, qmax;
   if (kMode == kPrefix) {
     if (tid < 32) {
-      int v = INT_MIN;
-      if (tid < nrow) {
+      int v = sees_whole_prefix(p) ? INT_MAX : INT_MIN;
+      if (tid < nrow && !sees_whole_prefix(p)) {
         const int64_t rr = row_of(tid);
         const int u = static_cast<int>(rr / p.R);
         const int t = static_cast<int>(rr - static_cast<int64_t>(u) * p.R) % p.nq;
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
     qmin = lo;
     qmax = hi;
   } else {
-    first = prefix_len(p, item);
+    first = own_first(p, item);
     qmax = p.q_pos ? static_cast<int64_t>(__ldg(&p.q_pos[item])) : static_cast<int64_t>(first) + N - 1;
     qmin = qmax - (p.nq - 1);
     if (!kOne) {
@@ -775,10 +775,13 @@ __global__ void __launch_bounds__(256) weights_kernel(const __grid_constant__ At
   const int item = blockIdx.x / p.maxch, chunk = blockIdx.x - item * p.maxch;
   const int64_t base = __ldg(&p.tok_off[item]);
   const int N = static_cast<int>(__ldg(&p.tok_off[item + 1]) - base);
+  const int first = own_first(p, item);
+  const int64_t qpos = p.q_pos ? static_cast<int64_t>(__ldg(&p.q_pos[item]))
+                               : static_cast<int64_t>(first) + N - 1;
   const int64_t i0 = static_cast<int64_t>(chunk) * p.gpc * 32;
   wait_for_previous_launch();
   if (i0 >= N) return;
-  weights_any<4>(p, base, prefix_len(p, item), newest_query(p, item),
+  weights_any<4>(p, base, first, qpos,
               p.lse2 + static_cast<int64_t>(item) * p.R, static_cast<int>(i0),
               static_cast<int>(min(static_cast<int64_t>(N), i0 + static_cast<int64_t>(p.gpc) * 32)));
 }

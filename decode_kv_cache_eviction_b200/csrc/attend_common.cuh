@@ -25,6 +25,16 @@ __device__ __forceinline__ int prefix_len(const AttendParams& p, int u) {
   const int x = __ldg(&p.unit_prefix[u]);
   return x < 0 ? 0 : static_cast<int>(__ldg(&p.pre_off[x + 1]) - __ldg(&p.pre_off[x]));
 }
+// The position of a unit's first own row, as far as what its own rows' queries see depends
+// on it (positions that are given, or sinks): else 0, as for a unit without a prefix, and
+// two loads that wait for one another are saved.
+__device__ __forceinline__ int own_first(const AttendParams& p, int u) {
+  return p.pos || p.q_pos || (p.local > 0 && p.sinks > 0) ? prefix_len(p, u) : 0;
+}
+// Whether every query row sees its whole prefix (or, of one query per head, its unit).
+__device__ __forceinline__ bool sees_whole_prefix(const AttendParams& p) {
+  return p.nq == 1 && p.local == 0 && !p.q_pos;
+}
 __device__ __forceinline__ int64_t newest_query(const AttendParams& p, int u) {
   if (p.q_pos) return __ldg(&p.q_pos[u]);
   return prefix_len(p, u) + (__ldg(&p.tok_off[u + 1]) - __ldg(&p.tok_off[u])) - 1;

@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(192, kBig ? 1 : 2)
   const int item = blockIdx.x / p.maxch, chunk = blockIdx.x - item * p.maxch;
   const int64_t base = __ldg(&p.tok_off[item]);
   const int N = static_cast<int>(__ldg(&p.tok_off[item + 1]) - base);
-  const int first = prefix_len(p, item);
+  const int first = own_first(p, item);
   const int tiles = (N + kTok - 1) / kTok;
   const int t_end = min(tiles, (chunk + 1) * p.gpc), t_begin = chunk * p.gpc;
   if (t_begin >= t_end) {

@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(64 + 256 * QT, 1)
   // position of query row `row` (of all units): the newest query of its unit stands behind
   // the prefix and the unit's own rows
   auto place = [&](int row) {
+    if (sees_whole_prefix(p)) return INT_MAX;
     const int u = row / p.R, x = row - u * p.R;
     const int64_t own = p.mem ? __ldg(&p.tok_off[u + 1]) - __ldg(&p.tok_off[u]) : 0;
     const int64_t newest = p.q_pos ? __ldg(&p.q_pos[u]) : N + own - 1;

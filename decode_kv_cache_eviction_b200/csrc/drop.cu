@@ -14,8 +14,9 @@
 //
 // Bound: instruction issue and the latency of a few dependent block reductions at small
 // units, HBM beyond; hence vectors of four rows, loops that stay rolled and few registers
-// (keys in registers and unrolled loops took 46 us instead of 39 for 2048 units of 2176
-// rows, at half the resident warps).
+// (keys in registers and unrolled loops at half the resident warps took a fifth longer).
+// 2048 units of 2176 rows, a fifth of the weights rounded to eighths, many of them 0: 27 us
+// (58 MB; 9 at HBM's rate); 64 units of 31K rows with live mask and positions: 28 us (36 MB).
 #include <limits.h>
 
 #include "ptx.cuh"
@@ -592,9 +593,10 @@ cudaError_t drop_configure() {
 
 // As many threads per unit as the GPU holds for all units at once (1024 per SM at 64
 // registers), at least 128, with a vector each in one CTA and two in a cluster, and at
-// most kMaxRun rows a CTA.  Measured: 2048 units of 2176 rows 33 / 40 / 57 us with 128 /
-// 256 / 512 threads, 148 units 12.6 / 9.5 / 8.4; 64 units of 32768 rows 63 / 36 / 24 us in
-// one CTA, 23 in four of 512 threads and 34 in eight; 8 units 24 us in one, 13 in eight.
+// most kMaxRun rows a CTA.  Measured: 2048 units of 2176 rows 26 / 33 / 51 us with 128 /
+// 256 / 512 threads, 148 units 9.4 / 7.8 / 7.4; 64 units of 32768 rows 44 / 28 / 22 us in as
+// few CTAs as hold them, 20 in four of 512 threads and 34 in eight; 8 units 21 us in two
+// CTAs of 512 threads, 15 in four, 13 in eight.
 cudaError_t launch_drop(const DropParams& p, int U, int nmax, int nsm, cudaStream_t st) {
   const int64_t threads = 1024ll * nsm / U, nv = (nmax + 3) / 4;
   int T = 128, cs = 1;
