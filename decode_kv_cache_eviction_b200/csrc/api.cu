@@ -613,7 +613,7 @@ int rkv_fill_slots(rkv_engine* e, const rkv_batch* b, void* K, void* V, const in
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const FillExtra x = {nullptr, nullptr, nullptr, free_slots, n_free};
   t_begin(e, RKV_KERNEL_FILL, st);
-  cudaError_t err = launch_fill_slots(b->tok_off, U, new_off, K_new, V_new, K, V, keep,
+  cudaError_t err = launch_fill_slots(b->tok_off, U, new_off, Tn, K_new, V_new, K, V, keep,
                                       free_slots, n_free, x, e->status, e->nsm, st);
   t_end(e, st);
   if (err != cudaSuccess) return cuda_fail(err);

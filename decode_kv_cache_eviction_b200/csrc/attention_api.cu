@@ -567,7 +567,7 @@ int rkv_fill_slots_ex(rkv_engine* e, const rkv_batch* b, void* K, void* V,
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const FillExtra x = {pos_new, pos, acc, free_out, n_free_out};
   t_begin(e, RKV_KERNEL_FILL, st);
-  cudaError_t err = launch_fill_slots(b->tok_off, U, new_off, K_new, V_new, K, V, keep,
+  cudaError_t err = launch_fill_slots(b->tok_off, U, new_off, Tn, K_new, V_new, K, V, keep,
                                       free_slots, n_free, x, e->status, e->nsm, st);
   t_end(e, st);
   if (err != cudaSuccess) return cuda_fail(err);

@@ -292,7 +292,7 @@ struct FillExtra {
   int32_t* n_free_out;
 };
 cudaError_t launch_fill_slots(const int64_t* tok_off, int U, const int64_t* new_off,
-                              const void* K_new, const void* V_new, void* K, void* V,
+                              int64_t new_tokens, const void* K_new, const void* V_new, void* K, void* V,
                               uint8_t* keep, const int32_t* free_slots, const int32_t* n_free,
                               const FillExtra& x, int* status, int nsm, cudaStream_t st);
 

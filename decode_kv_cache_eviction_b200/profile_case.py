@@ -12,7 +12,8 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__)))) 
 
 import torch  # noqa: E402
 
-from decode_kv_cache_eviction_b200 import Batch, Engine, workloads as W  # noqa: E402
+from decode_kv_cache_eviction_b200 import (Batch, Engine, Offsets, Prefix,  # noqa: E402
+                                           workloads as W)
 
 ap = argparse.ArgumentParser()
 ap.add_argument("--units", type=int, default=32)
@@ -24,11 +25,37 @@ ap.add_argument("--extras", action="store_true",
                 help="also run the in-place eviction and the adaptive-budget kernels")
 ap.add_argument("--select-only", type=int, default=0,
                 help="tile the units' scores over this many units and run only the selection")
+ap.add_argument("--decode", action="store_true",
+                help="a decode step on the cache instead: attention with weights for the newest "
+                     "query and for all window queries, a prefix of half a unit shared by 16 units "
+                     "each, eviction by the weights, one block of new tokens per unit")
 a = ap.parse_args()
 wl = W.custom(name="long_trace_32k", n_kv_head=a.units, group=4, window=8, budget=4096,
               n_min=a.n, dup_frac=0.3, dup_noise=0.05, span_len=(32, 256))
 gb = W.generate(wl, seed=0, device="cuda")
 b = Batch(gb.K, gb.V, gb.Q, gb.tok_off)
+if a.decode:
+    U, T, half = b.num_units, b.num_tokens, a.n // 2
+    eng = Engine(4, 8, U, T, redundancy="closed")
+    acc, acc2 = torch.zeros(T, device="cuda"), torch.zeros(T, device="cuda")
+    keep, free, nfree = eng.alloc_in_place(b)
+    P = (U + 15) // 16
+    pre = Prefix(gb.K[:P * half], gb.V[:P * half], [half * k for k in range(P + 1)],
+                 [u // 16 for u in range(U)])
+    short = Batch(gb.K[:256 * U], gb.V[:256 * U], None, [256 * u for u in range(U + 1)])
+    new = Offsets([512 * u for u in range(U + 1)], "cuda")
+    one = gb.Q[:, :, -1:].contiguous()
+    o1, o8 = torch.empty_like(one), torch.empty_like(gb.Q)
+    for _ in range(a.iters):
+        eng.attend(b, one, o1, acc=acc, acc_out=acc)
+        eng.attend(b, gb.Q, o8, acc=acc, acc_out=acc2)
+        eng.attend_shared(short, pre, gb.Q, o8)
+        eng.evict_accumulated(b, acc, 4096, keep, free, nfree, sinks=4, acc_out=acc2)
+        eng.fill_slots_ex(b, new, gb.K[:512 * U], gb.V[:512 * U], keep, free, nfree, acc=acc2)
+    eng.check_status()
+    torch.cuda.synchronize()
+    print("ok", U, T)
+    sys.exit(0)
 eng = Engine(4, 8, b.num_units, b.num_tokens, redundancy=a.mode, symmetric_gemm=a.symmetric)
 ra, rr = eng.alloc_scores(b)
 if a.select_only:

@@ -209,6 +209,40 @@ def test_fill_with_positions(in_place, seed):
         assert np.array_equal(d["free"].cpu().numpy(), free) and np.array_equal(d["nf"].cpu().numpy(), nf)
 
 
+@pytest.mark.parametrize("units,each", [(700, 1), (700, 100), (60, 150), (60, 3)])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_fill_many_units(units, each, in_place):
+    """More units than the grid, and fewer than SMs with more rows than a pass."""
+    rng = np.random.default_rng(units + each)
+    n, free_rows = 200, 170
+    T = units * n
+    slots = np.stack([np.sort(rng.permutation(n)[:free_rows]) for _ in range(units)])
+    free = np.full((units, n), -1, np.int32)
+    free[:, :free_rows] = slots
+    keep = np.ones((units, n), np.uint8)
+    np.put_along_axis(keep, slots, 0, axis=1)
+    K = torch.zeros((T, 128), dtype=torch.bfloat16, device=DEV)
+    V = torch.zeros_like(K)
+    Kn, Vn = (torch.randn((units * each, 128), device=DEV).to(torch.bfloat16) for _ in range(2))
+    to = dev((slots[:, :each] + n * np.arange(units)[:, None]).reshape(-1).astype(np.int64))
+    Kw, Vw = K.clone(), V.clone()
+    Kw[to], Vw[to] = Kn, Vn
+    np.put_along_axis(keep_want := keep.copy(), slots[:, :each], 1, axis=1)
+    left = np.full((units, n), -1, np.int32)
+    left[:, :free_rows - each] = slots[:, each:]
+    k, f = dev(keep.reshape(-1)), dev(free.reshape(-1))
+    c = torch.full((units,), free_rows, dtype=torch.int32, device=DEV)
+    fo, no = (f, c) if in_place else (torch.full_like(f, -7), torch.full_like(c, -7))
+    eng = Engine(1, 4, units, T, redundancy="closed")
+    kw = {} if in_place else dict(free_out=fo, n_free_out=no)
+    eng.fill_slots_ex(Batch(K, V, None, n * np.arange(units + 1)), Offsets(each * np.arange(units + 1), DEV),
+                      Kn, Vn, k, f, c, **kw)
+    eng.check_status()
+    assert torch.equal(K, Kw) and torch.equal(V, Vw)
+    assert np.array_equal(k.cpu().numpy(), keep_want.reshape(-1))
+    assert np.array_equal(fo.cpu().numpy(), left.reshape(-1)) and bool((no == free_rows - each).all())
+
+
 def test_fill_more_tokens_than_free_slots():
     rng, off, K, V, keep, free, nf = _fill_state([100, 50], 3, 0.2)
     eng = Engine(1, 4, 2, 150, redundancy="closed")
