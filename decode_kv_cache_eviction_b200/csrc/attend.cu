@@ -6,13 +6,18 @@
 //
 // One pass over K and V with a running maximum and sum.  A unit's rows are cut
 // into chunks, one CTA each, and the chunks' (maximum, sum, weighted V) are
-// joined in chunk order (join_kernel), so results do not depend on timing.
+// joined in chunk order, by the unit's last CTA (up to 8 query rows) or by
+// finish_kernel, so results do not depend on timing.
 //
 // Bound: HBM.  A row is 512 bytes, and with R = G n_q query rows costs 512 R
-// flops; at R <= 32 that is below what mma.sync sustains at full bandwidth, so
+// flops; at R <= 16 that is below what mma.sync sustains at full bandwidth, so
 // the products run on m16n8k16 steps with the 16 TOKENS as the M side: the few
 // query rows are the N side (8 per step), nothing is padded to 16 or 128 rows,
-// and a K or V fragment is read once for all query rows.
+// and a K or V fragment is read once for all query rows of a CTA, at most 16.  More
+// query rows go through the kernel on tcgen05, or where that does not apply (live masks,
+// positions) or does not pay (short units) to several CTAs per chunk that share its rows
+// in L2: 64 units of 16000 rows 99 / 103 / 147 us at 8 / 16 / 32 query rows (81 at HBM's
+// rate; one CTA with all 32 query rows held too many registers, 176).
 //
 // A warp works alone: it scans its 32-row groups (keep byte, position), appends
 // the visible rows to a short list, and copies 16 listed rows of K and V per
@@ -34,16 +39,12 @@ enum AtMode { kOwn = 0, kPrefix = 1 };
 
 constexpr int kStageBytes = 2 * kAtTok * kRowBytes;   // K and V
 
-// Ring depth and warps per SM.  Twelve warps with two stages each hide the steps'
-// latencies better than eight with three (2048 units x 2176 rows: 448 -> 394 us) and
-// keep 96 KB in flight per SM; 32 query rows need the registers.
-template <int NB>
-struct AtCfg {
-  static constexpr int kStages = NB == 4 ? 3 : 2;
-  static constexpr int kWarps = NB == 4 ? 8 : 12;
-};
+// Ring depth of a warp, and warps per SM.  Twelve warps with two stages each hide the
+// steps' latencies better than eight with three (2048 units x 2176 rows: 448 -> 394 us)
+// and keep 96 KB in flight per SM.
+constexpr int NS = 2;
+constexpr int kWarpsPerSm = 12;
 
-template <int NS>
 struct AtWarpShared {
   int slot[kList];
   int pos[kList];
@@ -286,26 +287,30 @@ __device__ __forceinline__ void weights_any(const AttendParams& p, int64_t base,
   }
 }
 
-// NB: query rows / 8 of this launch (1, 2 or 4).  kOne: one query per head, so a row
+// NB: query rows / 8 of a CTA (1 or 2).  kOne: one query per head, so a row
 // is seen by all query rows of its unit or by none.
 template <int NB, int kMode, bool kOne, int W>
-__global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(const __grid_constant__ AttendParams p) {
-  constexpr int NS = AtCfg<NB>::kStages;
+__global__ void __launch_bounds__(32 * W, kWarpsPerSm / W)
+    attend_kernel(const __grid_constant__ AttendParams p) {
+  constexpr int kRows = 8 * NB;   // query rows of a CTA
   extern __shared__ __align__(256) uint8_t at_smem[];
-  __shared__ AtWarpShared<NS> wsh[W];
-  __shared__ int s_qp[32];   // positions of the query rows
-  __shared__ float s_ml[W][2][32];
-  __shared__ float s_lse2[32];
+  __shared__ AtWarpShared wsh[W];
+  __shared__ int s_qp[kRows];   // positions of the query rows
+  __shared__ float s_ml[W][2][kRows];
+  __shared__ float s_lse2[kRows];
   __shared__ int s_last;
   const int tid = threadIdx.x, lane = tid & 31, wp = tid >> 5;
   const int g = lane >> 2, q = lane & 3;
-  AtWarpShared<NS>& ws = wsh[wp];
+  AtWarpShared& ws = wsh[wp];
 
   allow_next_launch();   // the own rows' kernel, or the weights'
   // what this CTA works on: rows [row0, row0 + nrow) of queries against groups
   // of the sequence of N rows at `base`
-  const int item = blockIdx.x / p.maxch, chunk = blockIdx.x - item * p.maxch;
-  const int row0 = static_cast<int>(blockIdx.y) * 32;
+  // (more than 16 query rows: the CTAs of one chunk next to each other, so that all but one
+  // find its rows in L2)
+  const int blocks = NB == 2 && kMode == kOwn ? (p.R + kRows - 1) / kRows : 1;
+  const int work = blockIdx.x / blocks, row0 = (blockIdx.x - work * blocks) * kRows;
+  const int item = work / p.maxch, chunk = work - item * p.maxch;
   int total = p.R;   // query rows of the item
   int64_t base, end;
   int mo = 0;
@@ -314,12 +319,12 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
     end = __ldg(&p.pre_off[item + 1]);
     mo = __ldg(&p.mem_off[item]);
     total = (__ldg(&p.mem_off[item + 1]) - mo) * p.R;
-    if (row0 >= total) return;
+    if (total == 0) return;
   } else {
     base = __ldg(&p.tok_off[item]);
     end = __ldg(&p.tok_off[item + 1]);
   }
-  const int nrow = min(32, total - row0);
+  const int nrow = min(kRows, total - row0);
   // query row r of this CTA: its unit and its row of Q
   auto row_of = [&](int r) -> int64_t {
     if (kMode != kPrefix) return static_cast<int64_t>(item) * p.R + row0 + r;
@@ -343,7 +348,7 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
   int first = 0;
   int64_t qmin, qmax;
   if (kMode == kPrefix) {
-    if (tid < 32) {
+    if (tid < kRows) {
       int v = sees_whole_prefix(p) ? INT_MAX : INT_MIN;
       if (tid < nrow && !sees_whole_prefix(p)) {
         const int64_t rr = row_of(tid);
@@ -366,7 +371,7 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
     qmax = p.q_pos ? static_cast<int64_t>(__ldg(&p.q_pos[item])) : static_cast<int64_t>(first) + N - 1;
     qmin = qmax - (p.nq - 1);
     if (!kOne) {
-      if (tid < 32) s_qp[tid] = tid < nrow ? clamp32(qmin + (row0 + tid) % p.nq) : INT_MIN;
+      if (tid < kRows) s_qp[tid] = tid < nrow ? clamp32(qmin + (row0 + tid) % p.nq) : INT_MIN;
       __syncthreads();
     }
   }
@@ -721,7 +726,7 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
   // the prefix's parts: this launch may have started while they were computed
   if (kMode == kOwn && p.pre_o) wait_for_previous_launch();
   // one warp per query row, lane = four dimensions
-  for (int r = wp; r < min(nrow, 8 * NB); r += W) {
+  for (int r = wp; r < nrow; r += W) {
     RowSum x = no_rows();
 #pragma unroll
     for (int w = 0; w < W; ++w) {
@@ -747,7 +752,7 @@ __global__ void __launch_bounds__(32 * W, AtCfg<NB>::kWarps / W) attend_kernel(c
       // the CTA that finishes a unit's rows last joins its parts
       __threadfence();
       __syncthreads();
-      int* cnt = p.count + static_cast<int64_t>(item) * gridDim.y + blockIdx.y;
+      int* cnt = p.count + item;
       if (tid == 0) s_last = atomicAdd(cnt, 1) == p.maxch - 1;
       __syncthreads();
       if (!s_last) return;
@@ -808,7 +813,7 @@ __global__ void __launch_bounds__(128) finish_kernel(const __grid_constant__ Att
 
 template <int NB, int kMode, int W>
 __host__ __device__ constexpr int at_smem_bytes() {
-  const int ring = W * AtCfg<NB>::kStages * kStageBytes;
+  const int ring = W * NS * kStageBytes;
   const int fin = W * 8 * NB * kOStride * 4;
   return ring > fin ? ring : fin;
 }
@@ -823,7 +828,6 @@ template <int kMode, int W>
 cudaError_t configure_mode() {
   cudaError_t e = configure_one<1, kMode, false, W>();
   if (e == cudaSuccess) e = configure_one<2, kMode, false, W>();
-  if (e == cudaSuccess) e = configure_one<4, kMode, false, W>();
   return e;
 }
 
@@ -855,8 +859,7 @@ cudaError_t launch_mode(const AttendParams& p, int rows, dim3 grid, bool early, 
     if (kMode == kOwn && p.nq == 1) return launch_one<1, kOwn, true, W>(p, grid, early, st);
     return launch_one<1, kMode, false, W>(p, grid, early, st);
   }
-  if (rows <= 16) return launch_one<2, kMode, false, W>(p, grid, early, st);
-  return launch_one<4, kMode, false, W>(p, grid, early, st);
+  return launch_one<2, kMode, false, W>(p, grid, early, st);
 }
 
 }  // namespace
@@ -870,16 +873,16 @@ cudaError_t attend_configure() {
   return e;
 }
 
-int attend_warps_per_sm(int rows) { return rows <= 16 ? AtCfg<1>::kWarps : AtCfg<4>::kWarps; }
+int attend_warps_per_sm() { return kWarpsPerSm; }
 
 cudaError_t launch_attend(const AttendParams& p, int U, int warps, bool early, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(U) * p.maxch, (p.R + 31) / 32);
+  const dim3 grid(static_cast<unsigned>(U) * p.maxch * ((p.R + 15) / 16));
   return warps == 2 ? launch_mode<kOwn, 2>(p, p.R, grid, early, st)
                     : launch_mode<kOwn, 4>(p, p.R, grid, early, st);
 }
 
 cudaError_t launch_attend_prefix(const AttendParams& p, int P, int max_rows, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(P) * p.maxch, (max_rows + 31) / 32);
+  const dim3 grid(static_cast<unsigned>(P) * p.maxch);
   return launch_mode<kPrefix, 4>(p, max_rows, grid, false, st);
 }
 

@@ -66,10 +66,6 @@ int64_t part_rows(const rkv_engine* e, bool shared) {
   const int64_t split = 6ll * e->nsm * std::min<int64_t>(one, 32);
   return split + (shared ? 2 * all + static_cast<int64_t>(e->nsm) * std::min<int64_t>(all, 256) : 0);
 }
-// Counters of split units: one per unit and 32 query rows.
-int64_t part_counts(const rkv_engine* e) {
-  return static_cast<int64_t>(e->cfg.max_units) * ((e->cfg.group * e->cfg.window + 31) / 32);
-}
 
 // Scratch of the attention calls, allocated once: `rows` parts, the rows' log2
 // sums and the counters (zero between calls).  Not while a stream is captured.
@@ -85,7 +81,7 @@ int attend_scratch(rkv_engine* e, float** buf, int64_t rows, bool logits, cudaSt
   if (*buf) return RKV_OK;
   const size_t sums = static_cast<size_t>(rows) * kPartFloats +
                       static_cast<size_t>(e->cfg.max_units) * e->cfg.group * e->cfg.window;
-  const size_t counts = static_cast<size_t>(part_counts(e));
+  const size_t counts = static_cast<size_t>(e->cfg.max_units);   // arrived chunks of split units
   if (rkv_engine_alloc(e, reinterpret_cast<void**>(buf), (sums + counts) * sizeof(float)) !=
       cudaSuccess) {
     cudaGetLastError();
@@ -286,7 +282,7 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
   rc = attend_scratch(e, buf, cap, logits, st);
   if (rc != RKV_OK) return rc;
   const int64_t rows = static_cast<int64_t>(U) * R;
-  const int rg = (R + 31) / 32;
+  const int rg = (R + 15) / 16;   // CTAs that share a chunk
   AttendParams p = {};
   p.tok_off = b->tok_off;
   p.K = static_cast<const uint4*>(b->K);
@@ -337,8 +333,8 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
   }
   int own = 1, warps = 4;
   const double narrow = pick_shape(sample, rg * static_cast<int64_t>(U), rg * gsum, gmax,
-                                   static_cast<int64_t>(attend_warps_per_sm(R)) * e->nsm,
-                                   R <= 8 ? 0.75 : R <= 16 ? 1.0 : 2.5, cap / rows - (x ? 1 : 0),
+                                   static_cast<int64_t>(attend_warps_per_sm()) * e->nsm,
+                                   R <= 8 ? 0.75 : 1.0, cap / rows - (x ? 1 : 0),
                                    logits, &warps, &own);
   const int64_t used = own > 1 ? static_cast<int64_t>(own) * rows : 0;   // parts of own chunks
   cudaError_t err;
@@ -363,7 +359,7 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     pp.pos = nullptr;
     pp.status = e->status;
     const int64_t pslots =
-        std::max<int64_t>(1, (wide ? 1 : attend_warps_per_sm(static_cast<int>(mrows)) / 4) *
+        std::max<int64_t>(1, (wide ? 1 : attend_warps_per_sm() / 4) *
                                  e->nsm / blocks);
     pp.maxch = pick_chunks(x->num_prefixes, pg, pmax, pslots, (cap - used) / rows, wide ? 1 : 4,
                            wide ? 3.0 : 4.0);
@@ -385,8 +381,8 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     ++e->launches;
   }
   // many query rows over whole units: each unit may go through the wide kernel as a
-  // prefix of its own (64 units of 15-16K rows, 32 query rows: 212 us narrow, 90 wide; 512
-  // units of 300 rows, 16 query rows: 21 and 41)
+  // prefix of its own (64 units of 16000 rows, 32 query rows: 147 us narrow, 91 wide; 512
+  // units of 300 rows, 16 query rows: 19 and 41)
   bool wide_own = false;
   if (!x && R > 8 && !a->keep && !a->pos && L.T > 0) {
     const int64_t blocks = (R + 255) / 256;

@@ -319,7 +319,7 @@ struct AttendParams {
   float* acc_out;                // [T] or null
   float* part_o;                 // parts [.., 128], null: the chunk is the whole row
   float2* part_ml;               // parts' (maximum in log2 units, sum)
-  int* count;                    // [U * row groups] arrived chunks (0 between calls)
+  int* count;                    // [U] arrived chunks (0 between calls)
   float* z;                      // [T, gp] logits for the weights, or null
   int gp;                        // heads of a row of z: R rounded up to a power of two
   // shared prefixes
@@ -335,7 +335,7 @@ struct AttendParams {
   const float2* pre_ml;
   int* status;
 };
-int attend_warps_per_sm(int rows);   // resident warps of a launch with this many query rows
+int attend_warps_per_sm();   // resident warps of the narrow kernel
 cudaError_t attend_configure();
 cudaError_t launch_attend(const AttendParams& p, int U, int warps, bool early, cudaStream_t st);
 cudaError_t launch_attend_prefix(const AttendParams& p, int P, int max_rows, cudaStream_t st);
