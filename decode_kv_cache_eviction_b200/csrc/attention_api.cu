@@ -447,7 +447,7 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     pw.status = e->status;
     const int64_t tile = p.z ? 32 : kWideTile;   // rows of a group
     const int64_t all = (static_cast<int64_t>(L.nmax) + tile - 1) / tile;
-    const int64_t wslots = (p.z ? 8 : tile_weights_ctas_per_sm(R)) * static_cast<int64_t>(e->nsm);
+    const int64_t wslots = (p.z ? 5 : tile_weights_ctas_per_sm(R)) * static_cast<int64_t>(e->nsm);
     pw.maxch = pick_chunks(U, L.T / tile + U, all, wslots, (static_cast<int64_t>(1) << 30) / U,
                            p.z ? 8 : 1, p.z ? 16.0 : 6.0);
     pw.gpc = static_cast<int>((all + pw.maxch - 1) / pw.maxch);
