@@ -520,7 +520,7 @@ int rkv_evict_accumulated(rkv_engine* e, const rkv_batch* b, const float* acc,
   p.idx = idx;
   p.n_kept = n_kept;
   p.vec = aligned(acc, 16) && aligned(acc_out, 16) && aligned(pos, 16) && aligned(live, 4) &&
-          aligned(keep, 4);
+          aligned(keep, 4) && aligned(free_slots, 16);
   p.status = e->status;
   t_begin(e, RKV_KERNEL_DROP, st);
   cudaError_t err = launch_drop(p, U, L.nmax, e->nsm, st);

@@ -58,15 +58,15 @@ constexpr int kList = 128;
 template <int T>
 struct DropShared {
   uint4 hist[2][kBins / 4];      // two in turn
-  uint32_t part[2][T / 32][4];   // the warps' values of an exchange (two in turn)
-  uint32_t total[2][4];          // this CTA's
+  uint32_t part[2][T / 32][8];   // the warps' values of an exchange (two in turn)
+  uint32_t total[2][8];          // this CTA's
   uint32_t wsum[T / 32];
   uint32_t found[3];             // bin, its rows, rows wanted of it
   uint32_t list[kList];          // keys of a small bin
   uint32_t listed;
 };
 
-// Exchanges of up to 4 values over the CTA and the cluster.
+// Exchanges of up to 8 values over the CTA and the cluster.
 template <int T>
 struct Exchange {
   DropShared<T>& s;
@@ -166,18 +166,21 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
   };
 
   // Keys of this thread's rows and what they say: the largest, the smallest, the smallest
-  // above that of 0 (less it), their number, and the newest live position.
+  // above that of 0 (less it), their number, that of those not above 0, and the newest live
+  // position.
   constexpr uint32_t kZero = 0x80000000u;   // the key of 0
-  uint32_t kmax, kmin, kpos, count;
+  uint32_t kmax, kmin, kpos, count, low_count;
   int newest;
   auto rank_rows = [&](int recent) {
-    kmax = count = 0u;
+    kmax = count = low_count = 0u;
     kmin = kpos = 0xffffffffu;
     newest = INT_MIN;
     auto see = [&](uint32_t q) {
       kmax = max(kmax, q);
       kmin = min(kmin, q);
-      kpos = min(kpos, q - (kZero + 1u));   // large below it, too
+      const uint32_t d = q - (kZero + 1u);   // its top bit: not above
+      kpos = min(kpos, d);
+      low_count += d >> 31;
     };
     // two vectors' loads in flight, without a branch between them (29.0 and 30.8 us one by one,
     // 26.8 and 27.4 two, 27.0 and 28.0 four: 2048 units of 2176 rows, 64 of 31K with positions)
@@ -246,10 +249,13 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
     rank_rows(window(N - 1));
   }
   // smallest keys as their complements
-  uint32_t m[4] = {__reduce_max_sync(0xffffffffu, kmax), ~__reduce_min_sync(0xffffffffu, kmin),
-                   __reduce_add_sync(0xffffffffu, count), ~__reduce_min_sync(0xffffffffu, kpos)};
-  uint32_t bm[4];
-  ex.all(m, bm, [](int k, uint32_t a, uint32_t x) { return k == 2 ? a + x : a > x ? a : x; });
+  uint32_t m[5] = {__reduce_max_sync(0xffffffffu, kmax), ~__reduce_min_sync(0xffffffffu, kmin),
+                   __reduce_add_sync(0xffffffffu, count), ~__reduce_min_sync(0xffffffffu, kpos),
+                   __reduce_add_sync(0xffffffffu, low_count)};
+  uint32_t bm[5];
+  ex.all(m, bm, [](int k, uint32_t a, uint32_t x) {
+    return k == 2 || k == 4 ? a + x : a > x ? a : x;
+  });
   const uint32_t ranked = m[2];
   int budget = p.budget;
   if (p.budgets) budget = min(max(p.budgets[u], 0), p.budget);
@@ -261,13 +267,17 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
     thr = kSafe - 1u;
   } else if (ranked > static_cast<uint32_t>(budget)) {
     uint32_t want = budget;
-    uint32_t high = m[0];
-    uint32_t low = ~m[1];              // the keys that are left: low .. low + span
-    // Rows of weight 0 (new tokens) would stretch the range over all exponents and crowd
-    // the others into few bins: first the keys above that of 0.
-    const uint32_t above_zero = ~m[3] + kZero + 1u;
-    bool rest = low <= kZero && above_zero > kZero && above_zero < high;
-    if (rest) low = above_zero;
+    // the keys that are left: low .. high.  Rows of weight 0 (new tokens) would stretch the
+    // range over all exponents and crowd the others into few bins: the last row to stay
+    // lies either above 0 or not.
+    uint32_t high = m[0], low = ~m[1];
+    const uint32_t positive = ranked - m[4];
+    if (positive >= want) {
+      low = ~m[3] + kZero + 1u;
+    } else {
+      want -= positive;
+      high = kZero;
+    }
     uint32_t span = high - low;
     some_ties = true;
     for (int round = 0; span > 0u; ++round) {
@@ -323,17 +333,6 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
 #pragma unroll
       for (int w = 0; w < 3; ++w)
         if (w < wp) incl += sh.wsum[w];   // bins lie in the first four warps
-      if (rest) {
-        rest = false;
-        const uint32_t total = sh.wsum[0] + sh.wsum[1] + sh.wsum[2] + sh.wsum[3];
-        if (total < want) {   // the last to stay is not among them
-          want -= total;
-          low = ~m[1];
-          high = kZero;
-          span = high - low;
-          continue;
-        }
-      }
       uint32_t above = incl - mine;
       if (wp < 4 && above < want && want <= incl) {   // one thread
 #pragma unroll
@@ -534,7 +533,16 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
     }
   }
   // what is left of the list and of idx
-  for (int i = N - nk + rank * T + tid; i < N; i += cs * T) fs[i] = -1;
+  const int rest = N - nk;
+  const int whole0 = p.vec ? rest + static_cast<int>(-(base + rest) & 3) : N;   // aligned
+  for (int i = rest + rank * T + tid; i < min(whole0, N); i += cs * T) fs[i] = -1;
+  for (int i = whole0 + 4 * (rank * T + tid); i < N; i += 4 * cs * T) {
+    if (i + 4 <= N) {
+      *reinterpret_cast<int4*>(fs + i) = make_int4(-1, -1, -1, -1);
+    } else {
+      for (int k = i; k < N; ++k) fs[k] = -1;
+    }
+  }
   if (idx)
     for (int i = nk + rank * T + tid; i < p.W; i += cs * T) idx[i] = -1;
   if (rank == 0 && tid == 0) {
