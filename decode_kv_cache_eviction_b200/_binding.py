@@ -89,6 +89,7 @@ class RkvError(RuntimeError):
 
 _lib = None
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_INT_MAX = 2**31 - 1
 
 
 def lib():
@@ -436,6 +437,8 @@ class Engine:
         U, T, dev = batch.num_units, batch.num_tokens, self.device
         if Q.dim() != 4:
             raise ValueError("Q must be [U, G, n_q, 128]")
+        if local > _INT_MAX or sinks > _INT_MAX:
+            raise ValueError("local and sinks must fit into 32 bits")
         nq = Q.shape[2]
         shape, rows, kv = (U, self.group, nq, 128), (T,), (T, 128)
         _tensor(batch.K, "K", _BF16, kv, dev, False)
@@ -456,6 +459,8 @@ class Engine:
         (may be keep); idx int32 [U, budget + sinks + w] with n_kept int32 [U]."""
         U, dev = batch.num_units, self.device
         rows, units = (batch.num_tokens,), (U,)
+        if budget > _INT_MAX or sinks > _INT_MAX:
+            raise ValueError("budget and sinks must fit into 32 bits")
         rc = _lib.rkv_evict_accumulated(
             self.h, batch.ref, _tensor(acc, "acc", _F32, rows, dev, False),
             _tensor(live, "live", _U8, rows, dev), _tensor(pos, "pos", _I32, rows, dev),

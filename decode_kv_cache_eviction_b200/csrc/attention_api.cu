@@ -260,6 +260,7 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
   if (!a->Q || !a->out || (L.T > 0 && (!b->K || !b->V))) return RKV_ERR_INVALID_ARG;
   if (a->pos && !a->q_pos) return RKV_ERR_INVALID_ARG;
   if (a->acc_in && !a->acc_out) return RKV_ERR_INVALID_ARG;
+  if (a->out == a->Q) return RKV_ERR_INVALID_ARG;   // Q is read until the last row is written
   if (!aligned(b->K, 16) || !aligned(b->V, 16) || !aligned(a->Q, 16) || !aligned(a->out, 16) ||
       !aligned(a->lse, 4) || !aligned(a->pos, 4) || !aligned(a->q_pos, 4) ||
       !aligned(a->acc_in, 4) || !aligned(a->acc_out, 4))

@@ -45,13 +45,14 @@ if a.decode:
     short = Batch(gb.K[:256 * U], gb.V[:256 * U], None, [256 * u for u in range(U + 1)])
     new = Offsets([512 * u for u in range(U + 1)], "cuda")
     one = gb.Q[:, :, -1:].contiguous()
+    kn, vn = gb.K[:512 * U].clone(), gb.V[:512 * U].clone()
     o1, o8 = torch.empty_like(one), torch.empty_like(gb.Q)
     for _ in range(a.iters):
         eng.attend(b, one, o1, acc=acc, acc_out=acc)
         eng.attend(b, gb.Q, o8, acc=acc, acc_out=acc2)
         eng.attend_shared(short, pre, gb.Q, o8)
         eng.evict_accumulated(b, acc, 4096, keep, free, nfree, sinks=4, acc_out=acc2)
-        eng.fill_slots_ex(b, new, gb.K[:512 * U], gb.V[:512 * U], keep, free, nfree, acc=acc2)
+        eng.fill_slots_ex(b, new, kn, vn, keep, free, nfree, acc=acc2)
     eng.check_status()
     torch.cuda.synchronize()
     print("ok", U, T)

@@ -246,7 +246,7 @@ typedef struct {
   const float* acc_in;     /* device [T] accumulated weights so far, NULL: zeros */
   float* acc_out;          /* device [T] or NULL: acc_in + sum over (g, t) of softmax(z)
                               for every row of the units; may be acc_in itself */
-  void* out;               /* device bf16 [U, G, n_q, d] */
+  void* out;               /* device bf16 [U, G, n_q, d], not Q's memory */
   float* lse;              /* device [U, G, n_q] or NULL */
 } rkv_attention;
 
@@ -311,7 +311,7 @@ int rkv_evict_accumulated(rkv_engine* eng, const rkv_batch* batch, const float* 
 
 /* rkv_fill_slots that also keeps what attention and eviction read: a filled row gets
  * its token's position (pos [T] from pos_new [new_off[U]]) and a zero accumulated
- * weight (acc [T]); pos and acc may be NULL.  The list that is left goes to
+ * weight (acc [T]); pos and acc may be NULL.  K_new and V_new are not part of K and V.  The list that is left goes to
  * free_out [T] and n_free_out [U]: the input buffers themselves (in place), or
  * others, which are written whole.  Units may have any length from 0 on.  Everything
  * else as for rkv_fill_slots. */

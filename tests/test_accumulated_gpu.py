@@ -287,6 +287,19 @@ def test_refusals():
     assert bool((keep == 9).all())
 
 
+def test_refusals_of_sizes():
+    eng = Engine(1, 4, 2, 150, redundancy="closed")
+    b = Batch(None, None, None, [0, 100, 150], device=DEV)
+    acc, keep = torch.rand(150, device=DEV), torch.full((150,), 9, dtype=torch.uint8, device=DEV)
+    free, nf = torch.zeros(150, dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+    for budget, sinks in ((2**32, 0), (10, 2**31)):
+        with pytest.raises(ValueError):
+            eng.evict_accumulated(b, acc, budget, keep, free, nf, sinks=sinks)
+    eng.evict_accumulated(b, acc, 2**31 - 1, keep, free, nf, sinks=2**31 - 1)    # the largest: all stay
+    torch.cuda.synchronize()
+    assert bool((keep == 1).all()) and bool((nf == 0).all())
+
+
 def test_decode_loop():
     """A decode loop on caches of fixed size: each step places one token in every
     unit, attends with accumulated weights, and evicts by them when a unit is

@@ -555,6 +555,18 @@ def test_refusals():
     assert bool(c.out.isnan().all())
 
 
+def test_refusals_of_sizes_and_overlap():
+    c = Case([100, 33], 4, 2, seed=51)
+    eng, b = c.engine(), Batch(c.K, c.V, None, c.off)
+    q = c.Q.clone()
+    _refused(B.RKV_ERR_INVALID_ARG, lambda: eng.attend(b, q, q))     # out is Q's memory
+    for kw in (dict(local=2**32 + 5), dict(sinks=2**31)):
+        with pytest.raises(ValueError):
+            eng.attend(b, q, c.out, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(q, c.Q) and bool(c.out.isnan().all())
+
+
 def _refused(code, call):
     with pytest.raises(RkvError) as ei:
         call()
