@@ -169,18 +169,12 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _tensor(t, name: str, dtype, shape, device: int, optional: bool = True):
-    """Pointer of a contiguous tensor of this type and shape on GPU ``device`` (or None)."""
-    if t is None:
-        if optional:
-            return None
-        raise ValueError(f"{name} is required")
-    if (t.dtype is dtype and t.shape == shape and t.get_device() == device
-            and t.is_contiguous()):
-        return t.data_ptr()
-    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                     f"cuda:{device}, got {t.dtype} {tuple(t.shape)} on {t.device}"
-                     f"{'' if t.is_contiguous() else ', not contiguous'}")
+try:
+    from ._tensors import tensor as _tensor   # (t, name, dtype, shape, device, optional=True)
+except ImportError:   # not built yet
+    def _tensor(*_):
+        raise RuntimeError("_tensors.so is missing: build it with "
+                           "`python -m decode_kv_cache_eviction_b200.build`")
 
 
 def _stream_on(device: int, stream) -> int:

@@ -1,4 +1,5 @@
-"""Build ``librkv.so`` (the C-ABI engine) in-tree for sm_100a with nvcc.
+"""Build ``librkv.so`` (the C-ABI engine) in-tree for sm_100a with nvcc, and with the host
+compiler ``_tensors.so``, the Python binding's argument check.
 
 Usage: ``python -m decode_kv_cache_eviction_b200.build [--force] [--verbose]``.
 The shared library is placed next to this file so that it travels with the
@@ -14,12 +15,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "librkv.so")
+TENSORS = os.path.join(HERE, "_tensors.so")
+TENSORS_SRC = os.path.join(CSRC, "tensors.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -51,20 +55,40 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _run(cmd, out: str, verbose: bool):
+    """Run a compiler that writes ``out`` (by way of a temporary file)."""
+    tmp = out + ".tmp"
+    res = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+    if verbose or res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+    if res.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed building {os.path.basename(out)}")
+    os.replace(tmp, out)
+
+
+def _build_tensors(verbose: bool):
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"]]
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *(x for i in inc for x in ("-isystem", i)), TENSORS_SRC,
+          "-L", os.path.join(root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"],
+         TENSORS, verbose)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    if force or not os.path.exists(TENSORS) or \
+            os.path.getmtime(TENSORS) < os.path.getmtime(TENSORS_SRC):
+        _build_tensors(verbose)
     if not force and not _stale():
         return LIB
     cmd = [nvcc_path(), *NVCC_FLAGS, "-I", INCLUDE]
     if verbose:
         cmd += ["-Xptxas", "-v"]
-    tmp = LIB + ".tmp"
-    cmd += ["-o", tmp, *sources()]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if verbose or res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-    if res.returncode != 0:
-        raise RuntimeError("nvcc failed building librkv.so")
-    os.replace(tmp, LIB)
+    _run([*cmd, *sources()], LIB, verbose)
     return LIB
 
 
