@@ -122,11 +122,13 @@ int pick_chunks(int64_t items, int64_t sum, int64_t nmax, int64_t slots, int64_t
 // Group counts of up to 32 units, evenly spaced over the batch, and what they say of all.
 struct Sample {
   int n = 0;
-  int groups[32];
-  // chunks of gpc groups that a unit takes on average, and groups of a chunk
+  float groups[32];
+  // chunks of gpc groups that a unit takes on average (a product with the reciprocal: whole
+  // divisions took the host longer than the launch)
   double per(int64_t gpc) const {
-    int64_t s = 0;
-    for (int i = 0; i < n; ++i) s += std::max<int64_t>(1, (groups[i] + gpc - 1) / gpc);
+    const float inv = 1.f / static_cast<float>(gpc), up = static_cast<float>(gpc) - 0.5f;
+    int s = 0;
+    for (int i = 0; i < n; ++i) s += std::max(1, static_cast<int>((groups[i] + up) * inv));
     return static_cast<double>(s) / std::max(n, 1);
   }
 };
@@ -238,13 +240,11 @@ int check_prefix(const rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, i
   return RKV_OK;
 }
 
-// Groups of `per` rows of a sequence of n that a window of `local` tokens and the
-// sinks can touch, at most.
-int64_t reach(int64_t n, int local, int sinks, int nq, int64_t per = 32) {
-  const int64_t all = (n + per - 1) / per;
-  if (local <= 0) return all;
-  return std::min<int64_t>(all, (static_cast<int64_t>(sinks) + per - 1) / per +
-                                    (static_cast<int64_t>(local) + nq) / per + 2);
+// Groups of `per` rows that a window of `local` tokens and the sinks can touch, at most.
+int64_t reach(int local, int sinks, int nq, int64_t per) {
+  if (local <= 0) return INT64_MAX;
+  return (static_cast<int64_t>(sinks) + per - 1) / per +
+         (static_cast<int64_t>(local) + nq) / per + 2;
 }
 
 int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_attention* a,
@@ -325,12 +325,13 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
   int64_t gsum = 0, gmax = 1;
   Sample sample;
   const int step = (U + 31) / 32;
+  const int64_t within = a->pos ? INT64_MAX : reach(a->local, a->sinks, p.nq, 32);
   for (int u = 0; u < U; ++u) {
     const int64_t n = b->tok_off_host[u + 1] - b->tok_off_host[u];
-    const int64_t g = a->pos ? (n + 31) / 32 : reach(n, a->local, a->sinks, p.nq);
+    const int64_t g = std::min((n + 31) / 32, within);
     gsum += g;
     gmax = std::max(gmax, g);
-    if (u % step == 0) sample.groups[sample.n++] = static_cast<int>(g);
+    if (u % step == 0) sample.groups[sample.n++] = static_cast<float>(g);
   }
   int own = 1, warps = 4;
   const double narrow = pick_shape(sample, rg * static_cast<int64_t>(U), rg * gsum, gmax,
@@ -389,12 +390,13 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     const int64_t blocks = (R + 255) / 256;
     int64_t tsum = 0, tmax = 1;
     Sample tiles;
+    const int64_t tiles_within = reach(a->local, a->sinks, p.nq, kWideTile);
     for (int u = 0; u < U; ++u) {
       const int64_t n = b->tok_off_host[u + 1] - b->tok_off_host[u];
-      const int64_t t = reach(n, a->local, a->sinks, p.nq, kWideTile);
+      const int64_t t = std::min((n + kWideTile - 1) / kWideTile, tiles_within);
       tsum += t;
       tmax = std::max(tmax, t);
-      if (u % step == 0) tiles.groups[tiles.n++] = static_cast<int>(t);
+      if (u == step * tiles.n) tiles.groups[tiles.n++] = static_cast<float>(t);
     }
     int c = 1;
     const double cost = pick_wide(tiles, U * blocks, tsum * blocks, tmax, e->nsm, cap / rows, &c);
