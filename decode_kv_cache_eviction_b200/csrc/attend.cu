@@ -35,7 +35,8 @@ constexpr int kAhead = 4;                      // groups whose masks are loaded 
 constexpr int kRowBytes = 256;
 constexpr int kOStride = 132;                  // floats per output row in shared memory
 
-enum AtMode { kOwn = 0, kPrefix = 1 };
+// kBoth: a unit's keys are its prefix's rows, then its own (each unit reads its prefix).
+enum AtMode { kOwn = 0, kBoth = 1 };
 
 constexpr int kStageBytes = 2 * kAtTok * kRowBytes;   // K and V
 
@@ -303,34 +304,28 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSm / W)
   const int g = lane >> 2, q = lane & 3;
   AtWarpShared& ws = wsh[wp];
 
-  allow_next_launch();   // the own rows' kernel, or the weights'
+  allow_next_launch();   // the join, or the weights
   // what this CTA works on: rows [row0, row0 + nrow) of queries against groups
   // of the sequence of N rows at `base`
   // (more than 16 query rows: the CTAs of one chunk next to each other, so that all but one
   // find its rows in L2)
-  const int blocks = NB == 2 && kMode == kOwn ? (p.R + kRows - 1) / kRows : 1;
+  const int blocks = NB == 2 ? (p.R + kRows - 1) / kRows : 1;
   const int work = blockIdx.x / blocks, row0 = (blockIdx.x - work * blocks) * kRows;
   const int item = work / p.maxch, chunk = work - item * p.maxch;
-  int total = p.R;   // query rows of the item
-  int64_t base, end;
-  int mo = 0;
-  if (kMode == kPrefix) {
-    base = __ldg(&p.pre_off[item]);
-    end = __ldg(&p.pre_off[item + 1]);
-    mo = __ldg(&p.mem_off[item]);
-    total = (__ldg(&p.mem_off[item + 1]) - mo) * p.R;
-    if (total == 0) return;
-  } else {
-    base = __ldg(&p.tok_off[item]);
-    end = __ldg(&p.tok_off[item + 1]);
+  const int64_t base = __ldg(&p.tok_off[item]);
+  const int N = static_cast<int>(__ldg(&p.tok_off[item + 1]) - base);
+  int NP = 0;   // rows of the prefix, from row pbase of PK and PV
+  int64_t pbase = 0;
+  if (kMode == kBoth) {
+    const int x = __ldg(&p.unit_prefix[item]);
+    if (x >= 0) {
+      pbase = __ldg(&p.pre_off[x]);
+      NP = static_cast<int>(__ldg(&p.pre_off[x + 1]) - pbase);
+    }
   }
-  const int nrow = min(kRows, total - row0);
-  // query row r of this CTA: its unit and its row of Q
-  auto row_of = [&](int r) -> int64_t {
-    if (kMode != kPrefix) return static_cast<int64_t>(item) * p.R + row0 + r;
-    const int m = (row0 + r) / p.R;
-    return static_cast<int64_t>(__ldg(&p.mem[mo + m])) * p.R + (row0 + r - m * p.R);
-  };
+  const int nrow = min(kRows, p.R - row0);
+  // query row r of this CTA: its row of Q
+  auto row_of = [&](int r) { return static_cast<int64_t>(item) * p.R + row0 + r; };
   // query rows as B fragments: row 8 nb + g, dimensions 16 ks + 2q + {0, 1} and + 8
   uint32_t bq[NB][8][2];
 #pragma unroll
@@ -344,36 +339,13 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSm / W)
       bq[nb][ks][1] = on ? __ldg(&src[8 * ks + q + 4]) : 0u;
     }
   }
-  const int N = static_cast<int>(end - base);
-  int first = 0;
-  int64_t qmin, qmax;
-  if (kMode == kPrefix) {
-    if (tid < kRows) {
-      int v = sees_whole_prefix(p) ? INT_MAX : INT_MIN;
-      if (tid < nrow && !sees_whole_prefix(p)) {
-        const int64_t rr = row_of(tid);
-        const int u = static_cast<int>(rr / p.R);
-        const int t = static_cast<int>(rr - static_cast<int64_t>(u) * p.R) % p.nq;
-        v = clamp32(newest_query(p, u) - (p.nq - 1) + t);
-      }
-      s_qp[tid] = v;
-    }
+  const int first = kMode == kBoth ? NP : own_first(p, item);
+  const int64_t qmax =
+      p.q_pos ? static_cast<int64_t>(__ldg(&p.q_pos[item])) : static_cast<int64_t>(first) + N - 1;
+  const int64_t qmin = qmax - (p.nq - 1);
+  if (!kOne) {
+    if (tid < kRows) s_qp[tid] = tid < nrow ? clamp32(qmin + (row0 + tid) % p.nq) : INT_MIN;
     __syncthreads();
-    int lo = s_qp[0], hi = s_qp[0];
-    for (int r = 1; r < nrow; ++r) {
-      lo = min(lo, s_qp[r]);
-      hi = max(hi, s_qp[r]);
-    }
-    qmin = lo;
-    qmax = hi;
-  } else {
-    first = own_first(p, item);
-    qmax = p.q_pos ? static_cast<int64_t>(__ldg(&p.q_pos[item])) : static_cast<int64_t>(first) + N - 1;
-    qmin = qmax - (p.nq - 1);
-    if (!kOne) {
-      if (tid < kRows) s_qp[tid] = tid < nrow ? clamp32(qmin + (row0 + tid) % p.nq) : INT_MIN;
-      __syncthreads();
-    }
   }
   const int qmax32 = clamp32(qmax), qmin32 = clamp32(qmin);
   const int lo_any = p.local > 0 ? clamp32(qmin - p.local) : INT_MIN;
@@ -385,11 +357,13 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSm / W)
   } else {
     sp = visible_span<5>(N, first, qmin, qmax, p.local, p.sinks);
   }
-  const int v_end = min(sp.nv, (chunk + 1) * p.gpc);
-  const uint8_t* keep = kMode == kPrefix ? nullptr : p.keep;
-  const int32_t* pos = kMode == kPrefix ? nullptr : p.pos;
-  const uint4* Kg = kMode == kPrefix ? p.PK : p.K;
-  const uint4* Vg = kMode == kPrefix ? p.PV : p.V;
+  // virtual groups: the prefix's visible ones, then the own rows'
+  Span sq = {0, 0, 0};
+  if (kMode == kBoth) sq = visible_span<5>(NP, 0, qmin, qmax, p.local, p.sinks);
+  const int nP = sq.nv;
+  const int v_end = min(nP + sp.nv, (chunk + 1) * p.gpc);
+  const uint8_t* keep = p.keep;
+  const int32_t* pos = p.pos;
 
   int qp[NB][2], qlo[NB][2];    // limits of this lane's rows 8 nb + 2q + e
 #pragma unroll
@@ -432,7 +406,12 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSm / W)
     int head = 0, cnt = 0;        // list: first entry, entries
     // a group's live bytes and positions, loaded kAhead groups ahead
     auto fetch = [&](int vv, int& alive, int& ps) {
-      const int slot = 32 * sp.group(vv) + lane;
+      if (kMode == kBoth && vv < nP) {
+        ps = 32 * sq.group(vv) + lane;
+        alive = vv < v_end && ps < NP ? 1 : 0;
+        return;
+      }
+      const int slot = 32 * sp.group(vv - nP) + lane;
       const bool in = vv < v_end && slot < N;
       alive = in ? 1 : 0;
       ps = first + slot;
@@ -444,7 +423,9 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSm / W)
     for (int k = 0; k < kAhead; ++k) fetch(v + k * W, live[k], at[k]);
     // rows of group v (virtual order: sinks' groups, then the window's)
     auto scan = [&]() {
-      const int slot = 32 * sp.group(v) + lane;
+      // a prefix's row i is listed as ~i
+      const int slot = kMode == kBoth && v < nP ? ~(32 * sq.group(v) + lane)
+                                                : 32 * sp.group(v - nP) + lane;
       const int ps = at[0];
       bool on = live[0] != 0;
 #pragma unroll
@@ -453,16 +434,7 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSm / W)
         at[k] = at[k + 1];
       }
       fetch(v + kAhead * W, live[kAhead - 1], at[kAhead - 1]);
-      if (kMode == kPrefix && p.local > 0) {
-        bool any = false;
-        for (int r = 0; r < nrow; ++r) {
-          const int x = s_qp[r];
-          any |= sees(ps, x, clamp32(static_cast<int64_t>(x) - p.local), p.sinks);
-        }
-        on = on && any;
-      } else {
-        on = on && sees(ps, qmax32, lo_any, p.sinks);
-      }
+      on = on && sees(ps, qmax32, lo_any, p.sinks);
       const uint32_t mask = __ballot_sync(0xffffffffu, on);
       if (on) {
         const int to = (head + cnt + __popc(mask & ((1u << lane) - 1u))) & (kList - 1);
@@ -487,9 +459,11 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSm / W)
         for (int h = 0; h < 2; ++h) {
           const int r = g + 8 * h;
           const bool on = r < n;
-          const int64_t row = base + (on ? ws.slot[(head + r) & (kList - 1)] : 0);
-          const uint4* ks = Kg + row * 16 + q;
-          const uint4* vs = Vg + row * 16 + q;
+          const int slot = on ? ws.slot[(head + r) & (kList - 1)] : 0;
+          const bool shared = kMode == kBoth && slot < 0;
+          const int64_t row = shared ? pbase + ~slot : base + slot;
+          const uint4* ks = (shared ? p.PK : p.K) + row * 16 + q;
+          const uint4* vs = (shared ? p.PV : p.V) + row * 16 + q;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t d = dst + 8 * h * kRowBytes + (((4 * c + q) ^ g) << 4);
@@ -552,16 +526,18 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSm / W)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) mma16816(c[nb], a, bq[nb][ks][0], bq[nb][ks][1]);
       }
-      if constexpr (kOne && kMode == kOwn) {
+      if constexpr (kOne) {
         if (p.z && 2 * q < p.gp) {   // logits for the weights, before masks and scaling
-          float* z0 = p.z + (base + ws.mslot[s][g]) * p.gp + 2 * q;
-          float* z1 = p.z + (base + ws.mslot[s][g + 8]) * p.gp + 2 * q;
+          const int r0 = ws.mslot[s][g], r1 = ws.mslot[s][g + 8];   // own rows only
+          const bool w0 = in0 && r0 >= 0, w1 = in1 && r1 >= 0;
+          float* z0 = p.z + (base + r0) * p.gp + 2 * q;
+          float* z1 = p.z + (base + r1) * p.gp + 2 * q;
           if (p.gp == 1) {
-            if (in0) *z0 = c[0][0];
-            if (in1) *z1 = c[0][2];
+            if (w0) *z0 = c[0][0];
+            if (w1) *z1 = c[0][2];
           } else {
-            if (in0) __stcg(reinterpret_cast<float2*>(z0), make_float2(c[0][0], c[0][1]));
-            if (in1) __stcg(reinterpret_cast<float2*>(z1), make_float2(c[0][2], c[0][3]));
+            if (w0) __stcg(reinterpret_cast<float2*>(z0), make_float2(c[0][0], c[0][1]));
+            if (w1) __stcg(reinterpret_cast<float2*>(z1), make_float2(c[0][2], c[0][3]));
           }
         }
       }
@@ -735,10 +711,7 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSm / W)
     }
     const int64_t row = row_of(r);
     if (p.part_o) {
-      const int64_t at =
-          kMode == kPrefix
-              ? static_cast<int64_t>(chunk) * p.rows + row
-              : (static_cast<int64_t>(item) * p.maxch + chunk) * p.R + row0 + r;
+      const int64_t at = (static_cast<int64_t>(item) * p.maxch + chunk) * p.R + row0 + r;
       __stcg(reinterpret_cast<float4*>(p.part_o + at * 128 + 4 * lane), x.o);
       if (lane == 0) __stcg(&p.part_ml[at], make_float2(x.M, x.L));
     } else {
@@ -747,31 +720,29 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSm / W)
       if (lane == 0) s_lse2[r] = x.L == 0.f ? INFINITY : x.M + log2f(x.L);
     }
   }
-  if constexpr (kMode == kOwn) {
-    if (p.count) {
-      // the CTA that finishes a unit's rows last joins its parts
-      __threadfence();
-      __syncthreads();
-      int* cnt = p.count + item;
-      if (tid == 0) s_last = atomicAdd(cnt, 1) == p.maxch - 1;
-      __syncthreads();
-      if (!s_last) return;
-      __threadfence();
-      if (tid == 0) *cnt = 0;   // ready for the next call
-      const int64_t at0 = static_cast<int64_t>(item) * p.maxch * p.R + row0;
-      for (int r = wp; r < nrow; r += W) {
-        RowSum x = join_row(no_rows(), p.maxch, [&](int c, float2& ml, const float4*& src) {
-          const int64_t at = at0 + static_cast<int64_t>(c) * p.R + r;
-          ml = __ldcg(&p.part_ml[at]);
-          src = reinterpret_cast<const float4*>(p.part_o + at * 128);
-        });
-        x = join_prefix(p, x, row_of(r), item);
-        attend_store(p, row_of(r), lane, x.M, x.L, x.o);
-      }
-    } else if (kOne && p.z && !p.part_o) {
-      __syncthreads();   // all logits of the unit are written
-      weights_any<8>(p, base, first, qmax, s_lse2, 0, N);
+  if (p.count) {
+    // the CTA that finishes a unit's rows last joins its parts
+    __threadfence();
+    __syncthreads();
+    int* cnt = p.count + item;
+    if (tid == 0) s_last = atomicAdd(cnt, 1) == p.maxch - 1;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    if (tid == 0) *cnt = 0;   // ready for the next call
+    const int64_t at0 = static_cast<int64_t>(item) * p.maxch * p.R + row0;
+    for (int r = wp; r < nrow; r += W) {
+      RowSum x = join_row(no_rows(), p.maxch, [&](int c, float2& ml, const float4*& src) {
+        const int64_t at = at0 + static_cast<int64_t>(c) * p.R + r;
+        ml = __ldcg(&p.part_ml[at]);
+        src = reinterpret_cast<const float4*>(p.part_o + at * 128);
+      });
+      x = join_prefix(p, x, row_of(r), item);
+      attend_store(p, row_of(r), lane, x.M, x.L, x.o);
     }
+  } else if (kOne && p.z && !p.part_o) {
+    __syncthreads();   // all logits of the unit are written
+    weights_any<8>(p, base, first, qmax, s_lse2, 0, N);
   }
 }
 
@@ -832,6 +803,7 @@ cudaError_t configure_one() {
 template <int kMode, int W>
 cudaError_t configure_mode() {
   cudaError_t e = configure_one<1, kMode, false, W>();
+  if (e == cudaSuccess) e = configure_one<1, kMode, true, W>();
   if (e == cudaSuccess) e = configure_one<2, kMode, false, W>();
   return e;
 }
@@ -860,10 +832,9 @@ cudaError_t launch_one(const AttendParams& p, dim3 grid, bool early, cudaStream_
 }
 template <int kMode, int W>
 cudaError_t launch_mode(const AttendParams& p, int rows, dim3 grid, bool early, cudaStream_t st) {
-  if (rows <= 8) {
-    if (kMode == kOwn && p.nq == 1) return launch_one<1, kOwn, true, W>(p, grid, early, st);
-    return launch_one<1, kMode, false, W>(p, grid, early, st);
-  }
+  if (rows <= 8)
+    return p.nq == 1 ? launch_one<1, kMode, true, W>(p, grid, early, st)
+                     : launch_one<1, kMode, false, W>(p, grid, early, st);
   return launch_one<2, kMode, false, W>(p, grid, early, st);
 }
 
@@ -872,23 +843,21 @@ cudaError_t launch_mode(const AttendParams& p, int rows, dim3 grid, bool early, 
 cudaError_t attend_configure() {
   cudaError_t e = configure_mode<kOwn, 4>();
   if (e == cudaSuccess) e = configure_mode<kOwn, 2>();
-  if (e == cudaSuccess) e = configure_one<1, kOwn, true, 4>();
-  if (e == cudaSuccess) e = configure_one<1, kOwn, true, 2>();
-  if (e == cudaSuccess) e = configure_mode<kPrefix, 4>();
+  if (e == cudaSuccess) e = configure_mode<kBoth, 4>();
+  if (e == cudaSuccess) e = configure_mode<kBoth, 2>();
   return e;
 }
 
 int attend_warps_per_sm() { return kWarpsPerSm; }
 
-cudaError_t launch_attend(const AttendParams& p, int U, int warps, bool early, cudaStream_t st) {
+cudaError_t launch_attend(const AttendParams& p, int U, int warps, bool both, bool early,
+                          cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(U) * p.maxch * ((p.R + 15) / 16));
+  if (both)
+    return warps == 2 ? launch_mode<kBoth, 2>(p, p.R, grid, early, st)
+                      : launch_mode<kBoth, 4>(p, p.R, grid, early, st);
   return warps == 2 ? launch_mode<kOwn, 2>(p, p.R, grid, early, st)
                     : launch_mode<kOwn, 4>(p, p.R, grid, early, st);
-}
-
-cudaError_t launch_attend_prefix(const AttendParams& p, int P, int max_rows, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(P) * p.maxch);
-  return launch_mode<kPrefix, 4>(p, max_rows, grid, false, st);
 }
 
 cudaError_t launch_attend_finish(const AttendParams& p, cudaStream_t st) {

@@ -136,15 +136,15 @@ struct Sample {
 // Warps per CTA and chunks per unit of the attention over own rows, by waves of CTAs on
 // the `resident` warps that the GPU holds at once.  In us: a CTA costs 5 for its start
 // and end, and per 16-row stage of a warp `step` when few run beside it and the stage's
-// share of HBM (8 KB at 6.5 TB/s) when many do; joining c parts costs 3 + 0.1 c, and the
+// share of HBM (8 KB at `rate` bytes per us) when many do; joining c parts costs 3 + 0.1 c, and the
 // weights 5 in a launch of their own or 0.3 per 32 rows and warp at the unit's end.  Measured: 128 units of 32768
 // rows 401 / 324 / 402 / 334 us in 1 / 2 / 4 / 6 chunks (modelled 389 / 340 / 395 / 344),
 // 509 windows of 1028 rows 50 us with two warps and 59 with four (50 / 62).
 double pick_shape(const Sample& sample, int64_t items, int64_t sum, int64_t nmax,
-                  int64_t resident, double step, int64_t cap, bool weights, int* warps,
-                  int* chunks) {
+                  int64_t resident, double step, double rate, int64_t cap, bool weights,
+                  int* warps, int* chunks) {
   const double avg = std::max(1.0, static_cast<double>(sum) / static_cast<double>(items));
-  const double share = resident * 8192.0 / 6.5e6;
+  const double share = resident * 8192.0 / rate;
   auto stage = [&](double part) { return std::max(step, share * part); };
   double least = 1e300;
   for (int w = 4; w >= 2; w -= 2)
@@ -171,22 +171,24 @@ double pick_shape(const Sample& sample, int64_t items, int64_t sum, int64_t nmax
   return least;
 }
 
-// The same for the wide kernel over own rows (tiles of 128, one CTA per SM): 7 us per
-// CTA, per tile 0.95 or its share of HBM, and 4 for the kernel that joins the parts.
+// The same for the wide kernel over units or prefixes (tiles of 128 tokens, one CTA per
+// SM): 7 us per CTA, per tile `step` or its share of HBM, and for the join of c parts
+// `last` + `join` c.
 double pick_wide(const Sample& sample, int64_t items, int64_t sum, int64_t nmax, int64_t slots,
-                 int64_t cap, int* chunks) {
+                 double step, double last, double join, int64_t cap, int* chunks) {
   const double avg = std::max(1.0, static_cast<double>(sum) / static_cast<double>(items));
   const double share = slots * 65536.0 / 6.5e6;
-  auto tile = [&](double part) { return std::max(0.95, share * part); };
+  auto tile = [&](double part) { return std::max(step, share * part); };
   double least = 1e300;
   for (int64_t c = 1; c <= std::min(std::max<int64_t>(1, cap), nmax); c += c < 4 ? 1 : c / 4) {
     const int64_t gpc = (nmax + c - 1) / c;
     const double per = c == 1 ? 1.0 : sample.per(gpc);
     const double waves = static_cast<double>(items) * per / slots;
     const double full = std::floor(waves), rest = waves - full;
-    double cost = 4.0 + full * (avg / per * tile(1.0) + 7.0);
+    double cost = last + full * (avg / per * tile(1.0) + 7.0);
     if (full == 0 || rest > 0.02) cost += gpc * tile(rest) + 7.0;
     cost *= full == 0 ? 0.87 : 1.05;   // against the other model, as measured
+    cost += join * c;
     if (cost < least) {
       least = cost;
       *chunks = static_cast<int>(c);
@@ -331,56 +333,86 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     const int64_t g = std::min((n + 31) / 32, within);
     gsum += g;
     gmax = std::max(gmax, g);
-    if (u % step == 0) sample.groups[sample.n++] = static_cast<float>(g);
+    if (u == step * sample.n) sample.groups[sample.n++] = static_cast<float>(g);
   }
+  const int64_t resident = static_cast<int64_t>(attend_warps_per_sm()) * e->nsm;
+  const double stage = R <= 8 ? 0.75 : 1.0;
+  // bytes per us: HBM's, or L2's where rows are read more than once
+  constexpr double kHbm = 6.5e6, kL2 = 13e6;
   int own = 1, warps = 4;
-  const double narrow = pick_shape(sample, rg * static_cast<int64_t>(U), rg * gsum, gmax,
-                                   static_cast<int64_t>(attend_warps_per_sm()) * e->nsm,
-                                   R <= 8 ? 0.75 : 1.0, cap / rows - (x ? 1 : 0),
-                                   logits, &warps, &own);
+  const double narrow =
+      pick_shape(sample, rg * static_cast<int64_t>(U), rg * gsum, gmax, resident, stage,
+                 std::min(kL2, kHbm * rg), cap / rows - (x ? 1 : 0), logits, &warps, &own);
   const int64_t used = own > 1 ? static_cast<int64_t>(own) * rows : 0;   // parts of own chunks
   cudaError_t err;
+  bool both = false;
   if (x) {
-    const int64_t mrows = static_cast<int64_t>(members) * R;
-    // up to 4 query rows per prefix: the same kernel as the own rows; more: 128- or
-    // 256-row tiles on tcgen05 (32 prefixes of 4096 tokens, 4 rows: 16.4 and 18.0 us; 8
-    // prefixes, 8 rows: 18.0 and 14.3; 32 prefixes, 16 rows: 22.9 and 20.3, 24 rows: 36.1
-    // and 21.5).  Up to 16 rows over few tokens also go the first way, whose CTAs share the
-    // SMs with the own rows' (8 prefixes of 2048 tokens, 16 rows: 16.6 and 19.8).
-    const bool wide = mrows > 16 || (mrows > 4 && psum > 2ll * e->nsm * kWideTile);
-    const int64_t tile = wide ? kWideTile : 32;
-    const int64_t blocks = wide ? (mrows + 255) / 256 : 1;
+    // Either each unit reads its prefix before its own rows (from L2, where others read it
+    // too), or the prefixes go through the wide kernel first, for all their units at once.
+    // One launch and two, in us: 8 prefixes of 2048 tokens with 4 units each 12.7 and 13.9; 2
+    // of 18500 with one unit of 16 query rows 19.9 and 26.8; 128 of 4096 with one unit 50 and
+    // 59; 32 of 4096 with 4 units 37 and 28, with 8 units 64 and 32; 1 of 8000 with 64 units
+    // 43 and 20.
+    Sample all;
+    int64_t dsum = 0, dmax = 1;
+    const int64_t pwithin = reach(a->local, a->sinks, p.nq, 32);
+    for (int u = 0; u < U; ++u) {
+      const int k = x->unit_prefix_host[u];
+      const int64_t n = b->tok_off_host[u + 1] - b->tok_off_host[u];
+      int64_t g = std::min((n + 31) / 32, within);
+      if (k >= 0) g += std::min((x->off_host[k + 1] - x->off_host[k] + 31) / 32, pwithin);
+      dsum += g;
+      dmax = std::max(dmax, g);
+      if (u == step * all.n) all.groups[all.n++] = static_cast<float>(g);
+    }
+    const double again = static_cast<double>(rg * dsum) / (gsum + (psum + 31) / 32);
+    int dwarps = 4, dchunks = 1;
+    const double direct =
+        pick_shape(all, rg * static_cast<int64_t>(U), rg * dsum, dmax, resident, stage,
+                   std::min(kL2, kHbm * std::max(1.0, again)), cap / rows, logits, &dwarps,
+                   &dchunks);
+    const int64_t mrows = static_cast<int64_t>(members) * R, blocks = (mrows + 255) / 256;
+    Sample tiles;
+    const int P = x->num_prefixes, pstep = (P + 31) / 32;
     int64_t pg = 0, pmax = 1;
-    for (int k = 0; k < x->num_prefixes; ++k) {
-      const int64_t g = (x->off_host[k + 1] - x->off_host[k] + tile - 1) / tile;
+    for (int k = 0; k < P; ++k) {
+      const int64_t g = (x->off_host[k + 1] - x->off_host[k] + kWideTile - 1) / kWideTile;
       pg += g;
       pmax = std::max(pmax, g);
+      if (k == pstep * tiles.n) tiles.groups[tiles.n++] = static_cast<float>(g);
     }
-    AttendParams pp = p;
-    pp.keep = nullptr;
-    pp.pos = nullptr;
-    pp.status = e->status;
-    const int64_t pslots =
-        std::max<int64_t>(1, (wide ? 1 : attend_warps_per_sm() / 4) *
-                                 e->nsm / blocks);
-    pp.maxch = pick_chunks(x->num_prefixes, pg, pmax, pslots, (cap - used) / rows, wide ? 1 : 4,
-                           wide ? 3.0 : 4.0);
-    pp.gpc = static_cast<int>((pmax + pp.maxch - 1) / pp.maxch);
-    pp.part_o = part_o + used * 128;
-    pp.part_ml = part_ml + used;
-    p.pre_chunks = pp.maxch;
-    p.pre_o = pp.part_o;
-    p.pre_ml = pp.part_ml;
-    CUtensorMap kmap, vmap;
-    if (wide && (make_map(e, &kmap, x->K, static_cast<uint64_t>(psum), kWideTile) != RKV_OK ||
-                 make_map(e, &vmap, x->V, static_cast<uint64_t>(psum), kWideTile) != RKV_OK))
-      return RKV_ERR_CUDA;
-    t_begin(e, RKV_KERNEL_SHARED, st);
-    err = wide ? launch_attend_wide(kmap, vmap, pp, x->num_prefixes, static_cast<int>(mrows), st)
-               : launch_attend_prefix(pp, x->num_prefixes, static_cast<int>(mrows), st);
-    t_end(e, st);
-    if (err != cudaSuccess) return cuda_fail(err);
-    ++e->launches;
+    int wchunks = 1;
+    // a tile takes 1.5 us with 256 query rows; a warp joins up to four rows one by one
+    const double wide = pick_wide(tiles, P * blocks, pg * blocks, pmax, e->nsm,
+                                  mrows > kWideTile ? 1.5 : 0.95, 0.0,
+                                  0.09 * ((std::min(R, 16) + 3) / 4), (cap - used) / rows, &wchunks);
+    both = direct < 1.15 * (wide + narrow - 5.0);   // as measured; 5: the second starts early
+    if (both) {
+      own = dchunks;
+      warps = dwarps;
+      gmax = dmax;
+    } else {
+      AttendParams pp = p;
+      pp.keep = nullptr;
+      pp.pos = nullptr;
+      pp.status = e->status;
+      pp.maxch = wchunks;
+      pp.gpc = static_cast<int>((pmax + pp.maxch - 1) / pp.maxch);
+      pp.part_o = part_o + used * 128;
+      pp.part_ml = part_ml + used;
+      p.pre_chunks = pp.maxch;
+      p.pre_o = pp.part_o;
+      p.pre_ml = pp.part_ml;
+      CUtensorMap kmap, vmap;
+      if (make_map(e, &kmap, x->K, static_cast<uint64_t>(psum), kWideTile) != RKV_OK ||
+          make_map(e, &vmap, x->V, static_cast<uint64_t>(psum), kWideTile) != RKV_OK)
+        return RKV_ERR_CUDA;
+      t_begin(e, RKV_KERNEL_SHARED, st);
+      err = launch_attend_wide(kmap, vmap, pp, P, static_cast<int>(mrows), st);
+      t_end(e, st);
+      if (err != cudaSuccess) return cuda_fail(err);
+      ++e->launches;
+    }
   }
   // many query rows over whole units: each unit may go through the wide kernel as a
   // prefix of its own (64 units of 16000 rows, 32 query rows: 147 us narrow, 91 wide; 512
@@ -399,7 +431,8 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
       if (u == step * tiles.n) tiles.groups[tiles.n++] = static_cast<float>(t);
     }
     int c = 1;
-    const double cost = pick_wide(tiles, U * blocks, tsum * blocks, tmax, e->nsm, cap / rows, &c);
+    const double cost = pick_wide(tiles, U * blocks, tsum * blocks, tmax, e->nsm, 0.95, 4.0, 0.0,
+                                  cap / rows, &c);
     wide_own = cost < narrow && static_cast<int64_t>(c) * rows <= cap;
     if (wide_own) {
       p.PK = p.K;
@@ -436,7 +469,7 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
       if (R <= 8) p.count = count;
     }
     t_begin(e, RKV_KERNEL_ATTEND, st);
-    err = launch_attend(p, U, warps, x != nullptr, st);
+    err = launch_attend(p, U, warps, both, x && !both, st);
     if (err == cudaSuccess && own > 1 && R > 8) {
       err = launch_attend_finish(p, st);
       ++e->launches;

@@ -337,8 +337,9 @@ struct AttendParams {
 };
 int attend_warps_per_sm();   // resident warps of the narrow kernel
 cudaError_t attend_configure();
-cudaError_t launch_attend(const AttendParams& p, int U, int warps, bool early, cudaStream_t st);
-cudaError_t launch_attend_prefix(const AttendParams& p, int P, int max_rows, cudaStream_t st);
+// both: each unit's prefix before its own rows
+cudaError_t launch_attend(const AttendParams& p, int U, int warps, bool both, bool early,
+                          cudaStream_t st);
 // Many query rows per prefix (tcgen05): 128-row K/V tiles, p.gpc tiles per chunk.
 constexpr int kWideTile = 128;
 cudaError_t wide_configure();

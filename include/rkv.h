@@ -407,8 +407,9 @@ enum {
   RKV_KERNEL_FILL = 6,    /* new tokens into free slots */
   RKV_KERNEL_REFREE = 7,  /* adaptive budget (newest query's attention row) */
   RKV_KERNEL_FINISH = 8,  /* symmetric GEMM form: partial sums -> m, token softmax -> r */
-  RKV_KERNEL_ATTEND = 9,  /* attention over the units' own rows, parts joined */
-  RKV_KERNEL_SHARED = 10, /* attention over shared prefixes */
+  RKV_KERNEL_ATTEND = 9,  /* attention over the units' own rows (and over prefixes that
+                             each unit reads itself), parts joined */
+  RKV_KERNEL_SHARED = 10, /* attention over shared prefixes for all their units at once */
   RKV_KERNEL_WEIGHT = 11, /* accumulated attention weights (a pass of their own) */
   RKV_KERNEL_DROP = 12,   /* eviction by accumulated weight */
   RKV_NUM_KERNELS = 13

@@ -519,6 +519,35 @@ def test_prefixes_without_rows(units):
     Case([30] * units, 4, 1, seed=48, prefixes=[0, 200], unit_prefix=up, weights=True).run().check()
 
 
+@pytest.mark.parametrize("G,nq", [(4, 1), (2, 3), (4, 4), (8, 4)])
+@pytest.mark.parametrize("local,sinks", [(0, 0), (2500, 40)])
+def test_shared_prefix_and_long_own_rows(G, nq, local, sinks):
+    """Many members of a long prefix, own rows in several parts: both kernels' parts are
+    joined; the timing names the kernels that ran."""
+    lengths = [2000, 1900, 0, 1, 700] * 8
+    for n, units in ((6000, None), (40000, [0, 1, 2, 3, 9])):
+        c = Case(lengths, G, nq, seed=70 + G, prefixes=[n, 100], local=local, sinks=sinks, weights=True,
+                 unit_prefix=[int(u % 5 == 3) for u in range(40)])
+        eng = c.engine()
+        eng.set_timing(True)
+        c.run(eng).check(units)
+    if not local:      # 32 units would read 40000 rows each
+        assert eng.read_timing()["shared"][1] == 1
+
+
+@pytest.mark.parametrize("G,nq", [(1, 1), (4, 1), (2, 3), (4, 4), (8, 4)])
+@pytest.mark.parametrize("weights", [False, True])
+def test_each_unit_reads_its_prefix(G, nq, weights):
+    """Few members: one launch over prefix and own rows, in one chunk or in many."""
+    for lengths, prefixes in (([40, 3, 0, 260], [70, 33]), ([500, 2000, 1, 64], [3000, 1])):
+        c = Case(lengths, G, nq, seed=80 + G, prefixes=prefixes, unit_prefix=[0, 1, 0, -1], weights=weights,
+                 live=0.8)
+        eng = c.engine()
+        eng.set_timing(True)
+        c.run(eng).check()
+        assert eng.read_timing()["shared"][1] == 0
+
+
 # ---------------------------------------------------------------- refusals
 def test_refusals():
     c = Case([100, 33], 4, 2, seed=50, weights=True)
