@@ -24,20 +24,22 @@ constexpr int kTok = kWideTile;
 constexpr uint32_t kTileB = kTok * 256;     // a K tile: two halves of 64 columns
 constexpr uint64_t kDrainNs = 100000000ull;
 
-// kBig: up to 256 query rows and one CTA per SM, else up to 64 and two.
-template <bool kBig>
+// Four stages of K tiles for up to 256 query rows and one CTA per SM; two for up to 64 rows
+// and two CTAs; one where a CTA has one tile, and five CTAs (671 units of 17 rows, 12 query
+// rows: 20.7 us with two stages, 16.9 with one).  Offsets behind the ring and NQ query rows:
+template <int NS>
 struct WLayout {
-  static constexpr int kStages = kBig ? 4 : 2;
-  static constexpr int kRows = kBig ? 256 : 64;
-  static constexpr uint32_t ring = 0;
-  static constexpr uint32_t q = kStages * kTileB;
-  static constexpr uint32_t qp = q + kRows * 256;             // [kRows] positions
-  static constexpr uint32_t lse = qp + kRows * 4;             // [kRows]
-  static constexpr uint32_t bars = lse + kRows * 4;
-  static constexpr uint32_t misc = bars + (2 * kStages + 5) * 8;
-  static constexpr uint32_t total = misc + 24;
-  static constexpr uint32_t alloc = total + 1024;
+  uint32_t q, qp, lse, bars, misc, alloc;   // Q, positions [NQ], log-sums [NQ], barriers, rest
+  __host__ __device__ explicit WLayout(int NQ) {
+    q = NS * kTileB;
+    qp = q + NQ * 256;
+    lse = qp + NQ * 4;
+    bars = lse + NQ * 4;
+    misc = bars + (2 * NS + 5) * 8;
+    alloc = misc + 24 + 1024;   // base aligned to 1024
+  }
 };
+__host__ __device__ __forceinline__ int padded_rows(int R) { return (R + 15) & ~15; }
 
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t par) {
   const uint32_t a = smem_u32(bar);
@@ -46,24 +48,24 @@ __device__ __forceinline__ void drain(uint64_t* bar, uint32_t par) {
     if (globaltimer_ns() - t0 > kDrainNs) return;
 }
 
-template <bool kBig>
-__global__ void __launch_bounds__(192, kBig ? 1 : 2)
+template <int NS>
+__global__ void __launch_bounds__(192, NS == 4 ? 1 : NS == 2 ? 2 : 5)
     tile_weights_kernel(const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ AttendParams p) {
-  using Lay = WLayout<kBig>;
-  constexpr int NS = Lay::kStages;
+  const int R = p.R, NQ = padded_rows(R);   // query rows, and as the N side of the product
+  const WLayout<NS> lay(NQ);
   extern __shared__ uint8_t w_raw[];
   uint8_t* sm = w_raw + ((1024u - (smem_u32(w_raw) & 1023u)) & 1023u);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + Lay::bars);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + lay.bars);
   uint64_t* empty = full + NS;
   uint64_t* d_full = empty + NS;   // [2] S^T of a tile is in tensor memory
   uint64_t* d_empty = d_full + 2;  // [2] it has been read
   uint64_t* mdone = d_empty + 2;
-  int* s_qp = reinterpret_cast<int*>(sm + Lay::qp);
-  float* s_lse = reinterpret_cast<float*>(sm + Lay::lse);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Lay::misc);
-  volatile int* abort = reinterpret_cast<volatile int*>(sm + Lay::misc + 4);
-  int8_t* lastp = reinterpret_cast<int8_t*>(sm + Lay::misc + 8);
+  int* s_qp = reinterpret_cast<int*>(sm + lay.qp);
+  float* s_lse = reinterpret_cast<float*>(sm + lay.lse);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + lay.misc);
+  volatile int* abort = reinterpret_cast<volatile int*>(sm + lay.misc + 4);
+  int8_t* lastp = reinterpret_cast<int8_t*>(sm + lay.misc + 8);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   const int item = blockIdx.x / p.maxch, chunk = blockIdx.x - item * p.maxch;
@@ -76,7 +78,6 @@ __global__ void __launch_bounds__(192, kBig ? 1 : 2)
     wait_for_previous_launch();
     return;
   }
-  const int R = p.R, NQ = (R + 15) & ~15;   // query rows, and as the N side of the product
   const int64_t qmax = p.q_pos ? static_cast<int64_t>(__ldg(&p.q_pos[item]))
                                : static_cast<int64_t>(first) + N - 1;
   const int64_t qmin = qmax - (p.nq - 1);
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(192, kBig ? 1 : 2)
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if (r < R)
       v = __ldg(reinterpret_cast<const uint4*>(p.Q) + (static_cast<int64_t>(item) * R + r) * 16 + c);
-    *reinterpret_cast<uint4*>(sm + Lay::q + (c >> 3) * NQ * 128 + r * 128 +
+    *reinterpret_cast<uint4*>(sm + lay.q + (c >> 3) * NQ * 128 + r * 128 +
                               (((c & 7) ^ (r & 7)) << 4)) = v;
   }
   for (int r = tid; r < NQ; r += 192) s_qp[r] = r < R ? clamp32(qmin + r % p.nq) : INT_MIN;
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(192, kBig ? 1 : 2)
         const int s = n % NS;
         const uint32_t ph = (n / NS) & 1;
         if (!mbar_wait(&empty[s], ph ^ 1, abort, p.status)) break;
-        uint8_t* dst = sm + Lay::ring + s * kTileB;
+        uint8_t* dst = sm + s * kTileB;
         const int y = static_cast<int>(base + static_cast<int64_t>(t) * kTok);
         mbar_arrive_expect_tx(&full[s], kTileB);
         tma_load_2d(dst, &kmap, &full[s], 0, y, pol);
@@ -155,8 +156,8 @@ __global__ void __launch_bounds__(192, kBig ? 1 : 2)
     // ------------------------------------------------------------ MMA issuer
     const uint32_t leader = elect_leader();
     const uint32_t idesc = idesc_bf16_f32(kTok, NQ);
-    const uint64_t kd = desc_kmajor_sw128(smem_u32(sm + Lay::ring));
-    const uint64_t qd = desc_kmajor_sw128(smem_u32(sm + Lay::q));
+    const uint64_t kd = desc_kmajor_sw128(smem_u32(sm));
+    const uint64_t qd = desc_kmajor_sw128(smem_u32(sm + lay.q));
     const uint32_t a_full = smem_u32(d_full), a_empty = smem_u32(empty);
     int n = 0;
     bool ok = true;
@@ -261,15 +262,33 @@ __global__ void __launch_bounds__(192, kBig ? 1 : 2)
   }
 }
 
+template <int NS>
+cudaError_t configure_one(int rows) {
+  return cudaFuncSetAttribute(tile_weights_kernel<NS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              WLayout<NS>(rows).alloc);
+}
+template <int NS>
+cudaError_t launch_one(const CUtensorMap& kmap, const AttendParams& p, int U, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(U) * p.maxch);
+  cfg.blockDim = dim3(192);
+  cfg.dynamicSmemBytes = WLayout<NS>(padded_rows(p.R)).alloc;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];   // starts while the sums are still being joined
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, tile_weights_kernel<NS>, kmap, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t tile_weights_configure() {
-  cudaError_t e = cudaFuncSetAttribute(tile_weights_kernel<false>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       WLayout<false>::alloc);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(tile_weights_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             WLayout<true>::alloc);
+  cudaError_t e = configure_one<4>(256);
+  if (e == cudaSuccess) e = configure_one<2>(64);
+  if (e == cudaSuccess) e = configure_one<1>(64);
   return e;
 }
 
@@ -277,19 +296,8 @@ int tile_weights_ctas_per_sm(int R) { return R <= 64 ? 2 : 1; }
 
 cudaError_t launch_tile_weights(const CUtensorMap& kmap, const AttendParams& p, int U,
                                 cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(U) * p.maxch);
-  cfg.blockDim = dim3(192);
-  cfg.dynamicSmemBytes = p.R <= 64 ? WLayout<false>::alloc : WLayout<true>::alloc;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];   // starts while the sums are still being joined
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = p.R <= 64 ? cudaLaunchKernelEx(&cfg, tile_weights_kernel<false>, kmap, p)
-                                  : cudaLaunchKernelEx(&cfg, tile_weights_kernel<true>, kmap, p);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  if (p.R > 64) return launch_one<4>(kmap, p, U, st);
+  return p.gpc > 1 ? launch_one<2>(kmap, p, U, st) : launch_one<1>(kmap, p, U, st);
 }
 
 }  // namespace rkv
