@@ -699,8 +699,10 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSm / W)
     }
   }
   __syncthreads();
-  // the prefix's parts: this launch may have started while they were computed
-  if (kMode == kOwn && p.pre_o) wait_for_previous_launch();
+  // The prefix's parts: this launch may have started while they were computed.  A CTA that
+  // leaves its part for a join does not hold its place until then, but one of them waits,
+  // so that this launch ends after the one before.
+  if (kMode == kOwn && p.pre_o && (!p.part_o || blockIdx.x == 0)) wait_for_previous_launch();
   // one warp per query row, lane = four dimensions
   for (int r = wp; r < nrow; r += W) {
     RowSum x = no_rows();
@@ -730,6 +732,7 @@ __global__ void __launch_bounds__(32 * W, kWarpsPerSm / W)
     if (!s_last) return;
     __threadfence();
     if (tid == 0) *cnt = 0;   // ready for the next call
+    if (kMode == kOwn && p.pre_o) wait_for_previous_launch();
     const int64_t at0 = static_cast<int64_t>(item) * p.maxch * p.R + row0;
     for (int r = wp; r < nrow; r += W) {
       RowSum x = join_row(no_rows(), p.maxch, [&](int c, float2& ml, const float4*& src) {

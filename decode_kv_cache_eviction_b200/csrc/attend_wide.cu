@@ -135,6 +135,10 @@ __global__ void __launch_bounds__(64 + 256 * QT, 1)
   const int total = p.mem ? (__ldg(&p.mem_off[item + 1]) - mo) * p.R : p.R;
   if (row0 >= total) return;
   const int nrow = min(QT * kWTile, total - row0);
+  // Row warps that have query rows (a tile's first always works); the others only copy Q.
+  // 64 units of 16000 rows, 32 query rows: 90 us either way at full clock, but 102 with all
+  // eight at work and 96 with two in a long run under the power cap.
+  auto row_warps = [&](int t) { return max(1, min(8, (nrow - t * kWTile + 15) / 16)); };
 
   // position of query row `row` (of all units): the newest query of its unit stands behind
   // the prefix and the unit's own rows
@@ -172,8 +176,8 @@ __global__ void __launch_bounds__(64 + 256 * QT, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[2 * i], 8);       // warps
-      mbar_init(&p_full[2 * i + 1], 8);
+      mbar_init(&p_full[2 * i], row_warps(QT == 2 ? i : 0));
+      mbar_init(&p_full[2 * i + 1], row_warps(QT == 2 ? i : 0));
       mbar_init(&o_done[i], 1);
     }
     mbar_init(q_full, kRowWarps);
@@ -330,10 +334,10 @@ __global__ void __launch_bounds__(64 + 256 * QT, 1)
     mma_commit_by(leader, smem_u32(mdone));
     wide_drain(mdone, 0);
     __syncwarp();
-  } else {
+  } else if (const int t = warp >> 3,   // query tile, and the warp's first row (lane) in it
+                       l0 = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);
+             l0 < 16 * row_warps(t)) {
     // ------------------------------------------------------------ rows
-    const int t = warp >> 3;                                   // query tile
-    const int l0 = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);   // first row (lane) of the warp
     const int q = lane & 3;
     const uint32_t lanes = static_cast<uint32_t>(l0) << 16;
     const uint32_t to = tmem + lanes + 256 + t * 128;

@@ -336,14 +336,18 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     if (u == step * sample.n) sample.groups[sample.n++] = static_cast<float>(g);
   }
   const int64_t resident = static_cast<int64_t>(attend_warps_per_sm()) * e->nsm;
-  const double stage = R <= 8 ? 0.75 : 1.0;
-  // bytes per us: HBM's, or L2's where rows are read more than once
+  const double stage = R <= 8 ? 0.75 : R <= 16 ? 1.0 : 1.3;
+  // bytes per us: HBM's, or L2's where units read the same rows (the CTAs of one chunk
+  // with more than 16 query rows do too, which measured 8e6)
   constexpr double kHbm = 6.5e6, kL2 = 13e6;
   int own = 1, warps = 4;
   const double narrow =
       pick_shape(sample, rg * static_cast<int64_t>(U), rg * gsum, gmax, resident, stage,
-                 std::min(kL2, kHbm * rg), cap / rows - (x ? 1 : 0), logits, &warps, &own);
-  const int64_t used = own > 1 ? static_cast<int64_t>(own) * rows : 0;   // parts of own chunks
+                 rg > 1 ? 8e6 : kHbm, cap / rows - (x ? 1 : 0), logits, &warps, &own);
+  // parts of own chunks; with more than 8 query rows and a prefix's parts also of a single
+  // one, so that every row has a warp of its own for the join (in the unit's CTA up to four
+  // rows wait for one another: 88 units of 800 rows, 32 query rows, 2 prefixes: 49.5 us, 47.7 so)
+  const int64_t used = own > 1 || (x && R > 8) ? static_cast<int64_t>(own) * rows : 0;
   cudaError_t err;
   bool both = false;
   if (x) {
@@ -365,7 +369,7 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
       dmax = std::max(dmax, g);
       if (u == step * all.n) all.groups[all.n++] = static_cast<float>(g);
     }
-    const double again = static_cast<double>(rg * dsum) / (gsum + (psum + 31) / 32);
+    const double again = static_cast<double>(dsum) / (gsum + (psum + 31) / 32);
     int dwarps = 4, dchunks = 1;
     const double direct =
         pick_shape(all, rg * static_cast<int64_t>(U), rg * dsum, dmax, resident, stage,
@@ -462,7 +466,7 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
   if (!wide_own) {
     p.maxch = own;
     p.gpc = static_cast<int>((gmax + own - 1) / own);
-    if (own > 1) {
+    if (own > 1 || (p.pre_o && R > 8)) {
       p.part_o = part_o;
       p.part_ml = part_ml;
       // up to 8 query rows are joined by the unit's last CTA, two per warp; 32 took it 16 us
@@ -470,7 +474,7 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     }
     t_begin(e, RKV_KERNEL_ATTEND, st);
     err = launch_attend(p, U, warps, both, x && !both, st);
-    if (err == cudaSuccess && own > 1 && R > 8) {
+    if (err == cudaSuccess && p.part_o && R > 8) {
       err = launch_attend_finish(p, st);
       ++e->launches;
     }
