@@ -136,13 +136,15 @@ struct Sample {
 // Warps per CTA and chunks per unit of the attention over own rows, by waves of CTAs on
 // the `resident` warps that the GPU holds at once.  In us: a CTA costs 5 for its start
 // and end, and per 16-row stage of a warp `step` when few run beside it and the stage's
-// share of HBM (8 KB at `rate` bytes per us) when many do; joining c parts costs 3 + 0.1 c, and the
-// weights 5 in a launch of their own or 0.3 per 32 rows and warp at the unit's end.  Measured: 128 units of 32768
-// rows 401 / 324 / 402 / 334 us in 1 / 2 / 4 / 6 chunks (modelled 389 / 340 / 395 / 344),
-// 509 windows of 1028 rows 50 us with two warps and 59 with four (50 / 62).
+// share of HBM (8 KB at `rate` bytes per us) when many do; joining c parts costs 3 and
+// 0.1 c for each row that a warp joins, and the weights 5 in a launch of their own or 0.3
+// per 32 rows and warp at the unit's end.  Measured: 128 units of 32768 rows 401 / 324 /
+// 402 / 334 us in 1 / 2 / 4 / 6 chunks (modelled 389 / 340 / 395 / 344), 509 windows of
+// 1028 rows 50 us with two warps and 59 with four (50 / 62).
 double pick_shape(const Sample& sample, int64_t items, int64_t sum, int64_t nmax,
-                  int64_t resident, double step, double rate, int64_t cap, bool weights,
-                  int* warps, int* chunks) {
+                  int64_t resident, int R, double rate, int64_t cap, bool weights, int* warps,
+                  int* chunks) {
+  const double step = R <= 8 ? 0.75 : R <= 16 ? 1.0 : 1.3;
   const double avg = std::max(1.0, static_cast<double>(sum) / static_cast<double>(items));
   const double share = resident * 8192.0 / rate;
   auto stage = [&](double part) { return std::max(step, share * part); };
@@ -157,7 +159,8 @@ double pick_shape(const Sample& sample, int64_t items, int64_t sum, int64_t nmax
       const double full = std::floor(waves), rest = waves - full;
       const double mean = 2.0 * avg / per / w + 0.5;
       const double most = 2.0 * static_cast<double>((gpc + w - 1) / w);
-      double cost = c > 1 ? 3.0 + 0.1 * c + (weights ? 5.0 : 0.0) : 0.0;
+      const int turns = R <= 8 ? (R + w - 1) / w : 1;   // rows that a warp joins
+      double cost = c > 1 ? 3.0 + 0.1 * c * turns + (weights ? 5.0 : 0.0) : 0.0;
       const double fixed = 5.0 + (weights && c == 1 ? 0.3 * avg / w : 0.0);
       if (full > 0) cost += full * (mean * stage(1.0) + fixed);
       cost += full == 0 || rest > 0.02 ? most * stage(rest) + fixed : (most - mean) * step;
@@ -336,13 +339,12 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     if (u == step * sample.n) sample.groups[sample.n++] = static_cast<float>(g);
   }
   const int64_t resident = static_cast<int64_t>(attend_warps_per_sm()) * e->nsm;
-  const double stage = R <= 8 ? 0.75 : R <= 16 ? 1.0 : 1.3;
   // bytes per us: HBM's, or L2's where units read the same rows (the CTAs of one chunk
   // with more than 16 query rows do too, which measured 8e6)
   constexpr double kHbm = 6.5e6, kL2 = 13e6;
   int own = 1, warps = 4;
   const double narrow =
-      pick_shape(sample, rg * static_cast<int64_t>(U), rg * gsum, gmax, resident, stage,
+      pick_shape(sample, rg * static_cast<int64_t>(U), rg * gsum, gmax, resident, R,
                  rg > 1 ? 8e6 : kHbm, cap / rows - (x ? 1 : 0), logits, &warps, &own);
   // parts of own chunks; with more than 8 query rows and a prefix's parts also of a single
   // one, so that every row has a warp of its own for the join (in the unit's CTA up to four
@@ -372,7 +374,7 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     const double again = static_cast<double>(dsum) / (gsum + (psum + 31) / 32);
     int dwarps = 4, dchunks = 1;
     const double direct =
-        pick_shape(all, rg * static_cast<int64_t>(U), rg * dsum, dmax, resident, stage,
+        pick_shape(all, rg * static_cast<int64_t>(U), rg * dsum, dmax, resident, R,
                    std::min(kL2, kHbm * std::max(1.0, again)), cap / rows, logits, &dwarps,
                    &dchunks);
     const int64_t mrows = static_cast<int64_t>(members) * R, blocks = (mrows + 255) / 256;
