@@ -267,9 +267,10 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
     thr = kSafe - 1u;
   } else if (ranked > static_cast<uint32_t>(budget)) {
     uint32_t want = budget;
-    // the keys that are left: low .. high.  Rows of weight 0 (new tokens) would stretch the
-    // range over all exponents and crowd the others into few bins: the last row to stay
-    // lies either above 0 or not.
+    // the keys that are left: low .. high, high = low + span; `want` counts from high down, so
+    // a key above it must never be taken in again.  Rows of weight 0 (new tokens) would stretch
+    // the range over all exponents and crowd the others into few bins: the last row to stay lies
+    // either above 0 or not.
     uint32_t high = m[0], low = ~m[1];
     const uint32_t positive = ranked - m[4];
     if (positive >= want) {
@@ -350,6 +351,7 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
       low += sh.found[0] << shift;
       want = sh.found[2];
       span = min((1u << shift) - 1u, high - low);
+      high = low + span;
       if (want == in_bin) {   // the whole bin stays
         thr = low - 1u;
         some_ties = false;
@@ -357,11 +359,13 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
       }
       if (span == 0u) break;
       if (cs == 1 && in_bin <= kList) {
-        // few rows left: each one's rank by comparing it with the others
+        // few rows left, in_bin of them: each one's rank by comparing it with the others
         for (int v = tid; v < nv; v += T) {
           const uint4 k = keys[v];
           auto put = [&](uint32_t x) {
-            if (x - low <= span) sh.list[atomicAdd(&sh.listed, 1u)] = x;
+            if (x - low > span) return;
+            const uint32_t to = atomicAdd(&sh.listed, 1u);
+            if (to < kList) sh.list[to] = x;
           };
           put(k.x);
           put(k.y);
@@ -391,7 +395,8 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
         break;
       }
       if (in_bin * 16u > ranked) {
-        // so many rows in one bin are likely equal: the range of their keys
+        // so many rows in one bin are likely equal: the range of their keys, which need not
+        // end where the next bins cut from it do
         uint32_t x[2] = {0u, 0u}, b[2];
         for (int v = tid; v < nv; v += T) {
           const uint4 k = keys[v];
@@ -410,7 +415,8 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
         x[1] = __reduce_max_sync(0xffffffffu, x[1]);
         ex.all(x, b, [](int, uint32_t a, uint32_t y) { return a > y ? a : y; });
         low = ~x[1];
-        span = x[0] - low;
+        high = x[0];
+        span = high - low;
       }
     }
     if (some_ties) {

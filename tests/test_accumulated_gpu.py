@@ -405,3 +405,39 @@ def test_captured_decode_step():
         for s, t in zip(x, y):
             assert torch.equal(s, t)
     assert int(ends[0][-1][6].sum()) > 0
+
+
+def crowded(bits, equal, rng):
+    """Weights of which a quarter each lies in one of four neighbouring bins of 2^bits keys when
+    the range up to the largest is cut into 512, in an order of their own.  The second bin starts
+    with a gap, so the range of its keys ends behind the bin if it is cut evenly from there, and
+    the first key of the third occurs `equal` times."""
+    size = 1 << bits
+    i = np.arange(4 * size)
+    key = np.concatenate([i[i != size], np.full(equal - 1, 2 * size), [512 * size - 1]])
+    return rng.permutation((0x3f800000 + key).astype(np.uint32).view(np.float32))
+
+
+@pytest.mark.parametrize("units,bits", [(600, 11), (150, 11), (24, 11), (24, 13)])
+@pytest.mark.parametrize("equal", [1, 40, 300])
+def test_evict_crowded_bins(units, bits, equal):
+    """Budgets at the ends of the bins that the weights crowd into, in one CTA of 128 and 512
+    threads per unit and in clusters of two and eight."""
+    rng = np.random.default_rng(units + bits + equal)
+    size = 1 << bits
+    ends = np.cumsum([1, size, size + equal - 1, size - 1])          # rows above each bin
+    budgets = (ends[:, None] + np.arange(-2, 4)).reshape(-1).clip(0)
+    acc = [crowded(bits, equal, rng) for _ in range(units)]
+    w, n = 2, len(acc[0])
+    # the two newest rows stay anyway and are not ranked
+    acc = np.concatenate([np.concatenate([a, [1.0, 1.0]]) for a in acc])
+    evict([n + w] * units, acc, int(budgets.max()), w=w, budgets=np.resize(budgets, units), with_idx=units < 100)
+
+
+@pytest.mark.parametrize("units,n", [(2048, 2176), (40, 32000)])
+def test_evict_alike_weights_beside_a_small_one(units, n):
+    """What decoding leaves where all rows are looked at alike and one is not."""
+    rng = np.random.default_rng(10)
+    acc = np.exp(0.1 * rng.standard_normal((units, n)))
+    acc[:, n // 3] = 1e-20
+    evict([n] * units, acc.reshape(-1), n, budgets=rng.integers(1, n, units), with_idx=False)
