@@ -224,6 +224,7 @@ class Batch:
         if dev is None:
             raise ValueError("a batch without K and Q needs a device")
         self.tok_off = torch.from_numpy(off).to(dev)
+        self.device = self.tok_off.get_device()
         self.c = RkvBatch(len(off) - 1, self.tok_off.data_ptr(),
                           off.ctypes.data, _ptr(K), _ptr(V), _ptr(Q))
         self.ref = ctypes.byref(self.c)
@@ -453,6 +454,9 @@ class Engine:
         (may be keep); idx int32 [U, budget + sinks + w] with n_kept int32 [U]."""
         U, dev = batch.num_units, self.device
         rows, units = (batch.num_tokens,), (U,)
+        if batch.device != dev:   # no K whose check would say so
+            raise ValueError(f"the batch's offsets are on {batch.tok_off.device}, the engine on "
+                             f"cuda:{dev}")
         if budget > _INT_MAX or sinks > _INT_MAX:
             raise ValueError("budget and sinks must fit into 32 bits")
         rc = _lib.rkv_evict_accumulated(

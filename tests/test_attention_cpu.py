@@ -111,3 +111,20 @@ def test_oracle_evict_accumulated_by_hand():
     assert kept([6, 5, 4, 3, 2, 1, 0], [1] * 7, 2, 1, sinks=1) == [0, 1, 2, 6]
     assert kept(range(7), [0, 1, 0, 1, 1, 1, 0], 1, 1) == [3, 5]
     assert kept(range(7), [0] * 7, 3, 5) == []
+
+
+def host_engine(group=4, window=8, device=0):
+    """An engine's Python side alone: what it refuses before the library is called."""
+    eng = object.__new__(rkv.Engine)
+    eng.h, eng.group, eng.window, eng.device = None, group, window, device
+    return eng
+
+
+def test_offsets_on_another_device_are_refused():
+    """A batch of offsets alone has no K that would be checked in their place."""
+    eng = host_engine()
+    rows = torch.zeros(5)
+    for device in ("cpu", "meta"):
+        b = rkv.Batch(None, None, None, [0, 5], device=device)
+        with pytest.raises(ValueError, match="offsets are on"):
+            eng.evict_accumulated(b, rows, 2, rows, rows, rows)
