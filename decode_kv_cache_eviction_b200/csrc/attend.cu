@@ -197,19 +197,21 @@ __device__ __noinline__ RowSum prefix_row(const AttendParams& p, int64_t row, in
   return s;
 }
 
-// Joins the parts that the prefix kernel left for a query row of unit u.
+// Joins the parts that the prefix kernel left for a query row of unit u.  That kernel may have
+// written them while this one was already running: no read-only loads (__ldg), which the
+// compiler may move above the wait.
 __device__ __forceinline__ RowSum join_prefix(const AttendParams& p, RowSum s, int64_t row, int u) {
   if (!p.pre_o || (p.unit_prefix && __ldg(&p.unit_prefix[u]) < 0)) return s;
   bool redo = false;
   for (int c = threadIdx.x & 31; c < p.pre_chunks; c += 32)
-    redo |= __ldg(&p.pre_ml[c * p.rows + row]).y == kRedo;
+    redo |= __ldcg(&p.pre_ml[c * p.rows + row]).y == kRedo;
   if (__any_sync(0xffffffffu, redo)) {   // from the rows themselves, then the parts of s
     const RowSum x = prefix_row(p, row, u, static_cast<int>(row - static_cast<int64_t>(u) * p.R));
     return add_rows(x, s);
   }
   return join_row(s, p.pre_chunks, [&](int c, float2& ml, const float4*& src) {
     const int64_t at = c * p.rows + row;
-    ml = __ldg(&p.pre_ml[at]);
+    ml = __ldcg(&p.pre_ml[at]);
     src = reinterpret_cast<const float4*>(p.pre_o + at * 128);
   });
 }
@@ -783,7 +785,7 @@ __global__ void __launch_bounds__(128) finish_kernel(const __grid_constant__ Att
   if (p.part_o)
     x = join_row(x, p.maxch, [&](int c, float2& ml, const float4*& src) {
       const int64_t at = (static_cast<int64_t>(u) * p.maxch + c) * p.R + r;
-      ml = p.part_ml[at];
+      ml = __ldcg(&p.part_ml[at]);
       src = reinterpret_cast<const float4*>(p.part_o + at * 128);
     });
   x = join_prefix(p, x, row, u);

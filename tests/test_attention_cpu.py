@@ -2,7 +2,9 @@
 argument checks of the C entry points and the binding, struct layouts, and the
 oracle's definitions pinned by hand."""
 import ctypes
+import glob
 import os
+import re
 import subprocess
 import tempfile
 
@@ -128,3 +130,13 @@ def test_offsets_on_another_device_are_refused():
         b = rkv.Batch(None, None, None, [0, 5], device=device)
         with pytest.raises(ValueError, match="offsets are on"):
             eng.evict_accumulated(b, rows, 2, rows, rows, rows)
+
+
+def test_no_read_only_loads_of_what_a_running_launch_writes():
+    """The second kernels of an attention call start while the first still writes its parts and
+    sums.  A race cannot be shown by its results, so the source is looked at: read-only loads
+    are for the caller's inputs."""
+    scratch = r"__ldg\(&?p\w*\.(part_o|part_ml|pre_o|pre_ml|lse2|z|count)\b"
+    files = glob.glob(os.path.join(ROOT, "decode_kv_cache_eviction_b200", "csrc", "attend*"))
+    assert len(files) >= 4
+    assert [(os.path.basename(f), m.group()) for f in files for m in re.finditer(scratch, open(f).read())] == []
