@@ -34,6 +34,7 @@ RKV_FLAG_GEMM_SYMMETRIC = 2
 RKV_FAULT_NONE = 0
 RKV_FAULT_ALLOC = 1
 RKV_FAULT_DROP_ANNOUNCE = 2
+RKV_FAULT_TENSOR_MAP = 3
 
 # Every function declared in include/rkv.h.
 EXPORTS = ("rkv_create", "rkv_destroy", "rkv_score", "rkv_select", "rkv_compact",

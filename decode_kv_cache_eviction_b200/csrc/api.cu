@@ -328,10 +328,11 @@ int rkv_destroy(rkv_engine* e) {
 int64_t rkv_launch_count(const rkv_engine* e) { return e ? e->launches : 0; }
 
 int rkv_inject_fault(rkv_engine* e, int fault) {
-  if (fault != RKV_FAULT_NONE && fault != RKV_FAULT_ALLOC && fault != RKV_FAULT_DROP_ANNOUNCE)
+  if (fault != RKV_FAULT_NONE && fault != RKV_FAULT_ALLOC && fault != RKV_FAULT_DROP_ANNOUNCE &&
+      fault != RKV_FAULT_TENSOR_MAP)
     return RKV_ERR_INVALID_ARG;
   if (!e) {
-    if (fault == RKV_FAULT_DROP_ANNOUNCE) return RKV_ERR_INVALID_ARG;
+    if (fault != RKV_FAULT_NONE && fault != RKV_FAULT_ALLOC) return RKV_ERR_INVALID_ARG;
     g_create_fault = fault;
     return RKV_OK;
   }

@@ -350,8 +350,10 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
   // one, so that every row has a warp of its own for the join (in the unit's CTA up to four
   // rows wait for one another: 88 units of 800 rows, 32 query rows, 2 prefixes: 49.5 us, 47.7 so)
   const int64_t used = own > 1 || (x && R > 8) ? static_cast<int64_t>(own) * rows : 0;
-  cudaError_t err;
-  bool both = false;
+  // which kernels run, and in how many chunks
+  bool both = false, wide_own = false;
+  AttendParams pp = {};   // the prefixes' launch
+  int prefix_rows = 0;    // query rows of its longest item
   if (x) {
     // Either each unit reads its prefix before its own rows (from L2, where others read it
     // too), or the prefixes go through the wide kernel first, for all their units at once.
@@ -398,7 +400,7 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
       warps = dwarps;
       gmax = dmax;
     } else {
-      AttendParams pp = p;
+      pp = p;
       pp.keep = nullptr;
       pp.pos = nullptr;
       pp.status = e->status;
@@ -406,24 +408,15 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
       pp.gpc = static_cast<int>((pmax + pp.maxch - 1) / pp.maxch);
       pp.part_o = part_o + used * 128;
       pp.part_ml = part_ml + used;
+      prefix_rows = static_cast<int>(mrows);
       p.pre_chunks = pp.maxch;
       p.pre_o = pp.part_o;
       p.pre_ml = pp.part_ml;
-      CUtensorMap kmap, vmap;
-      if (make_map(e, &kmap, x->K, static_cast<uint64_t>(psum), kWideTile) != RKV_OK ||
-          make_map(e, &vmap, x->V, static_cast<uint64_t>(psum), kWideTile) != RKV_OK)
-        return RKV_ERR_CUDA;
-      t_begin(e, RKV_KERNEL_SHARED, st);
-      err = launch_attend_wide(kmap, vmap, pp, P, static_cast<int>(mrows), st);
-      t_end(e, st);
-      if (err != cudaSuccess) return cuda_fail(err);
-      ++e->launches;
     }
   }
   // many query rows over whole units: each unit may go through the wide kernel as a
   // prefix of its own (64 units of 16000 rows, 32 query rows: 147 us narrow, 91 wide; 512
   // units of 300 rows, 16 query rows: 19 and 41)
-  bool wide_own = false;
   if (!x && R > 8 && !a->keep && !a->pos && L.T > 0) {
     const int64_t blocks = (R + 255) / 256;
     int64_t tsum = 0, tmax = 1;
@@ -449,23 +442,44 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
       p.part_o = part_o;
       p.part_ml = part_ml;
       p.status = e->status;
-      CUtensorMap kmap, vmap;
-      if (make_map(e, &kmap, b->K, static_cast<uint64_t>(L.T), kWideTile) != RKV_OK ||
-          make_map(e, &vmap, b->V, static_cast<uint64_t>(L.T), kWideTile) != RKV_OK)
-        return RKV_ERR_CUDA;
-      t_begin(e, RKV_KERNEL_ATTEND, st);
-      err = launch_attend_wide(kmap, vmap, p, U, R, st);
-      p.pre_chunks = p.maxch;
-      p.pre_o = part_o;
-      p.pre_ml = part_ml;
-      p.part_o = nullptr;
-      if (err == cudaSuccess) err = launch_attend_finish(p, st);
-      t_end(e, st);
-      if (err != cudaSuccess) return cuda_fail(err);
-      e->launches += 2;
     }
   }
-  if (!wide_own) {
+  const bool wide_prefix = x && !both;
+  // a unit of one chunk whose logits were left does its weights itself
+  const bool weights = a->acc_out && L.T > 0 && (own > 1 || !p.z);
+
+  // every tensor map before the first launch: on an error nothing is enqueued
+  CUtensorMap pkmap, pvmap, kmap, vmap;
+  if (wide_prefix &&
+      (make_map(e, &pkmap, x->K, static_cast<uint64_t>(psum), kWideTile) != RKV_OK ||
+       make_map(e, &pvmap, x->V, static_cast<uint64_t>(psum), kWideTile) != RKV_OK))
+    return RKV_ERR_CUDA;
+  if ((wide_own || (weights && !p.z)) &&
+      make_map(e, &kmap, b->K, static_cast<uint64_t>(L.T), kWideTile) != RKV_OK)
+    return RKV_ERR_CUDA;
+  if (wide_own && make_map(e, &vmap, b->V, static_cast<uint64_t>(L.T), kWideTile) != RKV_OK)
+    return RKV_ERR_CUDA;
+
+  cudaError_t err;
+  if (wide_prefix) {
+    t_begin(e, RKV_KERNEL_SHARED, st);
+    err = launch_attend_wide(pkmap, pvmap, pp, x->num_prefixes, prefix_rows, st);
+    t_end(e, st);
+    if (err != cudaSuccess) return cuda_fail(err);
+    ++e->launches;
+  }
+  if (wide_own) {
+    t_begin(e, RKV_KERNEL_ATTEND, st);
+    err = launch_attend_wide(kmap, vmap, p, U, R, st);
+    p.pre_chunks = p.maxch;
+    p.pre_o = part_o;
+    p.pre_ml = part_ml;
+    p.part_o = nullptr;
+    if (err == cudaSuccess) err = launch_attend_finish(p, st);
+    t_end(e, st);
+    if (err != cudaSuccess) return cuda_fail(err);
+    e->launches += 2;
+  } else {
     p.maxch = own;
     p.gpc = static_cast<int>((gmax + own - 1) / own);
     if (own > 1 || (p.pre_o && R > 8)) {
@@ -475,7 +489,7 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
       if (R <= 8) p.count = count;
     }
     t_begin(e, RKV_KERNEL_ATTEND, st);
-    err = launch_attend(p, U, warps, both, x && !both, st);
+    err = launch_attend(p, U, warps, both, wide_prefix, st);
     if (err == cudaSuccess && p.part_o && R > 8) {
       err = launch_attend_finish(p, st);
       ++e->launches;
@@ -484,7 +498,7 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     if (err != cudaSuccess) return cuda_fail(err);
     ++e->launches;
   }
-  if (a->acc_out && L.T > 0 && (own > 1 || !p.z)) {   // a unit of one chunk has done its weights
+  if (weights) {
     AttendParams pw = p;
     pw.status = e->status;
     const int64_t tile = p.z ? 32 : kWideTile;   // rows of a group
@@ -493,9 +507,6 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
     pw.maxch = pick_chunks(U, L.T / tile + U, all, wslots, (static_cast<int64_t>(1) << 30) / U,
                            p.z ? 8 : 1, p.z ? 16.0 : 6.0);
     pw.gpc = static_cast<int>((all + pw.maxch - 1) / pw.maxch);
-    CUtensorMap kmap;
-    if (!p.z && make_map(e, &kmap, b->K, static_cast<uint64_t>(L.T), kWideTile) != RKV_OK)
-      return RKV_ERR_CUDA;
     t_begin(e, RKV_KERNEL_WEIGHT, st);
     err = p.z ? launch_attend_weights(pw, U, st) : launch_tile_weights(kmap, pw, U, st);
     t_end(e, st);

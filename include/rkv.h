@@ -376,9 +376,17 @@ int rkv_check_status(rkv_engine* eng, rkv_stream_t stream);
  *   RKV_FAULT_DROP_ANNOUNCE: in the next score launch one chunk does not
  *     announce its statistics, and the waits of that launch give up after
  *     50 ms, so rkv_check_status then reports RKV_ERR_TIMEOUT;
+ *   RKV_FAULT_TENSOR_MAP: the engine's next tensor map cannot be made
+ *     (RKV_ERR_CUDA, and the call that needed it enqueues nothing in
+ *     rkv_attend and rkv_attend_shared);
  *   RKV_FAULT_NONE: disarm.
  * A fault fires once.  Returns RKV_ERR_INVALID_ARG for an unknown fault. */
-enum { RKV_FAULT_NONE = 0, RKV_FAULT_ALLOC = 1, RKV_FAULT_DROP_ANNOUNCE = 2 };
+enum {
+  RKV_FAULT_NONE = 0,
+  RKV_FAULT_ALLOC = 1,
+  RKV_FAULT_DROP_ANNOUNCE = 2,
+  RKV_FAULT_TENSOR_MAP = 3
+};
 int rkv_inject_fault(rkv_engine* eng, int fault);
 
 /* Intermediate arrays of the last rkv_score call on this engine, for checks

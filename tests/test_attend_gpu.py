@@ -632,3 +632,21 @@ def test_no_units_and_empty_units():
     eng.attend(Batch(empty, empty, None, [0, 0, 0, 0]), q, out, lse)
     torch.cuda.synchronize()
     assert bool((out == 0).all()) and bool((lse == float("-inf")).all())
+
+
+@pytest.mark.parametrize("lengths,G,nq,shared", [([300, 40], 2, 3, False), ([9000, 9000], 4, 8, False),
+                                                 ([40] * 40, 4, 1, True)])
+def test_tensor_map_that_cannot_be_made_enqueues_nothing(lengths, G, nq, shared):
+    """The weights pass from K, the wide kernel over units, and a prefix: their maps are made
+    before the first launch."""
+    kw = dict(prefixes=[9000], unit_prefix=[0] * 40) if shared else {}
+    c = Case(lengths, G, nq, seed=53, weights=True, **kw).run()
+    for t in (c.out, c.lse, c.acc_out):
+        t.fill_(float("nan"))
+    n = c.eng.launches
+    c.eng.inject_fault(B.RKV_FAULT_TENSOR_MAP)
+    _refused(B.RKV_ERR_CUDA, lambda: c.run(c.eng))
+    torch.cuda.synchronize()
+    assert c.eng.launches == n
+    assert all(bool(t.isnan().all()) for t in (c.out, c.lse, c.acc_out))
+    c.run(c.eng).check([0])

@@ -140,3 +140,8 @@ def test_no_read_only_loads_of_what_a_running_launch_writes():
     files = glob.glob(os.path.join(ROOT, "decode_kv_cache_eviction_b200", "csrc", "attend*"))
     assert len(files) >= 4
     assert [(os.path.basename(f), m.group()) for f in files for m in re.finditer(scratch, open(f).read())] == []
+
+
+def test_tensor_map_fault_needs_an_engine():
+    L = rkv.lib()
+    assert L.rkv_inject_fault(None, B.RKV_FAULT_TENSOR_MAP) == B.RKV_ERR_INVALID_ARG
