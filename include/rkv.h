@@ -253,8 +253,9 @@ typedef struct {
 /* Attention over the batch's own rows (K, V, tok_off; the batch's Q is not used).
  * Units may have any length from 0 to the engine's limit.  Sums are held in
  * fp32 and results do not depend on timing.  The first call allocates a scratch
- * of at most 15 MB (with acc_out, one query per head and G <= 8 also that of
- * rkv_refree_budget), kept until rkv_destroy (RKV_ERR_OOM if that fails;
+ * of at most 15 MB + 4 max_units (G w + 1) bytes (with acc_out, one query per head
+ * and G <= 8 also that of rkv_refree_budget), kept until rkv_destroy (RKV_ERR_OOM
+ * if that fails;
  * RKV_ERR_INVALID_ARG if `stream` is being captured then: make one call before a
  * capture).  Runs on the engine's device, whichever is current.  Captured calls
  * share the engine's scratch like eager ones: replays must be ordered with the
@@ -283,8 +284,8 @@ typedef struct {
  * row j sits at position j, own row i at prefix length + i (or pos[row]), and
  * the newest query at prefix length + N_u - 1 (or q_pos[u]).  All prefix rows are
  * live; keep, acc_in and acc_out cover the own rows (weights are those of the
- * softmax over both parts).  The first call allocates a scratch of about
- * 1040 max_units G w bytes and at most 35 MB, under the same conditions. */
+ * softmax over both parts).  The first call allocates a scratch of at most
+ * 35 MB + max_units (1044 G w + 4) bytes, under the same conditions. */
 int rkv_attend_shared(rkv_engine* eng, const rkv_batch* batch, const rkv_prefix* prefix,
                       const rkv_attention* att, rkv_stream_t stream);
 

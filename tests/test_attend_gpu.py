@@ -650,3 +650,24 @@ def test_tensor_map_that_cannot_be_made_enqueues_nothing(lengths, G, nq, shared)
     assert c.eng.launches == n
     assert all(bool(t.isnan().all()) for t in (c.out, c.lse, c.acc_out))
     c.run(c.eng).check([0])
+
+
+@pytest.mark.parametrize("units,G,nq", [(4, 4, 1), (65536, 16, 16), (4096, 4, 8)])
+@pytest.mark.parametrize("shared", [False, True])
+def test_scratch_of_the_first_call(units, G, nq, shared):
+    """At most what the header says (to 4 MB of the allocators): 15 MB + 4 max_units (G w + 1), and
+    35 MB + max_units (1044 G w + 4) for shared calls."""
+    c = Case([40, 3], G, nq, seed=54, **(dict(prefixes=[70], unit_prefix=[0, 0]) if shared else {}))
+    eng = Engine(G, nq, units, 43, redundancy="closed")
+    rows = units * G * nq
+    most = 35e6 + 1044 * rows + 4 * units if shared else 15e6 + 4 * (rows + units)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    free = torch.cuda.mem_get_info()[0]
+    b = Batch(c.K, c.V, None, c.off)
+    if shared:
+        eng.attend_shared(b, Prefix(c.PK, c.PV, c.poff, c.unit_prefix), c.Q, c.out)
+    else:
+        eng.attend(b, c.Q, c.out)
+    torch.cuda.synchronize()
+    assert free - torch.cuda.mem_get_info()[0] <= most + (1 << 22)
