@@ -172,9 +172,11 @@ def _stream(stream) -> ctypes.c_void_p:
 
 try:
     from ._tensors import tensor as _tensor   # (t, name, dtype, shape, device, optional=True)
-except ImportError:   # not built yet
+except ImportError as _e:   # not built yet, or for another PyTorch
+    _tensors_error = str(_e)
+
     def _tensor(*_):
-        raise RuntimeError("_tensors.so is missing: build it with "
+        raise RuntimeError(f"_tensors.so cannot be loaded ({_tensors_error}): build it with "
                            "`python -m decode_kv_cache_eviction_b200.build`")
 
 

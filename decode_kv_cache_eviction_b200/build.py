@@ -66,6 +66,20 @@ def _run(cmd, out: str, verbose: bool):
     os.replace(tmp, out)
 
 
+def _built_for() -> str:
+    """What _tensors.so depends on beside its source: PyTorch's C++ interface differs between
+    versions.  The text is part of the module, which loads into nothing else."""
+    import torch
+    return f"PyTorch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
+def _tensors_stale() -> bool:
+    if not os.path.exists(TENSORS) or os.path.getmtime(TENSORS) < os.path.getmtime(TENSORS_SRC):
+        return True
+    with open(TENSORS, "rb") as f:
+        return _built_for().encode() + b"\0" not in f.read()
+
+
 def _build_tensors(verbose: bool):
     import torch
     root = os.path.dirname(torch.__file__)
@@ -73,6 +87,7 @@ def _build_tensors(verbose: bool):
            os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"]]
     _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+          f'-DRKV_BUILT_FOR="{_built_for()}"',
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
           *(x for i in inc for x in ("-isystem", i)), TENSORS_SRC,
           "-L", os.path.join(root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"],
@@ -80,8 +95,7 @@ def _build_tensors(verbose: bool):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if force or not os.path.exists(TENSORS) or \
-            os.path.getmtime(TENSORS) < os.path.getmtime(TENSORS_SRC):
+    if force or _tensors_stale():
         _build_tensors(verbose)
     if not force and not _stale():
         return LIB

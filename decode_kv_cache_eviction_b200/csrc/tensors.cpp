@@ -68,6 +68,22 @@ PyMethodDef methods[] = {
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
+// Whether these are the PyTorch and the Python that the module was built for: in others the
+// objects above need not look the same.
+bool built_for_this() {
+  PyObject* torch = PyImport_ImportModule("torch");
+  PyObject* version = torch ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+  PyObject* here = version ? PyUnicode_FromFormat("PyTorch %S, %s", version, PyImport_GetMagicTag())
+                           : nullptr;
+  const bool same = here && PyUnicode_CompareWithASCIIString(here, RKV_BUILT_FOR) == 0;
+  if (here && !same)
+    PyErr_Format(PyExc_ImportError, "it was built for %s, this is %U", RKV_BUILT_FOR, here);
+  Py_XDECREF(here);
+  Py_XDECREF(version);
+  Py_XDECREF(torch);
+  return same;
+}
+
 }  // namespace
 
-PyMODINIT_FUNC PyInit__tensors() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__tensors() { return built_for_this() ? PyModule_Create(&module) : nullptr; }

@@ -6,6 +6,7 @@ import glob
 import os
 import re
 import subprocess
+import sys
 import tempfile
 
 import numpy as np
@@ -145,3 +146,23 @@ def test_no_read_only_loads_of_what_a_running_launch_writes():
 def test_tensor_map_fault_needs_an_engine():
     L = rkv.lib()
     assert L.rkv_inject_fault(None, B.RKV_FAULT_TENSOR_MAP) == B.RKV_ERR_INVALID_ARG
+
+
+def test_tensor_check_built_for_another_pytorch(tmp_path, monkeypatch):
+    """It is built again although its source is older, and it does not load."""
+    from decode_kv_cache_eviction_b200 import build
+    so = tmp_path / "_tensors.so"
+    monkeypatch.setattr(build, "TENSORS", str(so))
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "0.0.1")
+        build.build()
+    load = [sys.executable, "-c", f"import sys, torch; sys.path.insert(0, {str(tmp_path)!r}); import _tensors"]
+    got = subprocess.run(load, capture_output=True, text=True)
+    assert got.returncode != 0 and "ImportError: it was built for PyTorch 0.0.1" in got.stderr
+    was = so.stat().st_mtime_ns
+    build.build()
+    assert so.stat().st_mtime_ns > was
+    assert subprocess.run(load).returncode == 0
+    was = so.stat().st_mtime_ns
+    build.build()
+    assert so.stat().st_mtime_ns == was
