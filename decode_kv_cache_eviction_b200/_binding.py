@@ -90,7 +90,7 @@ class RkvError(RuntimeError):
 
 _lib = None
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-_INT_MAX = 2**31 - 1
+_INT_MIN, _INT_MAX = -2**31, 2**31 - 1
 
 
 def lib():
@@ -435,7 +435,7 @@ class Engine:
         U, T, dev = batch.num_units, batch.num_tokens, self.device
         if Q.dim() != 4:
             raise ValueError("Q must be [U, G, n_q, 128]")
-        if local > _INT_MAX or sinks > _INT_MAX:
+        if not (_INT_MIN <= local <= _INT_MAX and _INT_MIN <= sinks <= _INT_MAX):
             raise ValueError("local and sinks must fit into 32 bits")
         nq = Q.shape[2]
         shape, rows, kv = (U, self.group, nq, 128), (T,), (T, 128)
@@ -460,7 +460,7 @@ class Engine:
         if batch.device != dev:   # no K whose check would say so
             raise ValueError(f"the batch's offsets are on {batch.tok_off.device}, the engine on "
                              f"cuda:{dev}")
-        if budget > _INT_MAX or sinks > _INT_MAX:
+        if not (_INT_MIN <= budget <= _INT_MAX and _INT_MIN <= sinks <= _INT_MAX):
             raise ValueError("budget and sinks must fit into 32 bits")
         rc = _lib.rkv_evict_accumulated(
             self.h, batch.ref, _tensor(acc, "acc", _F32, rows, dev, False),

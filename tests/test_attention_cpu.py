@@ -166,3 +166,18 @@ def test_tensor_check_built_for_another_pytorch(tmp_path, monkeypatch):
     was = so.stat().st_mtime_ns
     build.build()
     assert so.stat().st_mtime_ns == was
+
+
+@pytest.mark.parametrize("big", [2**31, 2**32 + 5, -2**31 - 1, -2**32 + 5])
+def test_numbers_beyond_32_bits_are_refused(big):
+    """ctypes would pass their low 32 bits on."""
+    eng = host_engine()
+    b = rkv.Batch(None, None, None, [0, 5], device="cpu")
+    b.device = eng.device
+    q, rows = torch.zeros((1, 4, 1, 128), dtype=torch.bfloat16), torch.zeros(5)
+    for kw in (dict(local=big), dict(sinks=big)):
+        with pytest.raises(ValueError, match="must fit into 32 bits"):
+            eng.attend(b, q, q, **kw)
+    for budget, sinks in ((big, 0), (2, big)):
+        with pytest.raises(ValueError, match="must fit into 32 bits"):
+            eng.evict_accumulated(b, rows, budget, rows, rows, rows, sinks=sinks)
