@@ -265,7 +265,10 @@ int attend(rkv_engine* e, const rkv_batch* b, const rkv_prefix* x, const rkv_att
   if (!a->Q || !a->out || (L.T > 0 && (!b->K || !b->V))) return RKV_ERR_INVALID_ARG;
   if (a->pos && !a->q_pos) return RKV_ERR_INVALID_ARG;
   if (a->acc_in && !a->acc_out) return RKV_ERR_INVALID_ARG;
-  if (a->out == a->Q) return RKV_ERR_INVALID_ARG;   // Q is read until the last row is written
+  // Q is read until the last row is written: no byte of it may be out's
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(a->Q), o0 = reinterpret_cast<uintptr_t>(a->out);
+  const uint64_t span = static_cast<uint64_t>(U) * e->cfg.group * a->num_queries * kHeadDim * 2;
+  if (q0 < o0 + span && o0 < q0 + span) return RKV_ERR_INVALID_ARG;
   if (!aligned(b->K, 16) || !aligned(b->V, 16) || !aligned(a->Q, 16) || !aligned(a->out, 16) ||
       !aligned(a->lse, 4) || !aligned(a->pos, 4) || !aligned(a->q_pos, 4) ||
       !aligned(a->acc_in, 4) || !aligned(a->acc_out, 4))

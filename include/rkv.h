@@ -246,7 +246,7 @@ typedef struct {
   const float* acc_in;     /* device [T] accumulated weights so far, NULL: zeros */
   float* acc_out;          /* device [T] or NULL: acc_in + sum over (g, t) of softmax(z)
                               for every row of the units; may be acc_in itself */
-  void* out;               /* device bf16 [U, G, n_q, d], not Q's memory */
+  void* out;               /* device bf16 [U, G, n_q, d], no part of Q's memory */
   float* lse;              /* device [U, G, n_q] or NULL */
 } rkv_attention;
 

@@ -671,3 +671,18 @@ def test_scratch_of_the_first_call(units, G, nq, shared):
         eng.attend(b, c.Q, c.out)
     torch.cuda.synchronize()
     assert free - torch.cuda.mem_get_info()[0] <= most + (1 << 22)
+
+
+def test_output_over_a_part_of_the_queries_is_refused():
+    c = Case([100, 33, 7], 4, 2, seed=55)
+    eng, b = c.engine(), Batch(c.K, c.V, None, c.off)
+    buf = torch.cat([c.Q, c.Q])
+    was = buf.clone()
+    for q0, o0 in ((0, 1), (1, 0), (2, 0), (0, 2)):
+        _refused(B.RKV_ERR_INVALID_ARG, lambda: eng.attend(b, buf[q0:q0 + 3], buf[o0:o0 + 3]))
+    torch.cuda.synchronize()
+    assert torch.equal(buf, was)
+    eng.attend(b, buf[:3], buf[3:], c.lse)        # side by side
+    c.out = buf[3:]
+    torch.cuda.synchronize()
+    c.check()
