@@ -128,12 +128,13 @@ __global__ void __launch_bounds__(64 + 256 * QT, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   const int item = blockIdx.x / p.maxch, chunk = blockIdx.x - item * p.maxch;
-  const int row0 = blockIdx.y * QT * kWTile;
+  const unsigned from = (blockIdx.z * gridDim.y + blockIdx.y) * (QT * kWTile);   // below 2^32
   const int64_t base = __ldg(&p.pre_off[item]);
   const int N = static_cast<int>(__ldg(&p.pre_off[item + 1]) - base);
   const int mo = p.mem ? __ldg(&p.mem_off[item]) : item;
   const int total = p.mem ? (__ldg(&p.mem_off[item + 1]) - mo) * p.R : p.R;
-  if (row0 >= total) return;
+  if (from >= static_cast<unsigned>(total)) return;
+  const int row0 = static_cast<int>(from);
   const int nrow = min(QT * kWTile, total - row0);
   // Row warps that have query rows (a tile's first always works); the others only copy Q.
   // 64 units of 16000 rows, 32 query rows: 90 us either way at full clock, but 102 with all
@@ -546,8 +547,10 @@ cudaError_t launch_attend_wide(const CUtensorMap& kmap, const CUtensorMap& vmap,
   if (max_rows <= kWTile) {
     wide_kernel<1><<<dim3(x, 1), 320, WideLayout<1>::alloc, st>>>(kmap, vmap, p);
   } else {
-    const unsigned y = (max_rows + 2 * kWTile - 1) / (2 * kWTile);
-    wide_kernel<2><<<dim3(x, y), 576, WideLayout<2>::alloc, st>>>(kmap, vmap, p);
+    // blocks of query rows along y and, beyond the 65535 that a grid holds there, z
+    const unsigned blocks = (static_cast<unsigned>(max_rows) + 2 * kWTile - 1) / (2 * kWTile);
+    const unsigned z = (blocks + 65534) / 65535, y = (blocks + z - 1) / z;
+    wide_kernel<2><<<dim3(x, y, z), 576, WideLayout<2>::alloc, st>>>(kmap, vmap, p);
   }
   return cudaGetLastError();
 }

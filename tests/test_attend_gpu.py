@@ -686,3 +686,28 @@ def test_output_over_a_part_of_the_queries_is_refused():
     c.out = buf[3:]
     torch.cuda.synchronize()
     c.check()
+
+
+def test_more_query_rows_than_one_grid_dimension_holds():
+    """65600 units of 256 query rows behind one prefix: 65600 blocks of 256 rows."""
+    U = 65600
+    c = Case([0, 5], 16, 16, seed=56, prefixes=[300], unit_prefix=[0, 0])
+    Q = torch.zeros((U, 16, 16, 128), dtype=torch.bfloat16, device=DEV)
+    out = torch.full_like(Q, float("nan"))
+    Q[0], Q[-1] = c.Q
+    eng = Engine(16, 16, U, 5, redundancy="closed")
+    eng.set_timing(True)
+    b = Batch(c.K, c.V, None, np.array([0] * U + [5]))
+    eng.attend_shared(b, Prefix(c.PK, c.PV, c.poff, [0] * U), Q, out)
+    eng.check_status()
+    assert eng.read_timing()["shared"][1] == 1
+    eng.close()
+    c.run()                                       # the two alone, for their log-sums
+    c.out = torch.stack([out[0], out[-1]])
+    c.check()
+    # queries of 0 weigh alike what they see, query t the rows up to 284 + t
+    v = c.PV.double()
+    for t in range(16):
+        mean, size = v[:285 + t].mean(0), v[:285 + t].abs().mean(0)
+        assert bool(((out[1, 0, t].double() - mean).abs() <= 2.0 ** -8 * (mean.abs() + size)).all()), t
+    assert bool((out[1:-1] == out[1, :1]).all())
