@@ -15,8 +15,9 @@
 // Bound: instruction issue and the latency of a few dependent block reductions at small
 // units, HBM beyond; hence vectors of four rows, loops that stay rolled and few registers
 // (keys in registers and unrolled loops at half the resident warps took a fifth longer).
-// 2048 units of 2176 rows, a fifth of the weights rounded to eighths, many of them 0: 27 us
-// (58 MB; 9 at HBM's rate); 64 units of 31K rows with live mask and positions: 28 us (36 MB).
+// 2048 units of 2176 rows, a fifth of the weights rounded to eighths, many of them 0: 24.6 us
+// (58 MB; 9 at HBM's rate; issue slots 60% used, 1.7 waves of CTAs); 64 units of 31K rows with
+// live mask and positions: 26.7 us (36 MB).
 #include <limits.h>
 
 #include "ptx.cuh"
@@ -182,8 +183,9 @@ __global__ void __launch_bounds__(T, 1024 / T) drop_kernel(const DropParams p, i
       kpos = min(kpos, d);
       low_count += d >> 31;
     };
-    // two vectors' loads in flight, without a branch between them (29.0 and 30.8 us one by one,
-    // 26.8 and 27.4 two, 27.0 and 28.0 four: 2048 units of 2176 rows, 64 of 31K with positions)
+    // two vectors' loads in flight, without a branch between them (replayed: 23.8 and 26.3 us one
+    // by one, 22.5 and 25.8 two, 22.0 and 25.7 four: 2048 units of 2176 rows, 64 of 31K with
+    // positions)
     for (int v0 = tid; v0 < nv; v0 += 2 * T) {
       float4 fa[2];
       uint32_t fl[2];
@@ -607,10 +609,10 @@ cudaError_t drop_configure() {
 
 // As many threads per unit as the GPU holds for all units at once (1024 per SM at 64
 // registers), at least 128, with a vector each in one CTA and two in a cluster, and at
-// most kMaxRun rows a CTA.  Measured: 2048 units of 2176 rows 26 / 33 / 51 us with 128 /
-// 256 / 512 threads, 148 units 9.4 / 7.8 / 7.4; 64 units of 32768 rows 44 / 28 / 22 us in as
-// few CTAs as hold them, 20 in four of 512 threads and 34 in eight; 8 units 21 us in two
-// CTAs of 512 threads, 15 in four, 13 in eight.
+// most kMaxRun rows a CTA.  Measured, replayed: 2048 units of 2176 rows 23 / 28 / 39 us with
+// 128 / 256 / 512 threads, 148 units 6.5 / 5.3 / 5.1; 64 units of 32768 rows, half of them live,
+// with positions, 53 / 34 / 25 us in two CTAs, as few as hold them, 24 in four of 512 threads
+// and 40 in eight; 8 such units 22 us in two CTAs of 512 threads, 16 in four, 14.5 in eight.
 cudaError_t launch_drop(const DropParams& p, int U, int nmax, int nsm, cudaStream_t st) {
   const int64_t threads = 1024ll * nsm / U, nv = (nmax + 3) / 4;
   int T = 128, cs = 1;
